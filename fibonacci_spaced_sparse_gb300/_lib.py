@@ -35,6 +35,15 @@ class SfaParams(ctypes.Structure):
     ]
 
 
+class SfaPaged(ctypes.Structure):
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int),
+        ("cu_q", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("N", ctypes.c_int),
+    ]
+
+
 class SfaError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -47,6 +56,8 @@ _VP = ctypes.c_void_p
 _FP = ctypes.POINTER(ctypes.c_float)
 _IP = ctypes.POINTER(ctypes.c_int)
 _PP = ctypes.POINTER(SfaParams)
+_CP = ctypes.POINTER(SfaPaged)
+_LL = ctypes.c_longlong
 
 _SIGS = {
     "sfa_version": ([], ctypes.c_int),
@@ -68,6 +79,15 @@ _SIGS = {
     "sfa_decode": ([_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
     "sfa_selftest_wait_timeout": ([_VP, _VP], ctypes.c_int),
     "sfa_qkv_rope": ([_PP, ctypes.c_int, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "sfa_qk_norm_rope": ([_PP, _VP, _LL, _VP, _LL, _VP, _VP, ctypes.c_float, _VP, _VP, ctypes.c_int,
+                          _VP, _VP, _VP, _VP], ctypes.c_int),
+    "sfa_qk_norm_rope_backward_workspace_size": ([_PP], ctypes.c_size_t),
+    "sfa_qk_norm_rope_backward": ([_PP, _VP, _LL, _VP, _LL, _VP, _VP, ctypes.c_float, _VP, _VP,
+                                   ctypes.c_int] + [_VP] * 7 + [ctypes.c_size_t, _VP, _VP],
+                                  ctypes.c_int),
+    "sfa_paged_append": ([_PP, _CP, _VP, _LL, _VP, _LL, _VP, _LL, _VP, _VP, ctypes.c_float, _VP, _VP,
+                          _VP, _VP], ctypes.c_int),
+    "sfa_paged_forward": ([_PP, _CP, _VP, _LL, _VP, _VP, _VP, _VP], ctypes.c_int),
     "sfa_backward_workspace_size": ([_PP], ctypes.c_size_t),
     "sfa_backward": ([_PP] + [_VP] * 13 + [ctypes.c_size_t, _VP, _VP], ctypes.c_int),
     "sfa_read_status": ([_VP, ctypes.POINTER(ctypes.c_uint), _VP], ctypes.c_int),

@@ -1,0 +1,123 @@
+// sfa_append.cu -- one step's keys and values into a paged cache, with the
+// norm and rotation of the keys (and of the step's queries) on the way
+// (sfa_paged_append in include/sfa.h).
+//
+// A copy with arithmetic, bound by memory when there are many tokens and by
+// the latency of its lookups (cu_q -> seq_lens -> block_table) in a decode
+// step.  Four lanes hold a head row (sfa_heads.cuh); a quad of lanes handles
+// two rows of one token: queries 0-1, 2-3, 4-5, 6-7, keys 0-1, values 0-1.
+#include "sfa_heads.cuh"
+#include "sfa_paged.cuh"
+
+namespace sfa {
+
+namespace {
+
+using namespace heads;
+
+constexpr int kThreads = 192;  // 48 quads: 8 tokens with queries, 24 without
+
+// kQ: the step's queries are transformed too.
+template <typename T, bool kQ>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+    constexpr int kRoles = kQ ? kHq / 2 + 2 : 2;  // quads of a token
+    constexpr int kKey = kRoles - 2, kValue = kRoles - 1;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int quad = blockIdx.x * (kThreads / 4) + (threadIdx.x >> 2), c = threadIdx.x & 3;
+    const int t = quad / kRoles, role = quad - t * kRoles;
+    const int warp_t = __shfl_sync(kFull, t, 0);
+    if (warp_t >= a.c.N) return;
+    const bool in_n = t < a.c.N;
+    const int tt = in_n ? t : a.c.N - 1;
+    // the row's loads go out before the lookups
+    const T* src;
+    if (role == kValue)
+        src = static_cast<const T*>(a.vn) + (size_t)tt * a.vs;
+    else if (role == kKey)
+        src = static_cast<const T*>(a.kn) + (size_t)tt * a.ks;
+    else
+        src = static_cast<const T*>(a.q) + (size_t)tt * a.qs + role * 2 * kD;
+    Raw<T> raw[2];
+    fetch(src, c, raw[0]);
+    fetch(src + kD, c, raw[1]);
+    // the sequence of the warp's first token, then forward to this lane's
+    int s = paged::sequence_of(a.c, warp_t);
+    if (s >= a.c.S) return;  // it lies behind the last sequence, and so do the others
+    int end = __ldg(a.c.cu + s + 1);
+    while (end <= tt && s + 1 < a.c.S) end = __ldg(a.c.cu + ++s + 1);
+    if (!in_n || tt >= end) return;
+    const int pos = __ldg(a.c.lens + s) - (end - tt);
+    const bool good = pos >= 0 && pos < a.c.cap;
+    if (!good && c == 0 && role == kKey) paged::report(a.c.status);
+    T* dst;
+    if (role >= kKey) {
+        if (!good) return;
+        const int row = paged::page_row(a.c, s, pos);
+        if (row < 0) {
+            if (c == 0 && role == kKey) paged::report(a.c.status);
+            return;
+        }
+        dst = static_cast<T*>(role == kKey ? a.c.k : a.c.v) + (size_t)row * (kHkv * kD);
+        if (role == kValue || (!a.wk && !a.rope)) {
+            put(dst, c, raw[0]);
+            put(dst + kD, c, raw[1]);
+            return;
+        }
+    } else {
+        dst = static_cast<T*>(a.qhat) + (size_t)t * (kHq * kD) + role * 2 * kD;
+    }
+    const float* wp = role == kKey ? a.wk : a.wq;
+    const unsigned quad_mask = 0xfu << (threadIdx.x & 28);
+    Row w;
+    if (wp) w = weights(wp, c);
+    Angles rot;
+    if (a.rope && good) rot = angles(a.rope, pos, c);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        Row x = open(raw[h]);
+        if (wp) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss += x.x[j] * x.x[j] + x.y[j] * x.y[j];
+            ss += __shfl_xor_sync(quad_mask, ss, 1);
+            ss += __shfl_xor_sync(quad_mask, ss, 2);
+            const float r = 1.f / sqrtf(ss * (1.f / kD) + a.eps);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x.x[j] = x.x[j] * r * w.x[j];
+                x.y[j] = x.y[j] * r * w.y[j];
+            }
+        }
+        if (a.rope && good) rotate(x, rot);
+        if (!good) x = Row{};
+        store(dst + h * kD, c, x);
+    }
+}
+
+template <typename T, bool kQ>
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
+    const int roles = kQ ? kHq / 2 + 2 : 2, tokens = kThreads / 4 / roles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.c.N + tokens - 1) / tokens));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, append_kernel<T, kQ>, a);
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const AppendArgs& a, sfa_dtype dt, cudaStream_t s) {
+    if (dt == SFA_BF16)
+        return a.q ? launch_append<__nv_bfloat16, true>(a, s) : launch_append<__nv_bfloat16, false>(a, s);
+    return a.q ? launch_append<float, true>(a, s) : launch_append<float, false>(a, s);
+}
+
+}  // namespace sfa

@@ -1,0 +1,309 @@
+// sfa_paged_fwd.cu -- attention of a step's tokens over a paged cache
+// (sfa_paged_forward in include/sfa.h): the key list of sfa_forward ("Attended
+// set", section 2 of "Depth-Staggered Fibonacci Spacing for Sparse
+// Attention": window distances 0..W and one interpolated row per rung) read
+// through each sequence's block table.
+//
+// Rows kernel (this file's general path: fp32, wide windows, few tokens): kNW
+// warps per (token, key/value head).  A warp takes four entries of the key
+// list at a time, lane = (entry slot, 8-dimension chunk): a row of keys or
+// values is eight 16-byte loads (bf16), the score of an entry for the four
+// query heads is a reduction over its eight lanes that leaves head h in lanes
+// 2h, 2h + 1 of the slot, and every slot keeps its own running maximum and sum
+// (base 2), so that slots and warps meet only at the end.
+#include "sfa_mma.cuh"
+#include "sfa_paged.cuh"
+
+namespace sfa {
+
+namespace {
+
+using namespace mma;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;      // raise a running maximum past this margin
+constexpr float kFloor = -1e30f;   // running maximum before the first entry
+
+struct PagedFwd {
+    LayerArgs a;
+    PagedArgs c;
+    const void* q;
+    long long qs;
+    void* o;
+    float* lse;
+};
+
+template <typename T>
+struct Chunk;  // 8 values of a row
+template <>
+struct Chunk<__nv_bfloat16> {
+    uint4 u;
+};
+template <>
+struct Chunk<float> {
+    float4 u, v;
+};
+__device__ __forceinline__ void load(const __nv_bfloat16* p, Chunk<__nv_bfloat16>& x) {
+    x.u = __ldg(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ void load(const float* p, Chunk<float>& x) {
+    x.u = __ldg(reinterpret_cast<const float4*>(p));
+    x.v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+}
+__device__ __forceinline__ void open(const Chunk<__nv_bfloat16>& x, float (&f)[8]) {
+    const uint32_t w[4] = {x.u.x, x.u.y, x.u.z, x.u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void open(const Chunk<float>& x, float (&f)[8]) {
+    f[0] = x.u.x, f[1] = x.u.y, f[2] = x.u.z, f[3] = x.u.w;
+    f[4] = x.v.x, f[5] = x.v.y, f[6] = x.v.z, f[7] = x.v.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// A warp's part of one query over the entries first, first + step, ... (four
+// consecutive ones at a time): each lane ends with its slots' merged sums.
+// After merge(): lane (bits 4, 3) = head, chunk lane & 7: acc[0..7] unnormalised
+// against the maximum m of that head, l the sum (the same in all eight lanes).
+struct Partial {
+    float acc[8];
+    float m, l;
+};
+
+template <typename T>
+__device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const T* qrow, int first, int step) {
+    const int lane = threadIdx.x & 31, slot = lane >> 3, ch = lane & 7;
+    float q[kG][8];
+#pragma unroll
+    for (int h = 0; h < kG; ++h) {
+        Chunk<T> x;
+        load(qrow + h * kD + 8 * ch, x);
+        open(x, q[h]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[h][j] *= P.a.scale * kLog2e;
+    }
+    const int nwin = min(P.a.W, pos) + 1;
+    int nrung = 0;
+    for (int r = 0; r < P.a.nr; ++r) nrung += P.a.r[r].c <= pos ? 1 : 0;  // sorted: a prefix
+    const int n = nwin + nrung;
+    const T* kb = static_cast<const T*>(P.c.k) + g * kD + 8 * ch;
+    const T* vb = static_cast<const T*>(P.c.v) + g * kD + 8 * ch;
+    float acc[kG][8];
+#pragma unroll
+    for (int h = 0; h < kG; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[h][j] = 0.f;
+    float m = kFloor, l = 0.f;  // of head (lane >> 1) & 3, this slot's entries
+    bool bad = false;
+    for (int e0 = first; e0 < n; e0 += step) {
+        const int e = e0 + slot;
+        int ra = -1, rb = -1;
+        float wa = 1.f, wb = 0.f;
+        if (e < nwin) {
+            ra = paged::page_row(P.c, s, pos - e);
+            bad |= ra < 0;
+        } else if (e < n) {
+            const Rung R = P.a.r[e - nwin];
+            ra = paged::page_row(P.c, s, pos - R.n);
+            bad |= ra < 0;
+            if (R.t > 0.f) {
+                rb = paged::page_row(P.c, s, pos - R.n - 1);
+                bad |= rb < 0;
+                if (rb < 0) ra = -1;  // an entry needs both of its rows
+                wa = 1.f - R.t;
+                wb = R.t;
+            }
+        }
+        float k[8], v[8];
+        {
+            Chunk<T> ka{}, va{}, kc{}, vc{};
+            if (ra >= 0) {
+                load(kb + (size_t)ra * (kHkv * kD), ka);
+                load(vb + (size_t)ra * (kHkv * kD), va);
+                if (rb >= 0) {
+                    load(kb + (size_t)rb * (kHkv * kD), kc);
+                    load(vb + (size_t)rb * (kHkv * kD), vc);
+                }
+            }
+            open(ka, k);
+            open(va, v);
+            if (rb >= 0 && ra >= 0) {
+                float x[8], y[8];
+                open(kc, x);
+                open(vc, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    k[j] = wa * k[j] + wb * x[j];
+                    v[j] = wa * v[j] + wb * y[j];
+                }
+            }
+        }
+        float d[kG];
+#pragma unroll
+        for (int h = 0; h < kG; ++h) {
+            d[h] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[h] = fmaf(q[h][j], k[j], d[h]);
+        }
+        // sum over the slot's eight lanes; head h ends in lanes 2h, 2h + 1
+        const bool up4 = lane & 4, up2 = lane & 2;
+        float d0 = (up4 ? d[2] : d[0]) + __shfl_xor_sync(kFull, up4 ? d[0] : d[2], 4);
+        float d1 = (up4 ? d[3] : d[1]) + __shfl_xor_sync(kFull, up4 ? d[1] : d[3], 4);
+        float x = (up2 ? d1 : d0) + __shfl_xor_sync(kFull, up2 ? d0 : d1, 2);
+        x += __shfl_xor_sync(kFull, x, 1);
+        if (ra < 0) x = -INFINITY;
+        if (__any_sync(kFull, x > m + kLazy)) {
+            const float up = fmaxf(m, x);
+            const float f = exp2f(m - up);
+            m = up;
+            l *= f;
+#pragma unroll
+            for (int h = 0; h < kG; ++h) {
+                const float fh = __shfl_sync(kFull, f, (lane & 24) + 2 * h);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[h][j] *= fh;
+            }
+        }
+        const float p = exp2f(x - m);
+        l += p;
+#pragma unroll
+        for (int h = 0; h < kG; ++h) {
+            const float ph = __shfl_sync(kFull, p, (lane & 24) + 2 * h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[h][j] = fmaf(ph, v[j], acc[h][j]);
+        }
+    }
+    if (__any_sync(kFull, bad) && lane == 0) paged::report(P.c.status);
+    // the four slots: one maximum per head, then half the heads change sides twice
+    float top = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+    const float f = exp2f(m - top);
+    l *= f;
+    l += __shfl_xor_sync(kFull, l, 8);
+    l += __shfl_xor_sync(kFull, l, 16);
+#pragma unroll
+    for (int h = 0; h < kG; ++h) {
+        const float fh = __shfl_sync(kFull, f, (lane & 24) + 2 * h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[h][j] *= fh;
+    }
+    const bool up16 = lane & 16, up8 = lane & 8;
+    Partial out;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a0 = (up16 ? acc[2][j] : acc[0][j]) + __shfl_xor_sync(kFull, up16 ? acc[0][j] : acc[2][j], 16);
+        const float a1 = (up16 ? acc[3][j] : acc[1][j]) + __shfl_xor_sync(kFull, up16 ? acc[1][j] : acc[3][j], 16);
+        out.acc[j] = (up8 ? a1 : a0) + __shfl_xor_sync(kFull, up8 ? a0 : a1, 8);
+    }
+    out.m = __shfl_sync(kFull, top, 2 * slot);
+    out.l = __shfl_sync(kFull, l, 2 * slot);
+    return out;
+}
+
+// Token t of sequence s: its position; false when that is out of range (its
+// outputs become zeros).
+template <typename T>
+__device__ __forceinline__ void zero_out(const PagedFwd& P, int t, int g, int i, int n) {
+    T* o = static_cast<T*>(P.o) + ((size_t)t * kHq + g * kG) * kD;
+    for (int j = i; j < kG * kD; j += n) o[j] = from_f32<T>(0.f);
+    if (P.lse && i < kG) P.lse[(size_t)t * kHq + g * kG + i] = 0.f;
+}
+
+template <typename T, int kNW>
+__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ PagedFwd P) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kUnits = 8 / kNW;  // (token, head) of a block
+    __shared__ float part[kNW > 1 ? kNW : 1][kNW > 1 ? kG * kD : 1];
+    __shared__ float top[kNW][kG], sum[kNW][kG];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned unit = blockIdx.x * kUnits + warp / kNW;
+    const int t = (int)(unit / kHkv), g = (int)(unit % kHkv);
+    if (t >= P.c.N) return;  // with kNW > 1 the whole block
+    const int s = paged::sequence_of(P.c, t);
+    if (s >= P.c.S) return;
+    const int pos = __ldg(P.c.lens + s) - (__ldg(P.c.cu + s + 1) - t);
+    if (pos < 0 || pos >= P.c.cap) {
+        if (threadIdx.x % (32 * kNW) == 0 && g == 0) paged::report(P.c.status);
+        zero_out<T>(P, t, g, threadIdx.x % (32 * kNW), 32 * kNW);
+        return;
+    }
+    const T* qrow = static_cast<const T*>(P.q) + (size_t)t * P.qs + g * kG * kD;
+    const Partial x = query_part<T>(P, s, pos, g, qrow, 4 * (warp % kNW), 4 * kNW);
+    const int h = lane >> 3, ch = lane & 7;
+    T* o = static_cast<T*>(P.o) + ((size_t)t * kHq + g * kG) * kD;
+    float* lse = P.lse ? P.lse + (size_t)t * kHq + g * kG : nullptr;
+    if (kNW == 1) {
+        const float inv = x.l > 0.f || x.l != x.l ? 1.f / x.l : 0.f;  // no entry: zeros
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = x.acc[j] * inv;
+        store8(o + h * kD + 8 * ch, f);
+        if (lse && ch == 0) lse[h] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * kLn2;
+        return;
+    }
+    if (ch == 0) {
+        top[warp][h] = x.m;
+        sum[warp][h] = x.l;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[kNW > 1 ? warp : 0][kNW > 1 ? h * kD + 8 * ch + j : 0] = x.acc[j];
+    __syncthreads();
+    {
+        const int hh = threadIdx.x >> 6;  // 256 threads: one output each
+        float m = top[0][hh];
+#pragma unroll
+        for (int w = 1; w < kNW; ++w) m = fmaxf(m, top[w][hh]);
+        float l = 0.f, v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kNW; ++w) {
+            const float f = exp2f(top[w][hh] - m);
+            l = fmaf(f, sum[w][hh], l);
+            v = fmaf(f, part[kNW > 1 ? w : 0][kNW > 1 ? threadIdx.x : 0], v);
+        }
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        o[threadIdx.x] = from_f32<T>(v * inv);
+        if (lse && (threadIdx.x & 63) == 0) lse[hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+}
+
+template <typename T, int kNW>
+cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
+    constexpr int kUnits = 8 / kNW;
+    const long long units = (long long)P.c.N * kHkv;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((units + kUnits - 1) / kUnits));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rows_kernel<T, kNW>, P);
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs, void* o,
+                             float* lse, cudaStream_t s) {
+    const PagedFwd P = {a, c, q, qs, o, lse};
+    const bool few = c.N <= 512;
+    if (dt == SFA_BF16) return few ? launch_rows<__nv_bfloat16, 8>(P, s) : launch_rows<__nv_bfloat16, 1>(P, s);
+    return few ? launch_rows<float, 8>(P, s) : launch_rows<float, 1>(P, s);
+}
+
+}  // namespace sfa

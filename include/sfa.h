@@ -349,6 +349,133 @@ SFA_API sfa_status sfa_backward(const sfa_params *p, const void *Q, const void *
                                 void *workspace, size_t workspace_bytes,
                                 unsigned int *status, cudaStream_t stream);
 
+/* ---- norms of queries and keys with the rotation ---------------------- */
+
+/* RMS norm of every query and key head followed by RoPE, in one pass: the
+ * paper's model has no such norm; it serves models that norm queries and keys
+ * before the attention (QK norm).  For each head row x of D values at
+ * position i,
+ *   y = x / sqrt(mean(x^2) + eps) * w      (w = wq for queries, wk for keys)
+ *   xhat = R(i) y                          (the rotation of sfa_qkv_rope)
+ * in fp32, rounded once to p->dtype.  sfa_forward, sfa_backward and sfa_decode
+ * with rope_theta = 0 take the results.
+ *   p: B, T, Hq, Hkv, D, dtype and rope_theta are used (rope_theta <= 0: the
+ *     norm alone); the other fields are validated as for sfa_forward;
+ *   Q [B][T][Hq][D], K [B][T][Hkv][D]: token (b, t) starts q_stride (k_stride)
+ *     elements after the token before it, so both may be parts of one packed
+ *     projection; a multiple of 16 bytes, at least Hq D (Hkv D);
+ *   wq, wk: D fp32 (device, 16-byte aligned); eps: finite, >= 0;
+ *   positions: device int32 [B][T], or NULL for the index t; a position
+ *     outside [0, table_rows) reads no table row, writes zeros to that
+ *     token's outputs and sets SFA_DEVSTAT_BAD_INDEX in *status; not read
+ *     without a rotation;
+ *   rope_table: table_rows positions (from sfa_rope_table; at least T of them
+ *     when positions is NULL);
+ *   Qhat, Khat: [B][T][Hq][D] and [B][T][Hkv][D], contiguous; status: device
+ *     word or NULL.
+ * One launch; allocates nothing.  Asynchronous on stream. */
+SFA_API sfa_status sfa_qk_norm_rope(const sfa_params *p, const void *Q, long long q_stride,
+                                    const void *K, long long k_stride, const float *wq,
+                                    const float *wk, float eps, const int *positions,
+                                    const float *rope_table, int table_rows, void *Qhat,
+                                    void *Khat, unsigned int *status, cudaStream_t stream);
+
+/* Bytes of device workspace sfa_qk_norm_rope_backward needs. */
+SFA_API size_t sfa_qk_norm_rope_backward_workspace_size(const sfa_params *p);
+
+/* Gradients of a scalar loss through sfa_qk_norm_rope, given dQhat and dKhat
+ * (contiguous, p->dtype).  Per head row, with r = 1 / sqrt(mean(x^2) + eps),
+ * n = x r and g = R(i)^T dxhat,
+ *   dw = sum over tokens and heads of g n,
+ *   dx = r (w g - n mean(w g n)).
+ *   Q, K, strides, wq, wk, eps, positions, rope_table, table_rows: as in the
+ *     forward; dQ, dK: contiguous, p->dtype, fully overwritten;
+ *   dwq, dwk: D fp32 each, overwritten (zeros when B * T = 0);
+ *   workspace: device, 256-byte aligned, contents ignored on entry and
+ *     clobbered; two calls that may overlap need one each.
+ * A token whose position lies outside the table contributes nothing and gets
+ * zero gradients.  Sums are fp32 in a fixed order, so results do not change
+ * from run to run on one GPU model.  Two launches; allocates nothing.
+ * Asynchronous on stream. */
+SFA_API sfa_status sfa_qk_norm_rope_backward(const sfa_params *p, const void *Q,
+                                             long long q_stride, const void *K,
+                                             long long k_stride, const float *wq,
+                                             const float *wk, float eps, const int *positions,
+                                             const float *rope_table, int table_rows,
+                                             const void *dQhat, const void *dKhat, void *dQ,
+                                             void *dK, float *dwq, float *dwk, void *workspace,
+                                             size_t workspace_bytes, unsigned int *status,
+                                             cudaStream_t stream);
+
+/* ---- paged key/value cache -------------------------------------------- */
+
+/* A key/value cache in pages, and one step's new tokens.  N token rows hold
+ * the new tokens of p->B sequences one after another: row t with
+ * cu_q[s] <= t < cu_q[s + 1] is a token of sequence s, at position
+ *   i = seq_lens[s] - (cu_q[s + 1] - t),
+ * so seq_lens counts a sequence's rows with the new ones, and a sequence's
+ * new tokens are its last rows.  A sequence may bring no token, one or many.
+ * Rows t >= cu_q[B] belong to no sequence: they are not read, and their
+ * outputs are left as they were.  Position i of sequence s lives in row
+ * i % page_size of page block_table[s][i / page_size]; only the entries of
+ * block_table that a call needs are read, so entries of pages that are not
+ * yet or no longer there may hold anything.  Cached keys are rotated (and
+ * normed, where the model norms them): each key is rotated once, when it is
+ * appended, and not at every read.
+ * Metadata is checked on the device: a token whose position lies outside
+ * [0, min(p->T, max_pages * page_size)), and a page number outside
+ * [0, num_pages), set SFA_DEVSTAT_BAD_INDEX in *status and touch no memory. */
+typedef struct {
+    void *k_pages, *v_pages;  /* [num_pages][page_size][Hkv][D], p->dtype */
+    int num_pages;            /* >= 1; num_pages * page_size < 2^31 */
+    int page_size;            /* rows of a page: a power of two */
+    const int *block_table;   /* device [B][max_pages] */
+    int max_pages;            /* >= 1 */
+    const int *cu_q;          /* device [B + 1], cu_q[0] = 0, not decreasing */
+    const int *seq_lens;      /* device [B] */
+    int N;                    /* token rows, 0 <= N <= 2^28 */
+} sfa_paged;
+
+/* Appends the step's keys and values to the pages, rotating the keys (and the
+ * queries) on the way:
+ *   page row of token t: K <- R(i) norm(K[t]), V <- V[t];  Qhat[t] <- R(i) norm(Q[t])
+ * with the norm and rotation of sfa_qk_norm_rope, in fp32, rounded once.
+ *   p: B (sequences), T (capacity, and rows of rope_table), Hq, Hkv, D, dtype
+ *     and rope_theta are used (rope_theta <= 0: no rotation);
+ *   K, V [N][Hkv][D], Q [N][Hq][D] with token strides as in sfa_qk_norm_rope;
+ *   Q and Qhat: both given, or both NULL (keys and values alone);
+ *   wq, wk: D fp32, or NULL for no norm of the queries (keys);
+ *   Qhat [N][Hq][D], contiguous.  A token with a bad position gets zeros there;
+ *     one with a bad page is not stored.
+ * Two tokens that go to one page row (a page in two sequences' tables) race.
+ * One launch; allocates nothing.  Asynchronous on stream. */
+SFA_API sfa_status sfa_paged_append(const sfa_params *p, const sfa_paged *c, const void *Q,
+                                    long long q_stride, const void *K, long long k_stride,
+                                    const void *V, long long v_stride, const float *wq,
+                                    const float *wk, float eps, const float *rope_table,
+                                    void *Qhat, unsigned int *status, cudaStream_t stream);
+
+/* The attention of the step's tokens over their sequences' pages: row t is
+ * what sfa_forward computes for query i of a contiguous sequence ("Attended
+ * set", section 2), reading rows 0..i of the sequence.  Chunks of many tokens
+ * and single tokens may stand in one call.
+ *   p: B (sequences), T (capacity; the rung plan is made for a sequence of
+ *     this length), W, K, rungs, alpha, scale, dtype and round_offsets are
+ *     used; rope_theta must be <= 0: Q is already rotated, as sfa_paged_append
+ *     leaves it;
+ *   Q [N][Hq][D] with a token stride as above; O [N][Hq][D] and lse [N][Hq]
+ *     (or NULL), contiguous.
+ * A token with a bad position gets zeros in O and lse.  An entry of a token's
+ * key list with a row in a bad page is left out of its softmax; a token with
+ * no entry left gets zeros in O and minus infinity in lse.  Rows outside a
+ * token's key list never reach its output, whatever they hold.
+ * One launch (bf16 with many tokens and W <= 28: tensor cores, fp32
+ * accumulation, probabilities rounded to bf16 for the value product; else
+ * fp32 arithmetic); allocates nothing.  Asynchronous on stream. */
+SFA_API sfa_status sfa_paged_forward(const sfa_params *p, const sfa_paged *c, const void *Q,
+                                     long long q_stride, void *O, float *lse,
+                                     unsigned int *status, cudaStream_t stream);
+
 /* ---- device status ----------------------------------------------------- */
 
 /* Synchronises stream, copies the device status word to *host_word (may be
