@@ -309,158 +309,354 @@ cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
 // sequence and one key/value head, as two pairs of 2 queries x 4 heads, and
 // forms both products with mma.sync m16n8k16, keys on M:
 //   S^T (16 key rows x 8 columns) = K_rows . Q^T,   O^T += V_rows^T . P^T.
-// Window: rows i - W .. i + 3 of the quad are one M tile (two from W = 13 on)
-// shared by both pairs.  Rungs: one M tile a pair holds four rungs, row r < 8
-// the far row i + e - n - 1 and row r + 8 the near row i + e - n of rung r % 4
-// for query e = r / 4 of the pair, so both rows of an interpolation sit in one
-// thread: it mixes their scores, and splits the probability onto them.
+// Window: rows i - W .. i + 3 of the quad's first position i are one tile that
+// both pairs share, two from W = 13 on.  Rungs: one tile a pair holds four
+// rungs, row r < 8 the far row i + e - n - 1 and row r + 8 the near row
+// i + e - n of rung r % 4 for query e = r / 4 of the pair, so both rows of an
+// interpolation sit in one thread: it mixes their scores (the interpolated
+// key's score, by linearity), and splits the probability onto the rows.
+// (Tiles of five rows a rung that both pairs share load a third less, but the
+// two rows then sit in different threads and every thread computes four
+// exponentials for three rungs instead of two for four: 1870 instructions a
+// quad instead of 1520, 63 against 56 us for 32 x 1024 tokens.)
 //
 // Rows come through the block table, so no block of rows is contiguous and no
 // tiled copy fits; the fragments are loaded straight into registers instead,
 // with no shared memory, no transpose and no barrier.  The dimensions of the
-// two products are taken in an order that makes every load 16 bytes:
-//   scores: k-step s of thread (row g, lane t) takes words s of the row's
-//     16-byte chunks t and 4 + t, for keys and queries alike;
-//   values: output row m of tile j is dimension 8 (m % 8) + 2 j + m / 8, so
-//     thread (g, t) needs chunk g of its four rows 2t, 2t + 1, 2t + 8, 2t + 9,
-//     and ends with dimensions 8g .. 8g + 7 of its columns: one 16-byte store.
+// two products are taken in an order that keeps the loads wide:
+//   scores: k-step s of thread (row g, lane t) takes words s and 4 + s of
+//     bytes 32 t .. 32 t + 31 of the row, for keys and queries alike;
+//   values: the same loads, turned by movmatrix: words 2j and 2j + 1 make
+//     product j, whose output rows g and g + 8 are dimensions
+//     16 (g / 2) + 4 j + g % 2 and that + 2.
+// (Loading a row's chunk g for each of the four rows 2t, 2t + 1, 2t + 8,
+// 2t + 9 of the value fragment saves the turn, but eight neighbouring lanes
+// then hit two banks: 12 wavefronts a load instead of 4.)
 // Neighbouring queries read neighbouring rows, so a row comes from L2 once a
 // block and from L1 after that.
 //
-// Entries that are masked get probability 0, and rows that no query of the
-// quad may read are not loaded (zeros), but a row that one query reads is
-// multiplied with the others' zeros: infinity or NaN in it would reach them.
-// The epilogue looks for values that are not finite and redoes those queries
-// one at a time with the rows of that query alone.  Nothing of a column's
-// arithmetic depends on another column, so the second pass gives what the
-// first would have given without the others' rows, bit for bit.
+// Masked entries get probability 0.  A row that some queries of the quad read
+// is multiplied with the others' zeros, and a tile row that none reads is
+// filled with the first query's own row; infinity or NaN there would reach
+// queries that do not read it.  The epilogue looks for values that are not
+// finite and redoes those queries one at a time (kAlone), with that query's
+// rows and zeros.  Nothing of a column's arithmetic depends on another column,
+// so this gives what the first pass would have given without the others' rows,
+// bit for bit.
 
 constexpr int kQuadWarps = 4;
 
 struct Tile {
-    uint4 k[4];      // rows g, g + 8: chunks t, 4 + t of each
-    uint4 v[4];      // rows 2t, 2t + 1, 2t + 8, 2t + 9: chunk g
-    bool lo, hi;     // rows g and g + 8 are there
+    uint32_t k[2][8], v[2][8];  // rows g, g + 8: bytes 32 t .. 32 t + 31
 };
 
-// One query pair: the B fragments of Q^T, O^T, and the running maximum (log2
-// units) and sum of this thread's two columns (query tig / 2 of the pair,
-// heads 2 (tig & 1) and that + 1); the sums are this thread's rows' alone.
+// One query pair: the B fragments of Q^T, O^T, and of this thread's two
+// columns (query tig / 2 of the pair, heads 2 (tig & 1) and that + 1) minus
+// the running maximum (log2 units), the score that raises it, and the sum over
+// this thread's rows.
 struct Pair {
     uint32_t qf[4][2];
     float o[4][4];
-    float m[2], l[2];
+    float2 nm, th, l;
 };
+
+__device__ __forceinline__ float2 f2(float x, float y) { return make_float2(x, y); }
 
 __device__ __forceinline__ uint32_t word(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 
-// The tile whose 16 row numbers lanes base .. base + 15 hold in `row`.
-__device__ __forceinline__ void load_tile(const uint4* __restrict__ k, const uint4* __restrict__ v, int row, int base,
+__device__ __forceinline__ void load32(const char* p, uint32_t (&w)[8]) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(p));
+}
+
+// The tile whose 16 row numbers lanes base .. base + 15 hold in `row`; in a
+// kAlone pass rows that are not there (-1) are zeros.
+template <bool kAlone>
+__device__ __forceinline__ void load_tile(const char* __restrict__ k, const char* __restrict__ v, int row, int base,
                                           Tile& x) {
+    constexpr int kStride = kHkv * kD * 2;  // bytes of a page row
     const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const int ra = __shfl_sync(kFull, row, base + g8), rb = __shfl_sync(kFull, row, base + 8 + g8);
-    x.lo = ra >= 0;
-    x.hi = rb >= 0;
-    const uint4* pa = k + (size_t)ra * (kHkv * kD / 8) + tig;
-    const uint4* pb = k + (size_t)rb * (kHkv * kD / 8) + tig;
-    x.k[0] = x.lo ? __ldg(pa) : zero;
-    x.k[1] = x.lo ? __ldg(pa + 4) : zero;
-    x.k[2] = x.hi ? __ldg(pb) : zero;
-    x.k[3] = x.hi ? __ldg(pb + 4) : zero;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int r = __shfl_sync(kFull, row, base + 2 * tig + (j & 1) + 8 * (j >> 1));
-        x.v[j] = r >= 0 ? __ldg(v + (size_t)r * (kHkv * kD / 8) + g8) : zero;
+    for (int h = 0; h < 2; ++h) {
+        const int r = __shfl_sync(kFull, row, base + 8 * h + g8);
+        if (kAlone) {
+#pragma unroll
+            for (int w = 0; w < 8; ++w) x.k[h][w] = x.v[h][w] = 0u;
+            if (r < 0) continue;
+        }
+        const size_t at = (size_t)(unsigned)r * kStride + 32 * tig;
+        load32(k + at, x.k[h]);
+        load32(v + at, x.v[h]);
     }
 }
 
 // S^T of a tile and a pair: c[0], c[1] row g, c[2], c[3] row g + 8.
 __device__ __forceinline__ void scores(const Tile& x, const Pair& U, float (&c)[4]) {
-    mma16816_z(c, x.k[0].x, x.k[2].x, x.k[1].x, x.k[3].x, U.qf[0][0], U.qf[0][1]);
-    mma16816(c, x.k[0].y, x.k[2].y, x.k[1].y, x.k[3].y, U.qf[1][0], U.qf[1][1]);
-    mma16816(c, x.k[0].z, x.k[2].z, x.k[1].z, x.k[3].z, U.qf[2][0], U.qf[2][1]);
-    mma16816(c, x.k[0].w, x.k[2].w, x.k[1].w, x.k[3].w, U.qf[3][0], U.qf[3][1]);
-}
-
-// O^T += V_rows^T . P^T
-__device__ __forceinline__ void values(const Tile& x, Pair& U, uint32_t b0, uint32_t b1) {
+    mma16816_z(c, x.k[0][0], x.k[1][0], x.k[0][4], x.k[1][4], U.qf[0][0], U.qf[0][1]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t v0 = word(x.v[0], j), v1 = word(x.v[1], j), v2 = word(x.v[2], j), v3 = word(x.v[3], j);
-        mma16816(U.o[j], __byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x5410),
-                 __byte_perm(v2, v3, 0x7632), b0, b1);
-    }
+    for (int s = 1; s < 4; ++s)
+        mma16816(c, x.k[0][s], x.k[1][s], x.k[0][4 + s], x.k[1][4 + s], U.qf[s][0], U.qf[s][1]);
 }
 
-// Raise the running maximum of each column whose largest of x0 (x1) over the
-// eight threads that hold it passes the margin, and rescale it.
-__device__ __forceinline__ void raise(Pair& U, float x0, float x1) {
+// The A fragments of V_rows^T, product j: words 2j and 2j + 1 of the rows, each
+// an 8 x 8 matrix turned in registers.
+__device__ __forceinline__ void value_frag(const Tile& x, int j, uint32_t (&a)[4]) {
+    a[0] = movm_t(x.v[0][2 * j]);
+    a[1] = movm_t(x.v[0][2 * j + 1]);
+    a[2] = movm_t(x.v[1][2 * j]);
+    a[3] = movm_t(x.v[1][2 * j + 1]);
+}
+
+// Largest of a column over the eight threads that hold it.
+__device__ __forceinline__ float2 column_max(float2 x) {
 #pragma unroll
     for (int w = 4; w <= 16; w <<= 1) {
-        x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, w));
-        x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, w));
+        x.x = fmaxf(x.x, __shfl_xor_sync(kFull, x.x, w));
+        x.y = fmaxf(x.y, __shfl_xor_sync(kFull, x.y, w));
     }
-    const float n0 = x0 > U.m[0] + kLazy ? x0 : U.m[0], n1 = x1 > U.m[1] + kLazy ? x1 : U.m[1];
-    const float f0 = fast_exp2(U.m[0] - n0), f1 = fast_exp2(U.m[1] - n1);
-    U.m[0] = n0;
-    U.m[1] = n1;
-    U.l[0] *= f0;
-    U.l[1] *= f1;
+    return x;
+}
+
+// Raise the running maximum of each column whose largest x passes the margin,
+// and rescale it.
+__device__ __forceinline__ void raise(Pair& U, float2 x) {
+    x = column_max(x);
+    const float n0 = x.x > U.th.x ? -x.x : U.nm.x, n1 = x.y > U.th.y ? -x.y : U.nm.y;
+    const float2 f = f2(fast_exp2(n0 - U.nm.x), fast_exp2(n1 - U.nm.y));
+    U.nm = f2(n0, n1);
+    U.th = f2(kLazy - n0, kLazy - n1);
+    U.l = __fmul2_rn(U.l, f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        U.o[j][0] *= f0;
-        U.o[j][1] *= f1;
-        U.o[j][2] *= f0;
-        U.o[j][3] *= f1;
+        const float2 a = __fmul2_rn(f2(U.o[j][0], U.o[j][1]), f), b = __fmul2_rn(f2(U.o[j][2], U.o[j][3]), f);
+        U.o[j][0] = a.x;
+        U.o[j][1] = a.y;
+        U.o[j][2] = b.x;
+        U.o[j][3] = b.y;
     }
 }
 
-// Window tile: R is the tile's first row counted from i - W of the quad's
-// first query; pair k holds queries 2k, 2k + 1.
-__device__ __forceinline__ void window_tile(const Tile& x, int k, int R, int W, float sl2, Pair& U) {
-    const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
-    float c[4];
-    scores(x, U, c);
-    const int qq = 2 * k + (tig >> 1);
-    const bool lo = x.lo && R + g8 >= qq && R + g8 <= W + qq;
-    const bool hi = x.hi && R + g8 + 8 >= qq && R + g8 + 8 <= W + qq;
-    c[0] = lo ? c[0] * sl2 : -INFINITY;
-    c[1] = lo ? c[1] * sl2 : -INFINITY;
-    c[2] = hi ? c[2] * sl2 : -INFINITY;
-    c[3] = hi ? c[3] * sl2 : -INFINITY;
-    const float x0 = fmaxf(c[0], c[2]), x1 = fmaxf(c[1], c[3]);
-    if (__any_sync(kFull, x0 > U.m[0] + kLazy || x1 > U.m[1] + kLazy)) raise(U, x0, x1);
-    c[0] = fast_exp2(c[0] - U.m[0]);
-    c[1] = fast_exp2(c[1] - U.m[1]);
-    c[2] = fast_exp2(c[2] - U.m[0]);
-    c[3] = fast_exp2(c[3] - U.m[1]);
-    U.l[0] += c[0] + c[2];
-    U.l[1] += c[1] + c[3];
-    values(x, U, movm_t(pack_bf16(c[0], c[1])), movm_t(pack_bf16(c[2], c[3])));
+// Window tile.  mask: bit 2k (2k + 1) says that row g (g + 8) is in the window
+// of this thread's query of pair k.  kFirst: nothing is accumulated yet.
+template <bool kFirst>
+__device__ __forceinline__ void window_tile(const Tile& x, unsigned mask, float sl2, Pair (&U)[2]) {
+    uint32_t b[2][2];
+    const float2 sl = f2(sl2, sl2);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float c[4];
+        scores(x, U[k], c);
+        float2 lo = __fmul2_rn(f2(c[0], c[1]), sl), hi = __fmul2_rn(f2(c[2], c[3]), sl);
+        if (!(mask >> (2 * k) & 1u)) lo = f2(-INFINITY, -INFINITY);
+        if (!(mask >> (2 * k + 1) & 1u)) hi = f2(-INFINITY, -INFINITY);
+        const float2 top = f2(fmaxf(lo.x, hi.x), fmaxf(lo.y, hi.y));
+        if (kFirst) {
+            const float2 m = column_max(top);
+            U[k].nm = f2(-fmaxf(m.x, kFloor), -fmaxf(m.y, kFloor));
+            U[k].th = f2(kLazy - U[k].nm.x, kLazy - U[k].nm.y);
+        } else if (__any_sync(kFull, top.x > U[k].th.x || top.y > U[k].th.y)) {
+            raise(U[k], top);
+        }
+        lo = __fadd2_rn(lo, U[k].nm);
+        hi = __fadd2_rn(hi, U[k].nm);
+        lo = f2(fast_exp2(lo.x), fast_exp2(lo.y));
+        hi = f2(fast_exp2(hi.x), fast_exp2(hi.y));
+        U[k].l = kFirst ? __fadd2_rn(lo, hi) : __fadd2_rn(U[k].l, __fadd2_rn(lo, hi));
+        b[k][0] = movm_t(pack_bf16(lo.x, lo.y));
+        b[k][1] = movm_t(pack_bf16(hi.x, hi.y));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t a[4];
+        value_frag(x, j, a);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (kFirst)
+                mma16816_z(U[k].o[j], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
+            else
+                mma16816(U[k].o[j], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
+        }
+    }
 }
 
-// Rung tile of one pair; t: the fraction of this thread's rung (row g % 4).
-__device__ __forceinline__ void rung_tile(const Tile& x, float t, float sl2, Pair& U) {
-    const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
+// Rung tile of one pair.  ok: this thread's rung is an entry of its query;
+// t: the rung's fraction.
+__device__ __forceinline__ void rung_tile(const Tile& x, bool ok, float t, float sl2, Pair& U) {
     float c[4];
     scores(x, U, c);
-    const bool ok = (g8 >> 2) == (tig >> 1) && x.hi && (x.lo || t == 0.f);
     const float u = 1.f - t;
-    const float x0 = ok ? (u * c[2] + t * c[0]) * sl2 : -INFINITY;
-    const float x1 = ok ? (u * c[3] + t * c[1]) * sl2 : -INFINITY;
-    if (__any_sync(kFull, x0 > U.m[0] + kLazy || x1 > U.m[1] + kLazy)) raise(U, x0, x1);
-    const float p0 = fast_exp2(x0 - U.m[0]), p1 = fast_exp2(x1 - U.m[1]);
-    U.l[0] += p0;
-    U.l[1] += p1;
-    values(x, U, movm_t(pack_bf16(p0 * t, p1 * t)), movm_t(pack_bf16(p0 * u, p1 * u)));
+    const float2 tt = f2(t, t), uu = f2(u, u);
+    float2 s = __ffma2_rn(f2(t * sl2, t * sl2), f2(c[0], c[1]), __fmul2_rn(f2(u * sl2, u * sl2), f2(c[2], c[3])));
+    if (!ok) s = f2(-INFINITY, -INFINITY);
+    if (__any_sync(kFull, s.x > U.th.x || s.y > U.th.y)) raise(U, s);
+    s = __fadd2_rn(s, U.nm);
+    const float2 p = f2(fast_exp2(s.x), fast_exp2(s.y));
+    U.l = __fadd2_rn(U.l, p);
+    const float2 far_p = __fmul2_rn(p, tt), near_p = __fmul2_rn(p, uu);
+    const uint32_t b0 = movm_t(pack_bf16(far_p.x, far_p.y)), b1 = movm_t(pack_bf16(near_p.x, near_p.y));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t a[4];
+        value_frag(x, j, a);
+        mma16816(U.o[j], a[0], a[1], a[2], a[3], b0, b1);
+    }
+}
+
+struct Quad {
+    int s, t0, cnt, i0, last, g;
+    const int *rn, *rc;
+    const float* rt;
+};
+
+// All queries of the quad, or the query `only` alone; returns the queries
+// whose results are not finite (they are not written).
+template <bool kAlone>
+__device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, int only) {
+    const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
+    const int W = P.a.W, i0 = Q.i0, last = Q.last;
+    const float sl2 = P.a.scale * kLog2e;
+    const char* kb = static_cast<const char*>(P.c.k) + Q.g * (kD * 2);
+    const char* vb = static_cast<const char*>(P.c.v) + Q.g * (kD * 2);
+    // this lane's row of the window: position i0 - W + lane
+    bool want = lane < W + 4 && i0 - W + lane >= 0 && i0 - W + lane <= last && (!kAlone || (lane >= only && lane <= only + W));
+    int wrow = want ? paged::page_row(P.c, Q.s, i0 - W + lane) : -1;
+    bool bad = want && wrow < 0;
+    const int fill = kAlone ? -1 : max(__shfl_sync(kFull, wrow, W), 0);  // the first query's own row
+    // rungs that the last query uses: a prefix, four to a tile
+    const int nt = (__popc(__ballot_sync(kFull, Q.rc[lane] <= last)) + 3) >> 2;
+    // this lane's row of a rung tile: lanes 0-15 the first pair's, 16-31 the second's
+    const int my_q = 2 * (lane >> 4) + ((lane >> 2) & 1);
+    const bool near_row = lane & 8;
+    unsigned there = 0;  // rows of the tile that are there, where pages are bad
+    auto rung_rows = [&](int t) {
+        const int r = 4 * t + (lane & 3), i = i0 + my_q;
+        const bool w = i <= last && i >= Q.rc[r] && (near_row || Q.rt[r] > 0.f) && (!kAlone || my_q == only);
+        const int row = w ? paged::page_row(P.c, Q.s, i - Q.rn[r] - (near_row ? 0 : 1)) : -1;
+        bad |= w && row < 0;
+        return row;
+    };
+    Pair U[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int qt = Q.t0 + min(2 * k + (g8 >> 2), Q.cnt - 1);
+        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.q) + (size_t)qt * P.qs +
+                                                         (Q.g * kG + (g8 & 3)) * kD) + 2 * tig;
+        const uint4 a = __ldg(qp), b = __ldg(qp + 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            U[k].qf[j][0] = word(a, j);
+            U[k].qf[j][1] = word(b, j);
+        }
+    }
+    // window rows of this thread's queries
+    unsigned mask[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int R = 16 * (e >> 2) + 8 * (e & 1) + g8, d = R - 2 * ((e >> 1) & 1) - (tig >> 1);
+        if (d >= 0 && d <= W && R >= W - i0) mask[e >> 2] |= 1u << (e & 3);
+    }
+    if (__any_sync(kFull, bad)) {
+        const unsigned w = __ballot_sync(kFull, wrow >= 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (!(w >> (16 * (e >> 2) + 8 * (e & 1) + g8) & 1u)) mask[e >> 2] &= ~(1u << (e & 3));
+    }
+    // two tiles in turn: one is loaded while the other is used
+    Tile A, B;
+    load_tile<kAlone>(kb, vb, wrow >= 0 ? wrow : fill, 0, A);
+    int row = nt > 0 ? rung_rows(0) : -1;
+    if (W > 12) {
+        load_tile<kAlone>(kb, vb, wrow >= 0 ? wrow : fill, 16, B);
+        window_tile<true>(A, mask[0], sl2, U);
+        if (nt > 0) load_tile<kAlone>(kb, vb, row >= 0 ? row : fill, 0, A);
+        window_tile<false>(B, mask[1], sl2, U);
+    } else {
+        if (nt > 0) load_tile<kAlone>(kb, vb, row >= 0 ? row : fill, 0, B);
+        window_tile<true>(A, mask[0], sl2, U);
+        A = B;
+    }
+    const int my_i = (g8 >> 2) == (tig >> 1) ? i0 + (tig >> 1) : -(1 << 30);  // its own rung's query, or none
+    for (int t = 0; t < nt; ++t) {
+        load_tile<kAlone>(kb, vb, row >= 0 ? row : fill, 16, B);
+        const bool holes = __any_sync(kFull, bad);
+        if (holes) there = __ballot_sync(kFull, row >= 0);
+        const float frac = Q.rt[4 * t + (g8 & 3)];
+        const int c = Q.rc[4 * t + (g8 & 3)];
+        bool ok[2] = {my_i >= c, my_i + 2 >= c};
+        if (holes) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                ok[k] = ok[k] && (there >> (16 * k + 8 + g8) & 1u) && ((there >> (16 * k + g8) & 1u) || frac == 0.f);
+        }
+        row = t + 1 < nt ? rung_rows(t + 1) : -1;
+        rung_tile(A, ok[0], frac, sl2, U[0]);
+        if (t + 1 < nt) load_tile<kAlone>(kb, vb, row >= 0 ? row : fill, 0, A);
+        rung_tile(B, ok[1], frac, sl2, U[1]);
+    }
+    if (__any_sync(kFull, bad) && lane == 0) paged::report(P.c.status);
+    unsigned redo = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float2 l = U[k].l;
+#pragma unroll
+        for (int w = 4; w <= 16; w <<= 1)
+            l = __fadd2_rn(l, f2(__shfl_xor_sync(kFull, l.x, w), __shfl_xor_sync(kFull, l.y, w)));
+        const int qq = 2 * k + (tig >> 1);
+        const bool in = i0 + qq >= 0 && i0 + qq < P.c.cap;
+        if (!kAlone) {
+            float2 odd = f2(0.f, 0.f);  // stays 0 while every value is finite
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                odd = __ffma2_rn(f2(U[k].o[j][0], U[k].o[j][1]), f2(0.f, 0.f), odd);
+                odd = __ffma2_rn(f2(U[k].o[j][2], U[k].o[j][3]), f2(0.f, 0.f), odd);
+            }
+            // lanes with tig < 2 hold the pair's first query
+            const unsigned who = __ballot_sync(kFull, odd.x + odd.y != 0.f && qq < Q.cnt && in);
+            redo |= ((who & 0x33333333u ? 1u : 0u) | (who & 0xccccccccu ? 2u : 0u)) << (2 * k);
+        }
+        const bool stores = qq < Q.cnt && (kAlone ? qq == only : !(redo >> qq & 1u));
+        const unsigned who_stores = __ballot_sync(kFull, stores);
+        if (!stores) continue;
+        // l >= 2^-8 (the entry at the maximum, at most the margin below it), or 0 with no entry: zeros
+        const float2 f = f2(in && l.x != 0.f ? fast_rcp(l.x) : 0.f, in && l.y != 0.f ? fast_rcp(l.y) : 0.f);
+        const size_t at = (size_t)(Q.t0 + qq) * kHq + Q.g * kG + 2 * (tig & 1);
+        // dimensions 16 (g8 / 2) + g8 % 2 + 2 d, d = 0 .. 7, of both columns; lane ^ 4 has
+        // the others: the even one of the two takes the first eight, the odd one the last
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 a = __fmul2_rn(f2(U[k].o[j][0], U[k].o[j][1]), f), b = __fmul2_rn(f2(U[k].o[j][2], U[k].o[j][3]), f);
+            w[2 * j] = pack_bf16(a.x, a.y);
+            w[2 * j + 1] = pack_bf16(b.x, b.y);
+        }
+        const bool odd_row = g8 & 1;
+        uint32_t w0[4], w1[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t mine = odd_row ? w[4 + d] : w[d];
+            const uint32_t got = __shfl_xor_sync(who_stores, odd_row ? w[d] : w[4 + d], 4);
+            const uint32_t even = odd_row ? got : mine, odd = odd_row ? mine : got;
+            w0[d] = __byte_perm(even, odd, 0x5410);
+            w1[d] = __byte_perm(even, odd, 0x7632);
+        }
+        uint4* o = static_cast<uint4*>(P.o) + at * (kD / 8) + g8;
+        o[0] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+        o[kD / 8] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        if (P.lse && g8 == 0) {
+            const float y0 = l.x != 0.f ? (__log2f(l.x) - U[k].nm.x) * kLn2 : -INFINITY;
+            const float y1 = l.y != 0.f ? (__log2f(l.y) - U[k].nm.y) * kLn2 : -INFINITY;
+            *reinterpret_cast<float2*>(P.lse + at) = in ? f2(y0, y1) : f2(0.f, 0.f);
+        }
+    }
+    return redo;
 }
 
 __global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_constant__ PagedFwd P) {
     __shared__ int rn[SFA_MAX_RUNGS], rc[SFA_MAX_RUNGS];
     __shared__ float rt[SFA_MAX_RUNGS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, tig = lane & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x < SFA_MAX_RUNGS) {
         const Rung r = P.a.r[threadIdx.x];
         rn[threadIdx.x] = r.n;
@@ -471,129 +667,22 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // slots of four queries: sequence s starts at slot cu[s] / 4 + s, which
     // leaves room for ceil(tokens / 4) before the next one's
-    const int g = blockIdx.x % kHkv, slot = (int)(blockIdx.x / kHkv) * kQuadWarps + warp;
-    const int s = paged::last_at_most(P.c.S, slot, [&](int i) { return (__ldg(P.c.cu + i) >> 2) + i; });
-    const int start = __ldg(P.c.cu + s), end = __ldg(P.c.cu + s + 1);
-    const int t0 = start + 4 * (slot - (start >> 2) - s);
-    if (t0 < 0 || t0 >= P.c.N || t0 >= end) return;
-    const int cnt = min(4, min(end, P.c.N) - t0);
-    const int i0 = __ldg(P.c.lens + s) - (end - t0);     // position of the first query
-    const int last = min(i0 + cnt, P.c.cap) - 1;         // no row behind it is read
-    const float sl2 = P.a.scale * kLog2e;
-    const int W = P.a.W;
-    const uint4* kb = static_cast<const uint4*>(P.c.k) + g * (kD / 8);
-    const uint4* vb = static_cast<const uint4*>(P.c.v) + g * (kD / 8);
-    bool bad = false;
-    auto look_up = [&](int pos, bool want) {
-        if (!want) return -1;
-        const int row = paged::page_row(P.c, s, pos);
-        bad |= row < 0;
-        return row;
-    };
-    // rungs that the last query uses: a prefix, four to a tile
-    const int used = __popc(__ballot_sync(kFull, rc[lane] <= last));
-    const int nt = (used + 3) >> 2;
-    if (__any_sync(kFull, lane < cnt && (i0 + lane < 0 || i0 + lane >= P.c.cap)) && lane == 0) paged::report(P.c.status);
-    unsigned redo = 0;       // queries to do alone
-    for (int only = -1;;) {  // the query that is done alone, -1: all
-        // this lane's row of the window: position i0 - W + lane
-        const int wpos = i0 - W + lane;
-        const int wrow = look_up(wpos, wpos >= 0 && wpos <= last && (only < 0 || (lane >= only && lane <= only + W)));
-        // this lane's row of rung tile t: lanes 0-15 the first pair's, 16-31 the second's
-        const int my_q = 2 * (lane >> 4) + ((lane >> 2) & 1);
-        auto rung_row = [&](int t) {
-            const int r = 4 * t + (lane & 3), i = i0 + my_q;
-            const bool near_row = lane & 8;
-            return look_up(i - rn[r] - (near_row ? 0 : 1), i <= last && i >= rc[r] && (near_row || rt[r] > 0.f) &&
-                                                               (only < 0 || my_q == only));
-        };
-        Pair U[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int qt = t0 + min(2 * k + (g8 >> 2), cnt - 1);
-            const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.q) +
-                                                             (size_t)qt * P.qs + (g * kG + (g8 & 3)) * kD) + tig;
-            const uint4 a = __ldg(qp), b = __ldg(qp + 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                U[k].qf[j][0] = word(a, j);
-                U[k].qf[j][1] = word(b, j);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) U[k].o[j][e] = 0.f;
-            }
-            U[k].m[0] = U[k].m[1] = kFloor;
-            U[k].l[0] = U[k].l[1] = 0.f;
-        }
-        // two tiles in turn: one is loaded while the other is used
-        Tile A, B;
-        load_tile(kb, vb, wrow, 0, A);
-        int row = nt > 0 ? rung_row(0) : -1;
-        if (W > 12) {
-            load_tile(kb, vb, wrow, 16, B);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) window_tile(A, k, 0, W, sl2, U[k]);
-            load_tile(kb, vb, row, 0, A);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) window_tile(B, k, 16, W, sl2, U[k]);
-        } else {
-            load_tile(kb, vb, row, 0, B);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) window_tile(A, k, 0, W, sl2, U[k]);
-            A = B;
-        }
-        for (int t = 0; t < nt; ++t) {
-            load_tile(kb, vb, row, 16, B);
-            const int next = t + 1 < nt ? rung_row(t + 1) : -1;
-            const float frac = rt[4 * t + (g8 & 3)];
-            rung_tile(A, frac, sl2, U[0]);
-            if (t + 1 < nt) load_tile(kb, vb, next, 0, A);
-            rung_tile(B, frac, sl2, U[1]);
-            row = next;
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-            for (int w = 4; w <= 16; w <<= 1) {
-                U[k].l[0] += __shfl_xor_sync(kFull, U[k].l[0], w);
-                U[k].l[1] += __shfl_xor_sync(kFull, U[k].l[1], w);
-            }
-            const int qq = 2 * k + (tig >> 1), pos = i0 + qq;
-            const bool in = pos >= 0 && pos < P.c.cap;
-            float odd = 0.f;  // stays 0 while every value is finite
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) odd = fmaf(U[k].o[j][e], 0.f, odd);
-            if (only < 0) {
-                // lanes with tig < 2 hold the pair's first query
-                const unsigned who = __ballot_sync(kFull, odd != 0.f && qq < cnt && in);
-                redo |= ((who & 0x33333333u ? 1u : 0u) | (who & 0xccccccccu ? 2u : 0u)) << (2 * k);
-            }
-            if (qq >= cnt || (only < 0 ? (redo >> qq) & 1u : qq != only)) continue;
-            const float f0 = in && U[k].l[0] != 0.f ? 1.f / U[k].l[0] : 0.f;  // no entry: zeros
-            const float f1 = in && U[k].l[1] != 0.f ? 1.f / U[k].l[1] : 0.f;
-            const size_t at = (size_t)(t0 + qq) * kHq + g * kG + 2 * (tig & 1);
-            uint32_t w0[4], w1[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w0[j] = pack_bf16(U[k].o[j][0] * f0, U[k].o[j][2] * f0);
-                w1[j] = pack_bf16(U[k].o[j][1] * f1, U[k].o[j][3] * f1);
-            }
-            uint4* o = static_cast<uint4*>(P.o) + at * (kD / 8) + g8;
-            o[0] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-            o[kD / 8] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-            if (P.lse && g8 == 0) {
-                const float y0 = U[k].l[0] != 0.f ? (U[k].m[0] + __log2f(U[k].l[0])) * kLn2 : -INFINITY;
-                const float y1 = U[k].l[1] != 0.f ? (U[k].m[1] + __log2f(U[k].l[1])) * kLn2 : -INFINITY;
-                P.lse[at] = in ? y0 : 0.f;
-                P.lse[at + 1] = in ? y1 : 0.f;
-            }
-        }
-        if (redo == 0) break;
-        only = __ffs(redo) - 1;
-        redo &= redo - 1;
-    }
-    if (__any_sync(kFull, bad) && lane == 0) paged::report(P.c.status);
+    const int slot = (int)(blockIdx.x / kHkv) * kQuadWarps + warp;
+    Quad Q;
+    Q.g = blockIdx.x % kHkv;
+    Q.s = paged::last_at_most(P.c.S, slot, [&](int i) { return (__ldg(P.c.cu + i) >> 2) + i; });
+    const int start = __ldg(P.c.cu + Q.s), end = __ldg(P.c.cu + Q.s + 1);
+    Q.t0 = start + 4 * (slot - (start >> 2) - Q.s);
+    if (Q.t0 < 0 || Q.t0 >= P.c.N || Q.t0 >= end) return;
+    Q.cnt = min(4, min(end, P.c.N) - Q.t0);
+    Q.i0 = __ldg(P.c.lens + Q.s) - (end - Q.t0);       // position of the first query
+    Q.last = min(Q.i0 + Q.cnt, P.c.cap) - 1;           // no row behind it is read
+    Q.rn = rn;
+    Q.rc = rc;
+    Q.rt = rt;
+    if (__any_sync(kFull, lane < Q.cnt && (Q.i0 + lane < 0 || Q.i0 + lane >= P.c.cap)) && lane == 0)
+        paged::report(P.c.status);
+    for (unsigned redo = quad_pass<false>(P, Q, -1); redo; redo &= redo - 1) quad_pass<true>(P, Q, __ffs(redo) - 1);
 }
 
 cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
