@@ -6,10 +6,12 @@ implementation to fall back to.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libsfa.so")
+BIND_PATH = os.path.join(_PKG, "_build", "_sfa_bind.so")
 
 SFA_OK = 0
 SFA_ERR_INVALID_ARG = 1
@@ -109,6 +111,26 @@ def load():
             fn.restype = res
         _lib = lib
     return _lib
+
+
+_bind = None
+
+
+def bind():
+    """The native half of the binding (csrc/bind.cpp); raises if it is missing."""
+    global _bind
+    if _bind is None:
+        load()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError(
+                f"_sfa_bind.so is not built ({BIND_PATH}); run "
+                "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        import torch  # noqa: F401  (its libraries)
+        spec = importlib.util.spec_from_file_location("_sfa_bind", BIND_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _bind = module
+    return _bind
 
 
 def strerror(code: int) -> str:

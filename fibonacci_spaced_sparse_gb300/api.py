@@ -8,9 +8,7 @@ Schedules Beat Learned Dilation and Extrapolate Where Dense Attention Fails"
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import functools
 import math
 from typing import Sequence
 
@@ -342,112 +340,17 @@ def sfa_backward(q, k, v, o, dO, lse, *, alpha: float, W: int, rungs=FIBONACCI_B
     return dq, dk, dv, da, dth
 
 
-# ---------------------------------------- norms, paged cache: shared checks --
-#
-# These calls run once per layer and step of a serving loop, where the host's
-# time counts: parameter blocks are kept per set of values, pointers go to the
-# library as plain integers, and a tensor is looked at once.
-
-
-@functools.lru_cache(maxsize=512)
-def _params(B, T, W, alpha, rungs, rope_theta, scale, dtype, round_offsets):
-    return Params(B, T, W=W, alpha=alpha, rungs=rungs, rope_theta=rope_theta, scale=scale, dtype=dtype,
-                  round_offsets=round_offsets)
-
-
-def _on(device, stream):
-    """The context that a call on ``device`` (and ``stream``) runs in: outputs
-    and workspaces are allocated on that stream, and the launch goes to that
-    device, whatever the current ones are."""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
-
-
-def _raw_stream(device, stream):
-    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
-
-
-def _rows(name, t, lead, heads, like=None):
-    """Token stride (elements) of t [*lead, heads, 64]: heads and dimensions
-    contiguous, tokens at one stride, so that a part of a packed projection is
-    taken as it is."""
-    if t.dim() != len(lead) + 2 or t.shape[:-2] != lead or t.shape[-2] != heads or t.shape[-1] != 64:
-        raise ValueError(f"{name} must be {[*lead, heads, 64]}, got {tuple(t.shape)}")
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must share the other tensors' dtype and device")
-    st = t.stride()
-    if t.numel() == 0:
-        return heads * 64
-    step = st[-3]
-    if len(lead) == 2:
-        if lead[1] == 1:
-            step = st[0]
-        elif lead[0] > 1 and st[0] != step * lead[1]:
-            raise ValueError(f"{name}: tokens must lie at one stride, got strides {st}")
-    if math.prod(lead) == 1:
-        step = heads * 64
-    if st[-1] != 1 or (heads > 1 and st[-2] != 64) or step < heads * 64 or step * t.element_size() % 16:
-        raise ValueError(f"{name}: heads must be contiguous and tokens a multiple of 16 bytes apart, got strides {st}")
-    return step
-
-
-def _dense(name, t, shape, dtype, device):
-    """The pointer of a contiguous tensor of this shape and type, 0 for None."""
-    if t is None:
-        return 0
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
-    return t.data_ptr()
-
-
-def _status_ptr(status, device):
-    if status is None:
-        return 0
-    if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
-        raise ValueError(f"status must be an int32 word on {device}")
-    return status.data_ptr()
-
-
-def _table(rope, rows, device, rope_theta, stream):
-    """The RoPE table a call uses: the given one, or the shared one."""
-    if rope_theta <= 0:
-        return None
-    if rope is None:
-        return rope_table(rows, device, rope_theta=rope_theta, stream=stream)
-    if rope.dim() != 3 or rope.shape[1:] != (32, 2) or rope.dtype != torch.float32 or not rope.is_contiguous():
-        raise ValueError("rope must be a contiguous fp32 [rows, 32, 2] table (rope_table)")
-    if rope.device != device:
-        raise ValueError(f"rope must be on {device}")
-    return rope
-
-
 # ------------------------------------------------------- norm with rotation --
+#
+# The norm and paged-cache calls run once per layer and step of a serving loop
+# on kernels of a few microseconds, so their checks, allocations and launches
+# are native (csrc/bind.cpp).
 
 
-def _norm_args(q, k, wq, wk, rope_theta, positions, rope, stream):
-    if q.dim() != 4:
-        raise ValueError(f"q must be [B, T, 8, 64], got {tuple(q.shape)}")
-    lead, dev = q.shape[:2], q.device
-    qs, ks = _rows("q", q, lead, 8), _rows("k", k, lead, 2, q)
-    wqp = _dense("wq", wq, (64,), torch.float32, dev)
-    wkp = _dense("wk", wk, (64,), torch.float32, dev)
-    if not wqp or not wkp:
-        raise ValueError("wq and wk must be fp32 [64] tensors")
-    if positions is not None and rope is None and rope_theta > 0:
-        raise ValueError("positions need a rope table (rope_table) that covers them")
-    posp = _dense("positions", positions, lead, torch.int32, dev)
-    tab = _table(rope, lead[1], dev, rope_theta, stream) if q.numel() else None
-    if tab is not None and positions is None and tab.shape[0] < lead[1]:
-        raise ValueError(f"rope has {tab.shape[0]} rows, the sequence {lead[1]}")
-    p = _params(lead[0], lead[1], 0, 1.0, (), float(rope_theta), 0.0, q.dtype, False)
-    return p, qs, ks, wqp, wkp, posp, tab
+def _on(stream):
+    """The context that a call with ``stream`` runs in: outputs and workspaces
+    are allocated on it too."""
+    return torch.cuda.stream(stream)
 
 
 def sfa_qk_norm_rope(q, k, wq, wk, *, eps: float = 1e-6, rope_theta: float = 1e4, positions=None,
@@ -458,22 +361,14 @@ def sfa_qk_norm_rope(q, k, wq, wk, *, eps: float = 1e-6, rope_theta: float = 1e4
     0 .. T - 1, or ``positions`` (int32 [B, T]) together with a table ``rope``
     that covers them (rope_table(rows, device)).  Returns (qhat, khat), ready
     for the attention calls with rope_theta=0."""
-    dev = q.device
-    with _on(dev, stream):
-        p, qs, ks, wqp, wkp, posp, tab = _norm_args(q, k, wq, wk, rope_theta, positions, rope, stream)
-        if out is None:
-            qh = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            kh = torch.empty(k.shape, dtype=q.dtype, device=dev)
-        else:
-            qh, kh = out
-        st = _lib.load().sfa_qk_norm_rope(
-            p.ref(), q.data_ptr(), qs, k.data_ptr(), ks, wqp, wkp, eps, posp,
-            tab.data_ptr() if tab is not None else 0, tab.shape[0] if tab is not None else 0,
-            _dense("out[0]", qh, q.shape, q.dtype, dev), _dense("out[1]", kh, k.shape, q.dtype, dev),
-            _status_ptr(status, dev), _raw_stream(dev, stream))
-    if st:
-        _lib.check(st, "sfa_qk_norm_rope")
-    return qh, kh
+    if stream is not None:
+        with _on(stream):
+            return sfa_qk_norm_rope(q, k, wq, wk, eps=eps, rope_theta=rope_theta, positions=positions, rope=rope,
+                                    out=out, status=status)
+    if rope is None:
+        rope = _table_for(q, positions, rope_theta)
+    qh, kh = out if out is not None else (None, None)
+    return _native().norm_rope(q, k, wq, wk, eps, rope_theta, positions, rope, qh, kh, status)
 
 
 def sfa_qk_norm_rope_backward(q, k, wq, wk, dqhat, dkhat, *, eps: float = 1e-6,
@@ -482,59 +377,32 @@ def sfa_qk_norm_rope_backward(q, k, wq, wk, dqhat, dkhat, *, eps: float = 1e-6,
     """(dq, dk, dwq, dwk) of sfa_qk_norm_rope for the gradients dqhat, dkhat of
     its results (contiguous).  ``out`` may supply the four outputs and
     ``workspace`` (uint8) the scratch; calls that may overlap need one each."""
-    dev = q.device
-    with _on(dev, stream):
-        p, qs, ks, wqp, wkp, posp, tab = _norm_args(q, k, wq, wk, rope_theta, positions, rope, stream)
-        if out is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-            dwq = torch.empty(64, dtype=torch.float32, device=dev)
-            dwk = torch.empty(64, dtype=torch.float32, device=dev)
-        else:
-            dq, dk, dwq, dwk = out
-        lib = _lib.load()
-        need = lib.sfa_qk_norm_rope_backward_workspace_size(p.ref())
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        st = lib.sfa_qk_norm_rope_backward(
-            p.ref(), q.data_ptr(), qs, k.data_ptr(), ks, wqp, wkp, eps, posp,
-            tab.data_ptr() if tab is not None else 0, tab.shape[0] if tab is not None else 0,
-            _dense("dqhat", dqhat, q.shape, q.dtype, dev), _dense("dkhat", dkhat, k.shape, q.dtype, dev),
-            _dense("out[0]", dq, q.shape, q.dtype, dev), _dense("out[1]", dk, k.shape, q.dtype, dev),
-            _dense("out[2]", dwq, (64,), torch.float32, dev), _dense("out[3]", dwk, (64,), torch.float32, dev),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status_ptr(status, dev),
-            _raw_stream(dev, stream))
-    if st:
-        _lib.check(st, "sfa_qk_norm_rope_backward")
-    return dq, dk, dwq, dwk
+    if stream is not None:
+        with _on(stream):
+            return sfa_qk_norm_rope_backward(q, k, wq, wk, dqhat, dkhat, eps=eps, rope_theta=rope_theta,
+                                             positions=positions, rope=rope, workspace=workspace, out=out,
+                                             status=status)
+    if rope is None:
+        rope = _table_for(q, positions, rope_theta)
+    dq, dk, dwq, dwk = out if out is not None else (None,) * 4
+    return _native().norm_rope_backward(q, k, wq, wk, eps, rope_theta, positions, rope, dqhat, dkhat, workspace,
+                                        dq, dk, dwq, dwk, status)
+
+
+_native = _lib.bind
+
+
+def _table_for(q, positions, rope_theta):
+    """The shared RoPE table for the rows 0 .. T - 1 of q (none without a
+    rotation, or for a q that the call will refuse)."""
+    if rope_theta <= 0 or q.dim() != 4 or not q.is_cuda or q.numel() == 0:
+        return None
+    if positions is not None:
+        raise ValueError("positions need a rope table (rope_table) that covers them")
+    return rope_table(q.shape[1], q.device, rope_theta=rope_theta)
 
 
 # ------------------------------------------------------------- paged cache --
-
-
-def _paged(k_pages, v_pages, block_table, cu_q, seq_lens, N):
-    """The sfa_paged struct of a cache and a step, and the capacity of a
-    sequence."""
-    dev = k_pages.device
-    if not k_pages.is_cuda:
-        raise ValueError("k_pages must be a CUDA tensor")
-    if k_pages.dtype not in _DTYPES:
-        raise TypeError(f"unsupported dtype {k_pages.dtype}")
-    sh = k_pages.shape
-    if len(sh) != 4 or sh[2] != 2 or sh[3] != 64 or not k_pages.is_contiguous():
-        raise ValueError(f"k_pages must be a contiguous [num_pages, page_size, 2, 64] tensor, got {tuple(sh)}")
-    if sh[0] < 1 or sh[1] < 1 or sh[1] & (sh[1] - 1):
-        raise ValueError(f"page_size must be a power of two, got {sh[1]}")
-    if block_table.dim() != 2 or block_table.shape[1] < 1:
-        raise ValueError(f"block_table must be [S, max_pages], got {tuple(block_table.shape)}")
-    S, max_pages = block_table.shape
-    i32 = torch.int32
-    c = _lib.SfaPaged(k_pages.data_ptr(), _dense("v_pages", v_pages, sh, k_pages.dtype, dev), sh[0], sh[1],
-                      _dense("block_table", block_table, block_table.shape, i32, dev), max_pages,
-                      _dense("cu_q", cu_q, (S + 1,), i32, dev), _dense("seq_lens", seq_lens, (S,), i32, dev), N)
-    return c, S, min(max_pages * sh[1], 1 << 24)
 
 
 def sfa_paged_append(k, v, k_pages, v_pages, block_table, cu_q, seq_lens, *, q=None, wq=None, wk=None,
@@ -547,32 +415,20 @@ def sfa_paged_append(k, v, k_pages, v_pages, block_table, cu_q, seq_lens, *, q=N
     int32 [S] (rows with the new ones) on the device.  With ``q`` [N, 8, 64]
     the step's queries are normed (with wq) and rotated too and returned,
     ready for sfa_paged_forward; else returns None.  Rows at and behind
-    cu_q[S] are left as they are, in q_out too."""
-    dev = k_pages.device
-    if k.dim() != 3:
-        raise ValueError(f"k must be [N, 2, 64], got {tuple(k.shape)}")
-    lead = k.shape[:1]
-    with _on(dev, stream):
-        c, S, cap = _paged(k_pages, v_pages, block_table, cu_q, seq_lens, lead[0])
-        ks, vs = _rows("k", k, lead, 2, k_pages), _rows("v", v, lead, 2, k_pages)
-        qs = _rows("q", q, lead, 8, k_pages) if q is not None else 0
-        if q is None and (wq is not None or q_out is not None):
-            raise ValueError("wq and q_out go with q")
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        tab = _table(rope, cap, dev, rope_theta, stream) if lead[0] and S else None
-        if tab is not None:
-            cap = min(cap, tab.shape[0])
-        p = _params(S, cap, 0, 1.0, (), float(rope_theta), 0.0, k_pages.dtype, False)
-        st = _lib.load().sfa_paged_append(
-            p.ref(), ctypes.byref(c), q.data_ptr() if q is not None else 0, qs, k.data_ptr(), ks, v.data_ptr(), vs,
-            _dense("wq", wq, (64,), torch.float32, dev), _dense("wk", wk, (64,), torch.float32, dev), eps,
-            tab.data_ptr() if tab is not None else 0,
-            _dense("q_out", q_out, q.shape, q.dtype, dev) if q is not None else 0,
-            _status_ptr(status, dev), _raw_stream(dev, stream))
-    if st:
-        _lib.check(st, "sfa_paged_append")
-    return q_out
+    cu_q[S] are left as they are, in q_out too.  ``rope`` (rope_table(rows,
+    device)) bounds the positions; without it the shared table is grown to
+    max_pages * page_size rows."""
+    if stream is not None:
+        with _on(stream):
+            return sfa_paged_append(k, v, k_pages, v_pages, block_table, cu_q, seq_lens, q=q, wq=wq, wk=wk, eps=eps,
+                                    rope_theta=rope_theta, rope=rope, q_out=q_out, status=status)
+    if rope_theta <= 0:
+        rope = None
+    elif rope is None and k_pages.is_cuda and k_pages.dim() == 4 and block_table.numel():
+        rope = rope_table(min(block_table.shape[-1] * k_pages.shape[1], 1 << 24), k_pages.device,
+                          rope_theta=rope_theta)
+    return _native().paged_append(k, v, k_pages, v_pages, block_table, cu_q, seq_lens, q, wq, wk, eps, rope_theta,
+                                  rope, q_out, status)
 
 
 def sfa_paged_forward(q, k_pages, v_pages, block_table, cu_q, seq_lens, *, alpha: float, W: int,
@@ -583,27 +439,13 @@ def sfa_paged_forward(q, k_pages, v_pages, block_table, cu_q, seq_lens, *, alpha
     as in sfa_paged_append, after it.  Sequences may bring one token or many.
     Returns (o [N, 8, 64], lse [N, 8]); rows at and behind cu_q[S] are left as
     they are (uninitialised without ``out`` and ``lse``)."""
-    dev = k_pages.device
-    if q.dim() != 3:
-        raise ValueError(f"q must be [N, 8, 64], got {tuple(q.shape)}")
-    lead = q.shape[:1]
-    with _on(dev, stream):
-        c, S, cap = _paged(k_pages, v_pages, block_table, cu_q, seq_lens, lead[0])
-        qs = _rows("q", q, lead, 8, k_pages)
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        if not need_lse:
-            lse = None
-        elif lse is None:
-            lse = torch.empty((lead[0], 8), dtype=torch.float32, device=dev)
-        p = _params(S, cap, int(W), float(alpha), tuple(rungs), 0.0, float(scale), q.dtype, bool(round_offsets))
-        st = _lib.load().sfa_paged_forward(
-            p.ref(), ctypes.byref(c), q.data_ptr(), qs, _dense("out", out, q.shape, q.dtype, dev),
-            _dense("lse", lse, (lead[0], 8), torch.float32, dev), _status_ptr(status, dev),
-            _raw_stream(dev, stream))
-    if st:
-        _lib.check(st, "sfa_paged_forward")
-    return out, lse
+    if stream is not None:
+        with _on(stream):
+            return sfa_paged_forward(q, k_pages, v_pages, block_table, cu_q, seq_lens, alpha=alpha, W=W, rungs=rungs,
+                                     scale=scale, need_lse=need_lse, out=out, lse=lse, status=status,
+                                     round_offsets=round_offsets)
+    return _native().paged_forward(q, k_pages, v_pages, block_table, cu_q, seq_lens, alpha, W, rungs, scale, need_lse,
+                                   out, lse, status, round_offsets)
 
 
 def sfa_read_status(status: torch.Tensor, stream=None) -> int:

@@ -1,8 +1,11 @@
-"""Build libsfa.so in-tree with nvcc for sm_103a (GB300).
+"""Build libsfa.so in-tree with nvcc for sm_103a (GB300), and the native half
+of the Python binding with g++.
 
 Each .cu file under csrc/ is compiled in parallel into an object, then they
-are linked into ``fibonacci_spaced_sparse_gb300/_build/libsfa.so``.  The build
-is skipped when the library is newer than every source and header.
+are linked into ``fibonacci_spaced_sparse_gb300/_build/libsfa.so``;
+csrc/bind.cpp becomes ``_build/_sfa_bind.so``, which uses libsfa.so and the
+installed torch.  The build is skipped when both are newer than every source
+and header.
 """
 from __future__ import annotations
 
@@ -10,6 +13,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libsfa.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
+BIND = os.path.join(BUILD, "_sfa_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -34,14 +40,42 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _compile_bind() -> str:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           cuda, sysconfig.get_paths()["include"]]
+    obj = os.path.join(BUILD, "obj", "bind.cpp.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in inc),
+           "-c", BIND_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BIND_SRC}:\n{r.stderr}")
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BIND + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{BUILD}", "-l:libsfa.so", f"-L{lib}", "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
+    os.replace(tmp, BIND)
 
 
 def build(force: bool = False, ptxas_info: bool = False) -> str:
@@ -63,6 +97,7 @@ def build(force: bool = False, ptxas_info: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        bind_obj = ex.submit(_compile_bind)  # the slowest one: first
         objs = list(ex.map(compile_one, sources()))
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
@@ -70,6 +105,7 @@ def build(force: bool = False, ptxas_info: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_bind(bind_obj.result())
     return LIB
 
 

@@ -156,43 +156,50 @@ def test_accepted_calls_reach_the_launch(lib):
     assert got[0] == [_lib.SFA_ERR_CUDA] * 9 and got[1] == [BAD, BAD, OK]
 
 
-def test_binding_refuses_before_the_library():
+def test_binding_refuses_before_the_library(lib):
     """Shapes, types and devices that the binding turns away (CPU tensors)."""
     q, k = torch.zeros(1, 4, 8, 64), torch.zeros(1, 4, 2, 64)
     w = torch.ones(64)
     with pytest.raises(ValueError, match="CUDA"):
         api.sfa_qk_norm_rope(q, k, w, w)
     with pytest.raises(ValueError, match="must be"):
-        api._rows("q", q, (1, 4), 2)
-    with pytest.raises(TypeError):
-        api._rows("q", q.half(), (1, 4), 8)
+        api.sfa_qk_norm_rope(q[0], k, w, w)
+    with pytest.raises(TypeError, match="dtype"):
+        api.sfa_qk_norm_rope(q.half(), k.half(), w, w)
+    with pytest.raises(TypeError, match="tensor"):
+        api._native().norm_rope(None, k, w, w, 1e-6, 0.0, None, None, None, None, None)
+    with pytest.raises(TypeError, match="arguments"):
+        api._native().norm_rope(q, k)
+    pages = torch.zeros(4, 16, 2, 64)
     with pytest.raises(ValueError, match="k_pages"):
-        api.sfa_paged_append(k[0], k[0], torch.zeros(4, 16, 2, 64), torch.zeros(4, 16, 2, 64), None, None, None)
+        api.sfa_paged_append(k[0], k[0], pages, pages, torch.zeros(1, 2, dtype=torch.int32), None, None)
+    with pytest.raises(ValueError, match="k_pages"):
+        api.sfa_paged_forward(q[0], pages, pages, None, None, None, alpha=1.0, W=12)
+    with pytest.raises(ValueError, match="must be"):
+        api.sfa_paged_forward(q, pages, pages, None, None, None, alpha=1.0, W=12)
 
 
-class _Cuda:
-    """A stand-in with a CUDA tensor's shape and strides."""
-    is_cuda, dtype, device = True, torch.bfloat16, "cuda:0"
-
-    def __init__(self, t):
-        self.t, self.shape = t, t.shape
-
-    def __getattr__(self, name):
-        return getattr(self.t, name)
-
-    def element_size(self):
-        return 2
-
-
-def test_token_strides_of_the_binding():
+def test_token_strides_of_the_binding(lib):
+    stride = api._native().stride_of
     x = torch.zeros(3, 5, 768)
     q, k = x[..., :512].unflatten(-1, (8, 64)), x[..., 512:640].unflatten(-1, (2, 64))
-    assert api._rows("q", _Cuda(q), (3, 5), 8) == 768 and api._rows("k", _Cuda(k), (3, 5), 2) == 768
-    assert api._rows("q", _Cuda(q[:, :1]), (3, 1), 8) == 5 * 768      # single tokens of a longer batch
-    assert api._rows("q", _Cuda(q[0]), (5,), 8) == 768
-    assert api._rows("q", _Cuda(q[:1, :1]), (1, 1), 8) == 512
-    assert api._rows("q", _Cuda(q[:0]), (0, 5), 8) == 512
-    for bad, lead in ((q[:, :3], (3, 3)), (q.transpose(0, 1), (5, 3)), (q.flip(-1)[..., ::2].repeat(1, 1, 1, 2)[..., ::1].transpose(2, 3).contiguous().transpose(2, 3), (3, 5)),
-                      (torch.zeros(1, 1, 8, 64).expand(3, 5, 8, 64), (3, 5)), (torch.zeros(3, 5, 516)[..., :512].unflatten(-1, (8, 64)), (3, 5))):
+    assert stride(q, 8) == 768 and stride(k, 2) == 768
+    assert stride(q[:, :1], 8) == 5 * 768             # single tokens of a longer batch
+    assert stride(q[0], 8) == 768
+    assert stride(q[:1, :1], 8) == 512                # one token: any stride
+    assert stride(q[:0], 8) == 512
+    bad = (q[:, :3],                                  # sequences further apart than their tokens
+           q.transpose(0, 1), q.transpose(2, 3).contiguous().transpose(2, 3),
+           torch.zeros(1, 1, 8, 64).expand(3, 5, 8, 64),
+           torch.zeros(3, 5, 516, dtype=torch.bfloat16)[..., :512].unflatten(-1, (8, 64)),  # 1032 bytes apart
+           q[..., :32], x[..., :384].unflatten(-1, (8, 48)))
+    for t in bad:
         with pytest.raises(ValueError):
-            api._rows("q", _Cuda(bad), lead, 8)
+            stride(t, 8)
+
+
+def test_missing_binding_fails_loudly(lib, monkeypatch, tmp_path):
+    monkeypatch.setattr(_lib, "_bind", None)
+    monkeypatch.setattr(_lib, "BIND_PATH", str(tmp_path / "nope.so"))
+    with pytest.raises(RuntimeError, match="not built"):
+        _lib.bind()
