@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
         dst = static_cast<T*>(a.qhat) + (size_t)t * (kHq * kD) + role * 2 * kD;
     }
     const float* wp = role == kKey ? a.wk : a.wq;
-    const unsigned quad_mask = 0xfu << (threadIdx.x & 28);
+    const unsigned mask = 0xfu << (threadIdx.x & 28);
     Row w;
     if (wp) w = weights(wp, c);
     Angles rot;
@@ -76,19 +76,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         Row x = open(raw[h]);
-        if (wp) {
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss += x.x[j] * x.x[j] + x.y[j] * x.y[j];
-            ss += __shfl_xor_sync(quad_mask, ss, 1);
-            ss += __shfl_xor_sync(quad_mask, ss, 2);
-            const float r = 1.f / sqrtf(ss * (1.f / kD) + a.eps);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x.x[j] = x.x[j] * r * w.x[j];
-                x.y[j] = x.y[j] * r * w.y[j];
-            }
-        }
+        if (wp) scale(x, inv_rms(x, a.eps, mask), w);
         if (a.rope && good) rotate(x, rot);
         if (!good) x = Row{};
         store(dst + h * kD, c, x);

@@ -13,9 +13,14 @@
 namespace sfa {
 namespace heads {
 
+// Values in pairs (j, j + 1) for the packed two-lane fp32 instructions.
+constexpr int kP = 4;  // pairs of values of a half
 struct Row {
-    float x[8], y[8];
+    float2 x[kP], y[kP];
 };
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
 
 // The raw words of a lane's part of a row, kept apart from their conversion so
 // that the loads of several rows are in flight together.
@@ -56,19 +61,16 @@ __device__ __forceinline__ void put(float* row, int c, const Raw<float>& r) {
     p[9 + 2 * c] = r.y1;
 }
 
-__device__ __forceinline__ void words(const uint4& u, float (&f)[8]) {
+__device__ __forceinline__ void words(const uint4& u, float2 (&f)[kP]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+    for (int j = 0; j < kP; ++j) f[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+__device__ __forceinline__ uint4 pack(const float2 (&f)[kP]) {
     uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+    for (int j = 0; j < kP; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[j].x, f[j].y);
         w[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -85,14 +87,10 @@ __device__ __forceinline__ Row open(const Raw<float>& r) {
     const float4 v[4] = {r.x0, r.x1, r.y0, r.y1};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        a.x[4 * j] = v[j].x;
-        a.x[4 * j + 1] = v[j].y;
-        a.x[4 * j + 2] = v[j].z;
-        a.x[4 * j + 3] = v[j].w;
-        a.y[4 * j] = v[2 + j].x;
-        a.y[4 * j + 1] = v[2 + j].y;
-        a.y[4 * j + 2] = v[2 + j].z;
-        a.y[4 * j + 3] = v[2 + j].w;
+        a.x[2 * j] = make_float2(v[j].x, v[j].y);
+        a.x[2 * j + 1] = make_float2(v[j].z, v[j].w);
+        a.y[2 * j] = make_float2(v[2 + j].x, v[2 + j].y);
+        a.y[2 * j + 1] = make_float2(v[2 + j].z, v[2 + j].w);
     }
     return a;
 }
@@ -102,10 +100,49 @@ __device__ __forceinline__ void close(const Row& a, Raw<__nv_bfloat16>& r) {
     r.y = pack(a.y);
 }
 __device__ __forceinline__ void close(const Row& a, Raw<float>& r) {
-    r.x0 = make_float4(a.x[0], a.x[1], a.x[2], a.x[3]);
-    r.x1 = make_float4(a.x[4], a.x[5], a.x[6], a.x[7]);
-    r.y0 = make_float4(a.y[0], a.y[1], a.y[2], a.y[3]);
-    r.y1 = make_float4(a.y[4], a.y[5], a.y[6], a.y[7]);
+    r.x0 = make_float4(a.x[0].x, a.x[0].y, a.x[1].x, a.x[1].y);
+    r.x1 = make_float4(a.x[2].x, a.x[2].y, a.x[3].x, a.x[3].y);
+    r.y0 = make_float4(a.y[0].x, a.y[0].y, a.y[1].x, a.y[1].y);
+    r.y1 = make_float4(a.y[2].x, a.y[2].y, a.y[3].x, a.y[3].y);
+}
+
+// The same words through shared memory: each lane copies its own 16-byte pieces
+// there ahead of time and reads them back itself, so that loads in flight take
+// no registers and no barrier.  Slot p of thread i is slot[p * blockDim.x + i].
+template <typename T>
+constexpr int kPieces = sizeof(Raw<T>) / 16;
+
+__device__ __forceinline__ void copy16(uint4* slot, const void* src, bool keep = false) {
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
+    if (keep)  // worth a place in L1
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void copy_row(uint4* slot, const T* row, int c) {
+    const uint4* p = reinterpret_cast<const uint4*>(row);
+    if (kPieces<T> == 2) {
+        copy16(slot, p + c);
+        copy16(slot + blockDim.x, p + 4 + c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) copy16(slot + i * blockDim.x, p + 2 * c + (i & 1) + 8 * (i >> 1));
+    }
+}
+template <typename T>
+__device__ __forceinline__ Raw<T> take_row(const uint4* slot) {
+    Raw<T> r;
+    uint4* w = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+    for (int i = 0; i < kPieces<T>; ++i) w[i] = slot[i * blockDim.x];
+    return r;
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but the n latest groups of this thread's copies are there.
+template <int n>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
 template <typename T>
@@ -125,56 +162,81 @@ __device__ __forceinline__ Row weights(const float* w, int c) {
 // (cos, sin) of a lane's pairs at one position: 64 contiguous bytes of the
 // table row.
 struct Angles {
-    float c[8], s[8];
+    float2 c[kP], s[kP];
 };
 __device__ __forceinline__ Angles angles(const float2* __restrict__ rope, int pos, int c) {
     const float4* p = reinterpret_cast<const float4*>(rope + (size_t)pos * kPairs + 8 * c);
     Angles a;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kP; ++j) {
         const float4 v = __ldg(p + j);
-        a.c[2 * j] = v.x;
-        a.s[2 * j] = v.y;
-        a.c[2 * j + 1] = v.z;
-        a.s[2 * j + 1] = v.w;
+        a.c[j] = make_float2(v.x, v.z);
+        a.s[j] = make_float2(v.y, v.w);
+    }
+    return a;
+}
+
+// The same through shared memory (four pieces).
+__device__ __forceinline__ void copy_angles(uint4* slot, const float2* rope, int pos, int c) {
+    const uint4* p = reinterpret_cast<const uint4*>(rope + (size_t)pos * kPairs + 8 * c);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) copy16(slot + j * blockDim.x, p + j, true);
+}
+__device__ __forceinline__ Angles take_angles(const uint4* slot) {
+    Angles a;
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(slot + j * blockDim.x);
+        a.c[j] = make_float2(v.x, v.z);
+        a.s[j] = make_float2(v.y, v.w);
     }
     return a;
 }
 
 __device__ __forceinline__ void rotate(Row& a, const Angles& r) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float x = a.x[j], y = a.y[j];
-        a.x[j] = x * r.c[j] - y * r.s[j];
-        a.y[j] = y * r.c[j] + x * r.s[j];
+    for (int j = 0; j < kP; ++j) {
+        const float2 x = a.x[j], y = a.y[j];
+        a.x[j] = __ffma2_rn(x, r.c[j], __fmul2_rn(neg(y), r.s[j]));
+        a.y[j] = __ffma2_rn(y, r.c[j], __fmul2_rn(x, r.s[j]));
     }
 }
 // The transpose (inverse) of rotate.
 __device__ __forceinline__ void rotate_back(Row& a, const Angles& r) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float x = a.x[j], y = a.y[j];
-        a.x[j] = x * r.c[j] + y * r.s[j];
-        a.y[j] = y * r.c[j] - x * r.s[j];
+    for (int j = 0; j < kP; ++j) {
+        const float2 x = a.x[j], y = a.y[j];
+        a.x[j] = __ffma2_rn(x, r.c[j], __fmul2_rn(y, r.s[j]));
+        a.y[j] = __ffma2_rn(y, r.c[j], __fmul2_rn(neg(x), r.s[j]));
     }
 }
 
-// Sum over the four lanes of a row.
-__device__ __forceinline__ float row_sum(float v) {
-    v += __shfl_xor_sync(kFull, v, 1);
-    return v + __shfl_xor_sync(kFull, v, 2);
-}
-
-__device__ __forceinline__ float dot(const Row& a, const Row& b) {
-    float s = 0.f;
+// a <- a f w
+__device__ __forceinline__ void scale(Row& a, float f, const Row& w) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s += a.x[j] * b.x[j] + a.y[j] * b.y[j];
-    return row_sum(s);
+    for (int j = 0; j < kP; ++j) {
+        a.x[j] = __fmul2_rn(__fmul2_rn(a.x[j], both(f)), w.x[j]);
+        a.y[j] = __fmul2_rn(__fmul2_rn(a.y[j], both(f)), w.y[j]);
+    }
 }
 
-// 1 / sqrt(mean(x^2) + eps) of a row.
-__device__ __forceinline__ float inv_rms(const Row& a, float eps) {
-    return 1.f / sqrtf(dot(a, a) * (1.f / kD) + eps);
+// Sum of the products of two rows, in every lane of the row; `mask`: lanes
+// that are here together, whole rows.
+__device__ __forceinline__ float dot(const Row& a, const Row& b, unsigned mask = kFull) {
+    float2 s = __fmul2_rn(a.x[0], b.x[0]);
+#pragma unroll
+    for (int j = 1; j < kP; ++j) s = __ffma2_rn(a.x[j], b.x[j], s);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) s = __ffma2_rn(a.y[j], b.y[j], s);
+    float v = s.x + s.y;
+    v += __shfl_xor_sync(mask, v, 1);
+    return v + __shfl_xor_sync(mask, v, 2);
+}
+
+// 1 / sqrt(mean(x^2) + eps) of a row (the approximation's error, 2 units in
+// the last place, is that of the products around it).
+__device__ __forceinline__ float inv_rms(const Row& a, float eps, unsigned mask = kFull) {
+    return rsqrtf(dot(a, a, mask) * (1.f / kD) + eps);
 }
 
 }  // namespace heads

@@ -10,7 +10,8 @@
 // operations each.  Four lanes hold a row (sfa_heads.cuh); a quad of lanes
 // handles two heads of one token that share their weights (queries 0-1, 2-3,
 // 4-5, 6-7, keys 0-1), so five quads cover a token and the (cos, sin) of its
-// position are read once for two rows.
+// position are read once for two rows.  Packed fp32 arithmetic and one
+// approximate root a row keep the instructions well below the memory time.
 #include "sfa_heads.cuh"
 
 namespace sfa {
@@ -19,7 +20,7 @@ namespace {
 
 using namespace heads;
 
-constexpr int kTok = 16;                        // tokens of a block
+constexpr int kTok = 8;                          // tokens of a block's step
 constexpr int kPairsOfHeads = (kHq + kHkv) / 2;  // quads of a token
 constexpr int kThreads = kTok * kPairsOfHeads * 4;
 
@@ -30,77 +31,158 @@ __device__ __forceinline__ int position(const NormArgs& a, int t) {
     return pos >= 0 && pos < a.table_rows ? pos : -1;
 }
 
+// The two rows of a quad's heads in a [token][head][64] tensor.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormArgs a, T* __restrict__ qhat,
-                                                            T* __restrict__ khat) {
+struct Rows {
+    T* p;
+    long long stride;  // of tokens
+    __device__ T* of(int t) const { return p + (size_t)t * stride; }
+};
+template <typename T>
+__device__ __forceinline__ Rows<const T> inputs(const NormArgs& a, int hp) {
+    return hp < kHq / 2 ? Rows<const T>{static_cast<const T*>(a.q) + hp * 2 * kD, a.qs}
+                        : Rows<const T>{static_cast<const T*>(a.k), a.ks};
+}
+template <typename T>
+__device__ __forceinline__ Rows<T> dense(T* q, T* k, int hp) {
+    return hp < kHq / 2 ? Rows<T>{q + hp * 2 * kD, kHq * kD} : Rows<T>{k, kHkv * kD};
+}
+
+// A bad position is reported once a token.
+__device__ __forceinline__ void report(const NormArgs& a, int hp, int c) {
+    if (hp == 0 && c == 0 && a.status) atomicOr(a.status, SFA_DEVSTAT_BAD_INDEX);
+}
+
+// Norm and rotation of a row at position pos (< 0: zeros).
+__device__ __forceinline__ void norm_row(const NormArgs& a, Row& x, const Row& w, const Angles& rot, int pos,
+                                         unsigned mask) {
+    scale(x, inv_rms(x, a.eps, mask), w);
+    if (a.rope) rotate(x, rot);
+    if (pos < 0) x = Row{};
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) norm_fwd_kernel(const NormArgs a, T* __restrict__ qhat,
+                                                               T* __restrict__ khat) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int quad = threadIdx.x >> 2, c = threadIdx.x & 3;
-    const int hp = quad % kPairsOfHeads;
-    const bool is_q = hp < kHq / 2;
+    const int quad = threadIdx.x >> 2, c = threadIdx.x & 3, hp = quad % kPairsOfHeads;
     const int t = blockIdx.x * kTok + quad / kPairsOfHeads;
     const bool live = t < a.N;
     const int tt = live ? t : a.N - 1;  // idle lanes repeat the last token and store nothing
-    const T* src = is_q ? static_cast<const T*>(a.q) + (size_t)tt * a.qs + hp * 2 * kD
-                        : static_cast<const T*>(a.k) + (size_t)tt * a.ks;
-    T* dst = is_q ? qhat + (size_t)tt * (kHq * kD) + hp * 2 * kD : khat + (size_t)tt * (kHkv * kD);
+    const T* src = inputs<T>(a, hp).of(tt);
+    T* dst = dense(qhat, khat, hp).of(tt);
     Raw<T> raw[2];
     fetch(src, c, raw[0]);
     fetch(src + kD, c, raw[1]);
-    const Row w = weights(is_q ? a.wq : a.wk, c);
+    const Row w = weights(hp < kHq / 2 ? a.wq : a.wk, c);
     const int pos = position(a, tt);
     Angles rot;
     if (a.rope) rot = angles(a.rope, max(pos, 0), c);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         Row x = open(raw[h]);
-        const float r = inv_rms(x, a.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x.x[j] = x.x[j] * r * w.x[j];
-            x.y[j] = x.y[j] * r * w.y[j];
-        }
-        if (a.rope) rotate(x, rot);
-        if (pos < 0) x = Row{};
+        norm_row(a, x, w, rot, pos, kFull);
         if (live) store(dst + h * kD, c, x);
     }
-    if (pos < 0 && live && c == 0 && hp == 0 && a.status) atomicOr(a.status, SFA_DEVSTAT_BAD_INDEX);
+    if (pos < 0 && live) report(a, hp, c);
+}
+
+// The same for many bf16 tokens: a bf16 lane's loads are too few bytes in
+// flight for the memory's latency (45 KB a SM), so a block goes through tokens
+// a grid apart and copies the next step's rows and angles to shared memory
+// meanwhile, each lane its own pieces (sfa_heads.cuh): no registers, no
+// barrier.
+constexpr int kFwdPieces = 2 * kPieces<__nv_bfloat16>, kSlots = kFwdPieces + 4;  // pieces of a step: rows, angles
+constexpr int kAhead = 2;  // steps whose rows are on their way or in use
+constexpr int kPipedBlocks = 152 * 3;
+constexpr size_t kPipedSmem = (size_t)kAhead * kSlots * kThreads * sizeof(uint4);
+
+__global__ void __launch_bounds__(kThreads, 3)
+    norm_fwd_piped_kernel(const NormArgs a, __nv_bfloat16* __restrict__ qhat, __nv_bfloat16* __restrict__ khat) {
+    using T = __nv_bfloat16;
+    extern __shared__ uint4 slots[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int quad = threadIdx.x >> 2, c = threadIdx.x & 3, hp = quad % kPairsOfHeads;
+    const unsigned mask = 0xfu << (threadIdx.x & 28);  // this quad's lanes
+    const Rows<const T> in = inputs<T>(a, hp);
+    const Rows<T> out = dense(qhat, khat, hp);
+    const Row w = weights(hp < kHq / 2 ? a.wq : a.wk, c);
+    const int step = gridDim.x * kTok;
+    int next = blockIdx.x * kTok + quad / kPairsOfHeads;  // the token to copy next
+    int t[kAhead], pos[kAhead];                           // of the steps on their way
+    auto start = [&](int i) {
+        t[i] = next;
+        if (next < a.N) {
+            uint4* slot = slots + i * kSlots * kThreads + threadIdx.x;
+            pos[i] = position(a, next);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) copy_row(slot + h * kPieces<T> * kThreads, in.of(next) + h * kD, c);
+            if (a.rope) copy_angles(slot + kFwdPieces * kThreads, a.rope, max(pos[i], 0), c);
+            next += step;
+        }
+        copies_end();
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) start(i);
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (t[i] >= a.N) return;
+            copies_wait<kAhead - 1>();
+            const uint4* slot = slots + i * kSlots * kThreads + threadIdx.x;
+            T* dst = out.of(t[i]);
+            const int p = pos[i];
+            Angles rot;
+            if (a.rope) rot = take_angles(slot + kFwdPieces * kThreads);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Row x = open(take_row<T>(slot + h * kPieces<T> * kThreads));
+                if (h == 1) start(i);  // the slots have been read
+                norm_row(a, x, w, rot, p, mask);
+                store(dst + h * kD, c, x);
+            }
+            if (p < 0) report(a, hp, c);
+        }
+    }
 }
 
 // -------------------------------------------------------------- backward
 
-constexpr int kMaxBlocks = 608;          // partial sums of dw (4 a SM at 152 SMs)
-constexpr int kPartial = 2 * kD;         // floats of one: dwq, dwk
+// Resident blocks (of 8 tokens a step): 3 a SM at the 128 registers of bf16, 2
+// at the 165 of fp32.
+template <typename T>
+constexpr int kBwdBlocks = 152 * (sizeof(T) == 2 ? 3 : 2);
+constexpr int kMaxBlocks = 152 * 3;  // partial sums of dw
+constexpr int kPartial = 2 * kD;     // floats of one: dwq, dwk
 
 // Block b writes dx of its tokens (b, b + gridDim, ... in groups of kTok) and
 // its part of dwq, dwk to partial[b]; dw is summed by the launch after it, in
-// a fixed order.
+// a fixed order.  (Copies ahead through shared memory, as in the forward, are
+// no faster here: 27.3 against 26.4 us for 32 x 1024 bf16 tokens, 75 against
+// 48 us in fp32.)
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormArgs a, const T* __restrict__ dqhat,
-                                                            const T* __restrict__ dkhat, T* __restrict__ dq,
-                                                            T* __restrict__ dk, float* __restrict__ partial) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocks<T> / 152)
+    norm_bwd_kernel(const NormArgs a, const T* __restrict__ dqhat, const T* __restrict__ dkhat, T* __restrict__ dq,
+                    T* __restrict__ dk, float* __restrict__ partial) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float sums[kTok * kPairsOfHeads][kD + 1];
-    const int quad = threadIdx.x >> 2, c = threadIdx.x & 3;
-    const int hp = quad % kPairsOfHeads;
-    const bool is_q = hp < kHq / 2;
-    const Row w = weights(is_q ? a.wq : a.wk, c);
+    const int quad = threadIdx.x >> 2, c = threadIdx.x & 3, hp = quad % kPairsOfHeads;
+    const Rows<const T> in = inputs<T>(a, hp), up = dense(dqhat, dkhat, hp);
+    const Rows<T> out = dense(dq, dk, hp);
+    const Row w = weights(hp < kHq / 2 ? a.wq : a.wk, c);
     Row dw{};
     for (int t0 = blockIdx.x * kTok; t0 < a.N; t0 += gridDim.x * kTok) {
         const int t = t0 + quad / kPairsOfHeads;
         const bool live = t < a.N;
-        const int tt = live ? t : a.N - 1;
-        const T* src = is_q ? static_cast<const T*>(a.q) + (size_t)tt * a.qs + hp * 2 * kD
-                            : static_cast<const T*>(a.k) + (size_t)tt * a.ks;
-        const size_t at = is_q ? (size_t)tt * (kHq * kD) + hp * 2 * kD : (size_t)tt * (kHkv * kD);
-        const T* up = (is_q ? dqhat : dkhat) + at;
-        T* dst = (is_q ? dq : dk) + at;
+        const int tt = live ? t : a.N - 1;  // idle lanes repeat the last token; it counts once
         Raw<T> rx[2], rg[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            fetch(src + h * kD, c, rx[h]);
-            fetch(up + h * kD, c, rg[h]);
+            fetch(in.of(tt) + h * kD, c, rx[h]);
+            fetch(up.of(tt) + h * kD, c, rg[h]);
         }
         const int pos = position(a, tt);
         Angles rot;
@@ -109,32 +191,35 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormArgs a, co
         for (int h = 0; h < 2; ++h) {
             Row x = open(rx[h]), g = open(rg[h]);
             if (a.rope) rotate_back(g, rot);
-            const float r = inv_rms(x, a.eps);
-            const bool counts = live && pos >= 0;
+            const float2 r = both(inv_rms(x, a.eps));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x.x[j] *= r;
-                x.y[j] *= r;
-                dw.x[j] += counts ? g.x[j] * x.x[j] : 0.f;
-                dw.y[j] += counts ? g.y[j] * x.y[j] : 0.f;
-                g.x[j] *= w.x[j];
-                g.y[j] *= w.y[j];
+            for (int j = 0; j < kP; ++j) {
+                x.x[j] = __fmul2_rn(x.x[j], r);
+                x.y[j] = __fmul2_rn(x.y[j], r);
+                if (live && pos >= 0) {
+                    dw.x[j] = __ffma2_rn(g.x[j], x.x[j], dw.x[j]);
+                    dw.y[j] = __ffma2_rn(g.y[j], x.y[j], dw.y[j]);
+                }
+                g.x[j] = __fmul2_rn(g.x[j], w.x[j]);
+                g.y[j] = __fmul2_rn(g.y[j], w.y[j]);
             }
-            const float m = dot(g, x) * (1.f / kD);
+            const float2 m = both(dot(g, x) * (-1.f / kD));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                g.x[j] = r * (g.x[j] - x.x[j] * m);
-                g.y[j] = r * (g.y[j] - x.y[j] * m);
+            for (int j = 0; j < kP; ++j) {
+                g.x[j] = __fmul2_rn(__ffma2_rn(x.x[j], m, g.x[j]), r);
+                g.y[j] = __fmul2_rn(__ffma2_rn(x.y[j], m, g.y[j]), r);
             }
             if (pos < 0) g = Row{};
-            if (live) store(dst + h * kD, c, g);
+            if (live) store(out.of(tt) + h * kD, c, g);
         }
-        if (pos < 0 && live && c == 0 && hp == 0 && a.status) atomicOr(a.status, SFA_DEVSTAT_BAD_INDEX);
+        if (pos < 0 && live) report(a, hp, c);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        sums[quad][8 * c + j] = dw.x[j];
-        sums[quad][kPairs + 8 * c + j] = dw.y[j];
+    for (int j = 0; j < kP; ++j) {
+        sums[quad][8 * c + 2 * j] = dw.x[j].x;
+        sums[quad][8 * c + 2 * j + 1] = dw.x[j].y;
+        sums[quad][kPairs + 8 * c + 2 * j] = dw.y[j].x;
+        sums[quad][kPairs + 8 * c + 2 * j + 1] = dw.y[j].y;
     }
     __syncthreads();
     if (threadIdx.x < kPartial) {
@@ -153,32 +238,44 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormArgs a, co
     }
 }
 
-// dwq, dwk: the sum of the blocks' parts.  A block sums 16 columns, 32 threads
-// a column.
-constexpr int kFinCols = 16, kFinRows = 32;
+// dwq, dwk: the sum of the blocks' parts.  A block sums kFinCols columns,
+// kFinRows threads a column, each with all of its loads in flight at once.
+constexpr int kFinCols = 8, kFinRows = 64, kFinEach = (kMaxBlocks + kFinRows - 1) / kFinRows;
 __global__ void __launch_bounds__(kFinCols* kFinRows) norm_dw_kernel(const float* __restrict__ partial, int blocks,
                                                                      float* __restrict__ dwq, float* __restrict__ dwk) {
+    __shared__ float sums[kFinRows / 4][kFinCols + 1];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ float sums[kFinRows][kFinCols + 1];
     const int col = threadIdx.x % kFinCols, row = threadIdx.x / kFinCols;
     const int d = blockIdx.x * kFinCols + col;
+    float part[kFinEach];
+#pragma unroll
+    for (int i = 0; i < kFinEach; ++i) {
+        const int b = row + i * kFinRows;
+        part[i] = b < blocks ? __ldg(partial + (size_t)b * kPartial + d) : 0.f;
+    }
     float s = 0.f;
-    for (int b = row; b < blocks; b += kFinRows) s += partial[(size_t)b * kPartial + d];
-    sums[row][col] = s;
+#pragma unroll
+    for (int i = 0; i < kFinEach; ++i) s += part[i];
+    // a warp holds four rows of the same columns
+    s += __shfl_xor_sync(kFull, s, 8);
+    s += __shfl_xor_sync(kFull, s, 16);
+    if ((threadIdx.x & 31) < kFinCols) sums[row / 4][col] = s;
     __syncthreads();
-    if (row == 0) {
+    if (threadIdx.x < kFinCols) {
         s = 0.f;
-        for (int r = 0; r < kFinRows; ++r) s += sums[r][col];
+#pragma unroll
+        for (int r = 0; r < kFinRows / 4; ++r) s += sums[r][col];
         (d < kD ? dwq : dwk)[d & (kD - 1)] = s;
     }
 }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t s, A... args) {
+cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -190,32 +287,53 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, cudaSt
     return e;
 }
 
-unsigned blocks_of(int N) { return (unsigned)((N + kTok - 1) / kTok); }
+unsigned steps_of(int N) { return (unsigned)((N + kTok - 1) / kTok); }
+
+cudaError_t launch_piped(const NormArgs& a, __nv_bfloat16* qhat, __nv_bfloat16* khat, cudaStream_t s) {
+    static CtxSetting done[64];  // per device: dynamic shared memory allowed
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!ctx_setting_holds(done[dev & 63], kPipedSmem)) {
+        e = cudaFuncSetAttribute(norm_fwd_piped_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPipedSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(norm_fwd_piped_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e != cudaSuccess) return e;
+        ctx_setting_done(done[dev & 63], kPipedSmem);
+    }
+    return launch(norm_fwd_piped_kernel, kPipedBlocks, kThreads, kPipedSmem, s, a, qhat, khat);
+}
+
+// bf16 tokens from which the piped kernel is the faster one (us, direct and
+// piped): 8192 tokens 4.8 and 5.4, 12288 8.9 and 8.4, 32768 18.2 and 15.9,
+// 131072 65.1 and 54.3 (92 % of the measured copy rate).
+constexpr int kPipedFrom = 10240;
 
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormArgs& a, sfa_dtype dt, void* qhat, void* khat, cudaStream_t s) {
-    if (dt == SFA_BF16)
-        return launch(norm_fwd_kernel<__nv_bfloat16>, blocks_of(a.N), kThreads, s, a, (__nv_bfloat16*)qhat,
-                      (__nv_bfloat16*)khat);
-    return launch(norm_fwd_kernel<float>, blocks_of(a.N), kThreads, s, a, (float*)qhat, (float*)khat);
+    if (dt == SFA_F32)
+        return launch(norm_fwd_kernel<float>, steps_of(a.N), kThreads, 0, s, a, (float*)qhat, (float*)khat);
+    if (a.N >= kPipedFrom) return launch_piped(a, (__nv_bfloat16*)qhat, (__nv_bfloat16*)khat, s);
+    return launch(norm_fwd_kernel<__nv_bfloat16>, steps_of(a.N), kThreads, 0, s, a, (__nv_bfloat16*)qhat,
+                  (__nv_bfloat16*)khat);
 }
 
 size_t norm_bwd_workspace() { return (size_t)kMaxBlocks * kPartial * sizeof(float); }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, sfa_dtype dt, const void* dqhat, const void* dkhat, void* dq, void* dk,
                             float* dwq, float* dwk, void* ws, cudaStream_t s) {
-    const unsigned blocks = blocks_of(a.N) < (unsigned)kMaxBlocks ? blocks_of(a.N) : (unsigned)kMaxBlocks;
+    const unsigned most = (unsigned)(dt == SFA_BF16 ? kBwdBlocks<__nv_bfloat16> : kBwdBlocks<float>);
+    const unsigned blocks = steps_of(a.N) < most ? steps_of(a.N) : most;
     float* partial = static_cast<float*>(ws);
-    cudaError_t e;
-    if (dt == SFA_BF16)
-        e = launch(norm_bwd_kernel<__nv_bfloat16>, blocks, kThreads, s, a, (const __nv_bfloat16*)dqhat,
-                   (const __nv_bfloat16*)dkhat, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, partial);
-    else
-        e = launch(norm_bwd_kernel<float>, blocks, kThreads, s, a, (const float*)dqhat, (const float*)dkhat,
-                   (float*)dq, (float*)dk, partial);
+    const cudaError_t e =
+        dt == SFA_BF16
+            ? launch(norm_bwd_kernel<__nv_bfloat16>, blocks, kThreads, 0, s, a, (const __nv_bfloat16*)dqhat,
+                     (const __nv_bfloat16*)dkhat, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, partial)
+            : launch(norm_bwd_kernel<float>, blocks, kThreads, 0, s, a, (const float*)dqhat, (const float*)dkhat,
+                     (float*)dq, (float*)dk, partial);
     if (e != cudaSuccess) return e;
-    return launch(norm_dw_kernel, (unsigned)(kPartial / kFinCols), (unsigned)(kFinCols * kFinRows), s,
+    return launch(norm_dw_kernel, (unsigned)(kPartial / kFinCols), (unsigned)(kFinCols * kFinRows), 0, s,
                   (const float*)partial, (int)blocks, dwq, dwk);
 }
 
