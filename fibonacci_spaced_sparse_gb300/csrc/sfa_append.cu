@@ -15,7 +15,7 @@ namespace {
 
 using namespace heads;
 
-constexpr int kThreads = 192;  // 48 quads: 8 tokens with queries, 24 without
+constexpr int kThreads = 96;  // 24 quads: 4 tokens with queries, 12 without
 
 // kQ: the step's queries are transformed too.
 template <typename T, bool kQ>

@@ -232,43 +232,50 @@ __device__ __forceinline__ void write_part(const PagedFwd& P, int t, int g, int 
     if (P.lse && ch == 0) P.lse[at] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * kLn2;
 }
 
+template <int kNW>
+constexpr int kRowThreads = kNW > 1 ? 32 * kNW : 256;  // one unit a block, or eight of one warp each
+
 template <typename T, int kNW>
-__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ PagedFwd P) {
+__global__ void __launch_bounds__(kRowThreads<kNW>, 512 / kRowThreads<kNW>) rows_kernel(const __grid_constant__ PagedFwd P) {
+    constexpr int kThreads = kRowThreads<kNW>, kUnits = kNW > 1 ? 1 : 8;  // (token, head) of a block
+    __shared__ __align__(16) float part[kNW > 1 ? kNW : 1][kNW > 1 ? kG * kD : 4];
+    __shared__ float top[kNW][kG], sum[kNW][kG];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int kUnits = 8 / kNW;  // (token, head) of a block
-    __shared__ float part[kNW > 1 ? kNW : 1][kNW > 1 ? kG * kD : 1];
-    __shared__ float top[kNW][kG], sum[kNW][kG];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned unit = blockIdx.x * kUnits + warp / kNW;
+    const unsigned unit = blockIdx.x * kUnits + (kNW > 1 ? 0 : warp);
     const int t = (int)(unit / kHkv), g = (int)(unit % kHkv);
-    if (t >= P.c.N) return;  // with kNW > 1 the whole block
+    if (t >= P.c.N) return;  // with kNW > 1 the whole block, here and below
     const int s = paged::sequence_of(P.c, t);
     if (s >= P.c.S) return;
     const int pos = __ldg(P.c.lens + s) - (__ldg(P.c.cu + s + 1) - t);
     if (pos < 0 || pos >= P.c.cap) {
-        if (threadIdx.x % (32 * kNW) == 0 && g == 0) paged::report(P.c.status);
-        zero_out<T>(P, t, g, threadIdx.x % (32 * kNW), 32 * kNW);
+        const int i = kNW > 1 ? threadIdx.x : lane;
+        if (i == 0 && g == 0) paged::report(P.c.status);
+        zero_out<T>(P, t, g, i, kNW > 1 ? kThreads : 32);
         return;
     }
     const T* qrow = static_cast<const T*>(P.q) + (size_t)t * P.qs + g * kG * kD;
-    const Partial x = query_part<T>(P, s, pos, g, qrow, 4 * (warp % kNW), 4 * kNW);
+    const Partial x = query_part<T>(P, s, pos, g, qrow, kNW > 1 ? 4 * warp : 0, 4 * kNW);
     const int h = lane >> 3, ch = lane & 7;
     if (kNW == 1) {
         write_part<T>(P, t, g, h, ch, x);
         return;
     }
-    T* o = static_cast<T*>(P.o) + ((size_t)t * kHq + g * kG) * kD;
-    float* lse = P.lse ? P.lse + (size_t)t * kHq + g * kG : nullptr;
     if (ch == 0) {
         top[warp][h] = x.m;
         sum[warp][h] = x.l;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) part[kNW > 1 ? warp : 0][kNW > 1 ? h * kD + 8 * ch + j : 0] = x.acc[j];
+    float* mine = part[kNW > 1 ? warp : 0] + (kNW > 1 ? h * kD + 8 * ch : 0);
+    if (kNW > 1) {
+        reinterpret_cast<float4*>(mine)[0] = make_float4(x.acc[0], x.acc[1], x.acc[2], x.acc[3]);
+        reinterpret_cast<float4*>(mine)[1] = make_float4(x.acc[4], x.acc[5], x.acc[6], x.acc[7]);
+    }
     __syncthreads();
-    {
-        const int hh = threadIdx.x >> 6;  // 256 threads: one output each
+    T* o = static_cast<T*>(P.o) + ((size_t)t * kHq + g * kG) * kD;
+#pragma unroll
+    for (int i = threadIdx.x; i < kG * kD; i += kThreads) {
+        const int hh = i / kD;
         float m = top[0][hh];
 #pragma unroll
         for (int w = 1; w < kNW; ++w) m = fmaxf(m, top[w][hh]);
@@ -277,21 +284,22 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Paged
         for (int w = 0; w < kNW; ++w) {
             const float f = exp2f(top[w][hh] - m);
             l = fmaf(f, sum[w][hh], l);
-            v = fmaf(f, part[kNW > 1 ? w : 0][kNW > 1 ? threadIdx.x : 0], v);
+            v = fmaf(f, part[kNW > 1 ? w : 0][kNW > 1 ? i : 0], v);
         }
         const float inv = l != 0.f ? 1.f / l : 0.f;
-        o[threadIdx.x] = from_f32<T>(v * inv);
-        if (lse && (threadIdx.x & 63) == 0) lse[hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        o[i] = from_f32<T>(v * inv);
+        if (P.lse && i % kD == 0)
+            P.lse[(size_t)t * kHq + g * kG + hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
 }
 
 template <typename T, int kNW>
-cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
-    constexpr int kUnits = 8 / kNW;
+cudaError_t launch_rows_nw(const PagedFwd& P, cudaStream_t s) {
+    constexpr int kUnits = kNW > 1 ? 1 : 8;
     const long long units = (long long)P.c.N * kHkv;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((units + kUnits - 1) / kUnits));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kRowThreads<kNW>);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -301,6 +309,20 @@ cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
     const cudaError_t e = cudaLaunchKernelEx(&cfg, rows_kernel<T, kNW>, P);
     if (e == cudaSuccess) count_launch();
     return e;
+}
+
+// As many warps a (token, head) as keep all of them resident at once (16 a SM
+// at 128 registers, 152 SMs): a decode step is then one wave of one or two
+// rounds of loads.  us for N single tokens over 3000 rows, bf16, with 8, 4, 2
+// and 1 warps: N = 128 3.9, 4.6, 5.6, 6.6; 256 6.9, 4.8, 6.2, 6.9; 1024 22.7,
+// 16.0, 12.0, 8.6.
+template <typename T>
+cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
+    const long long most = 152 * 16 / ((long long)P.c.N * kHkv);
+    return most >= 8   ? launch_rows_nw<T, 8>(P, s)
+           : most >= 4 ? launch_rows_nw<T, 4>(P, s)
+           : most >= 2 ? launch_rows_nw<T, 2>(P, s)
+                       : launch_rows_nw<T, 1>(P, s);
 }
 
 // ------------------------------------------------- many tokens: tensor cores
@@ -652,6 +674,9 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
     return redo;
 }
 
+// A call of its own, so that the rare pass takes no registers of the common one.
+__device__ __noinline__ void one_alone(const PagedFwd& P, const Quad& Q, int only) { quad_pass<true>(P, Q, only); }
+
 __global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_constant__ PagedFwd P) {
     __shared__ int rn[SFA_MAX_RUNGS], rc[SFA_MAX_RUNGS];
     __shared__ float rt[SFA_MAX_RUNGS];
@@ -682,7 +707,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_c
     Q.rt = rt;
     if (__any_sync(kFull, lane < Q.cnt && (Q.i0 + lane < 0 || Q.i0 + lane >= P.c.cap)) && lane == 0)
         paged::report(P.c.status);
-    for (unsigned redo = quad_pass<false>(P, Q, -1); redo; redo &= redo - 1) quad_pass<true>(P, Q, __ffs(redo) - 1);
+    for (unsigned redo = quad_pass<false>(P, Q, -1); redo; redo &= redo - 1) one_alone(P, Q, __ffs(redo) - 1);
 }
 
 cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
@@ -701,15 +726,16 @@ cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
     return e;
 }
 
+constexpr int kQuadsFrom = 512;
+
 }  // namespace
 
 cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs, void* o,
                              float* lse, cudaStream_t s) {
     const PagedFwd P = {a, c, q, qs, o, lse};
-    const bool few = c.N <= 512;
-    if (dt == SFA_BF16 && !few && a.W <= 28) return launch_quads(P, s);
-    if (dt == SFA_BF16) return few ? launch_rows<__nv_bfloat16, 8>(P, s) : launch_rows<__nv_bfloat16, 1>(P, s);
-    return few ? launch_rows<float, 8>(P, s) : launch_rows<float, 1>(P, s);
+    const bool quads = dt == SFA_BF16 && a.W <= 28 && c.N >= kQuadsFrom && c.N >= 2 * c.S;
+    if (quads) return launch_quads(P, s);
+    return dt == SFA_BF16 ? launch_rows<__nv_bfloat16>(P, s) : launch_rows<float>(P, s);
 }
 
 }  // namespace sfa
