@@ -47,5 +47,24 @@ __device__ __forceinline__ void report(unsigned* status) {
     if (status) atomicOr(status, SFA_DEVSTAT_BAD_INDEX);
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;     // raise a running maximum (log2 units) past this margin
+constexpr float kFloor = -1e30f;  // running maximum before the first entry
+
+// Arguments of the attention kernels.
+struct PagedFwd {
+    LayerArgs a;
+    PagedArgs c;
+    const void* q;
+    long long qs;  // token stride of q
+    void* o;
+    float* lse;
+};
+
 }  // namespace paged
+
+// The kernel for long chunks (sfa_paged_tile.cu).
+cudaError_t launch_paged_tiles(const paged::PagedFwd& P, cudaStream_t s);
+
 }  // namespace sfa

@@ -13,26 +13,14 @@
 // (base 2), so that slots and warps meet only at the end.
 #include "sfa_mma.cuh"
 #include "sfa_paged.cuh"
+#include "sfa_paged_quad.cuh"
 
 namespace sfa {
 
 namespace {
 
 using namespace mma;
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.0f;      // raise a running maximum past this margin
-constexpr float kFloor = -1e30f;   // running maximum before the first entry
-
-struct PagedFwd {
-    LayerArgs a;
-    PagedArgs c;
-    const void* q;
-    long long qs;
-    void* o;
-    float* lse;
-};
+using namespace paged;
 
 template <typename T>
 struct Chunk;  // 8 values of a row
@@ -326,356 +314,13 @@ cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
 }
 
 // ------------------------------------------------- many tokens: tensor cores
-//
-// Quad kernel (bf16, W <= 28): a warp owns four consecutive queries of one
-// sequence and one key/value head, as two pairs of 2 queries x 4 heads, and
-// forms both products with mma.sync m16n8k16, keys on M:
-//   S^T (16 key rows x 8 columns) = K_rows . Q^T,   O^T += V_rows^T . P^T.
-// Window: rows i - W .. i + 3 of the quad's first position i are one tile that
-// both pairs share, two from W = 13 on.  Rungs: one tile a pair holds four
-// rungs, row r < 8 the far row i + e - n - 1 and row r + 8 the near row
-// i + e - n of rung r % 4 for query e = r / 4 of the pair, so both rows of an
-// interpolation sit in one thread: it mixes their scores (the interpolated
-// key's score, by linearity), and splits the probability onto the rows.
-// (Tiles of five rows a rung that both pairs share load a third less, but the
-// two rows then sit in different threads and every thread computes four
-// exponentials for three rungs instead of two for four: 1870 instructions a
-// quad instead of 1520, 63 against 56 us for 32 x 1024 tokens.)
-//
-// Rows come through the block table, so no block of rows is contiguous and no
-// tiled copy fits; the fragments are loaded straight into registers instead,
-// with no shared memory, no transpose and no barrier.  The dimensions of the
-// two products are taken in an order that keeps the loads wide:
-//   scores: k-step s of thread (row g, lane t) takes words s and 4 + s of
-//     bytes 32 t .. 32 t + 31 of the row, for keys and queries alike;
-//   values: the same loads, turned by movmatrix: words 2j and 2j + 1 make
-//     product j, whose output rows g and g + 8 are dimensions
-//     16 (g / 2) + 4 j + g % 2 and that + 2.
-// (Loading a row's chunk g for each of the four rows 2t, 2t + 1, 2t + 8,
-// 2t + 9 of the value fragment saves the turn, but eight neighbouring lanes
-// then hit two banks: 12 wavefronts a load instead of 4.)
-// Neighbouring queries read neighbouring rows, so a row comes from L2 once a
-// block and from L1 after that.
-//
-// Masked entries get probability 0.  A row that some queries of the quad read
-// is multiplied with the others' zeros, and a tile row that none reads is
-// filled with the first query's own row; infinity or NaN there would reach
-// queries that do not read it.  The epilogue looks for values that are not
-// finite and redoes those queries one at a time (kAlone), with that query's
-// rows and zeros.  Nothing of a column's arithmetic depends on another column,
-// so this gives what the first pass would have given without the others' rows,
-// bit for bit.
 
 constexpr int kQuadWarps = 4;
 
-struct Tile {
-    uint32_t k[2][8], v[2][8];  // rows g, g + 8: bytes 32 t .. 32 t + 31
-};
-
-// One query pair: the B fragments of Q^T, O^T, and of this thread's two
-// columns (query tig / 2 of the pair, heads 2 (tig & 1) and that + 1) minus
-// the running maximum (log2 units), the score that raises it, and the sum over
-// this thread's rows.
-struct Pair {
-    uint32_t qf[4][2];
-    float o[4][4];
-    float2 nm, th, l;
-};
-
-__device__ __forceinline__ float2 f2(float x, float y) { return make_float2(x, y); }
-
-__device__ __forceinline__ uint32_t word(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
-
-__device__ __forceinline__ void load32(const char* p, uint32_t (&w)[8]) {
-    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-        : "l"(p));
-}
-
-// The tile whose 16 row numbers lanes base .. base + 15 hold in `row`; in a
-// kAlone pass rows that are not there (-1) are zeros.
-template <bool kAlone>
-__device__ __forceinline__ void load_tile(const char* __restrict__ k, const char* __restrict__ v, int row, int base,
-                                          Tile& x) {
-    constexpr int kStride = kHkv * kD * 2;  // bytes of a page row
-    const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int r = __shfl_sync(kFull, row, base + 8 * h + g8);
-        if (kAlone) {
-#pragma unroll
-            for (int w = 0; w < 8; ++w) x.k[h][w] = x.v[h][w] = 0u;
-            if (r < 0) continue;
-        }
-        const size_t at = (size_t)(unsigned)r * kStride + 32 * tig;
-        load32(k + at, x.k[h]);
-        load32(v + at, x.v[h]);
-    }
-}
-
-// S^T of a tile and a pair: c[0], c[1] row g, c[2], c[3] row g + 8.
-__device__ __forceinline__ void scores(const Tile& x, const Pair& U, float (&c)[4]) {
-    mma16816_z(c, x.k[0][0], x.k[1][0], x.k[0][4], x.k[1][4], U.qf[0][0], U.qf[0][1]);
-#pragma unroll
-    for (int s = 1; s < 4; ++s)
-        mma16816(c, x.k[0][s], x.k[1][s], x.k[0][4 + s], x.k[1][4 + s], U.qf[s][0], U.qf[s][1]);
-}
-
-// The A fragments of V_rows^T, product j: words 2j and 2j + 1 of the rows, each
-// an 8 x 8 matrix turned in registers.
-__device__ __forceinline__ void value_frag(const Tile& x, int j, uint32_t (&a)[4]) {
-    a[0] = movm_t(x.v[0][2 * j]);
-    a[1] = movm_t(x.v[0][2 * j + 1]);
-    a[2] = movm_t(x.v[1][2 * j]);
-    a[3] = movm_t(x.v[1][2 * j + 1]);
-}
-
-// Largest of a column over the eight threads that hold it.
-__device__ __forceinline__ float2 column_max(float2 x) {
-#pragma unroll
-    for (int w = 4; w <= 16; w <<= 1) {
-        x.x = fmaxf(x.x, __shfl_xor_sync(kFull, x.x, w));
-        x.y = fmaxf(x.y, __shfl_xor_sync(kFull, x.y, w));
-    }
-    return x;
-}
-
-// Raise the running maximum of each column whose largest x passes the margin,
-// and rescale it.
-__device__ __forceinline__ void raise(Pair& U, float2 x) {
-    x = column_max(x);
-    const float n0 = x.x > U.th.x ? -x.x : U.nm.x, n1 = x.y > U.th.y ? -x.y : U.nm.y;
-    const float2 f = f2(fast_exp2(n0 - U.nm.x), fast_exp2(n1 - U.nm.y));
-    U.nm = f2(n0, n1);
-    U.th = f2(kLazy - n0, kLazy - n1);
-    U.l = __fmul2_rn(U.l, f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 a = __fmul2_rn(f2(U.o[j][0], U.o[j][1]), f), b = __fmul2_rn(f2(U.o[j][2], U.o[j][3]), f);
-        U.o[j][0] = a.x;
-        U.o[j][1] = a.y;
-        U.o[j][2] = b.x;
-        U.o[j][3] = b.y;
-    }
-}
-
-// Window tile.  mask: bit 2k (2k + 1) says that row g (g + 8) is in the window
-// of this thread's query of pair k.  kFirst: nothing is accumulated yet.
-template <bool kFirst>
-__device__ __forceinline__ void window_tile(const Tile& x, unsigned mask, float sl2, Pair (&U)[2]) {
-    uint32_t b[2][2];
-    const float2 sl = f2(sl2, sl2);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        float c[4];
-        scores(x, U[k], c);
-        float2 lo = __fmul2_rn(f2(c[0], c[1]), sl), hi = __fmul2_rn(f2(c[2], c[3]), sl);
-        if (!(mask >> (2 * k) & 1u)) lo = f2(-INFINITY, -INFINITY);
-        if (!(mask >> (2 * k + 1) & 1u)) hi = f2(-INFINITY, -INFINITY);
-        const float2 top = f2(fmaxf(lo.x, hi.x), fmaxf(lo.y, hi.y));
-        if (kFirst) {
-            const float2 m = column_max(top);
-            U[k].nm = f2(-fmaxf(m.x, kFloor), -fmaxf(m.y, kFloor));
-            U[k].th = f2(kLazy - U[k].nm.x, kLazy - U[k].nm.y);
-        } else if (__any_sync(kFull, top.x > U[k].th.x || top.y > U[k].th.y)) {
-            raise(U[k], top);
-        }
-        lo = __fadd2_rn(lo, U[k].nm);
-        hi = __fadd2_rn(hi, U[k].nm);
-        lo = f2(fast_exp2(lo.x), fast_exp2(lo.y));
-        hi = f2(fast_exp2(hi.x), fast_exp2(hi.y));
-        U[k].l = kFirst ? __fadd2_rn(lo, hi) : __fadd2_rn(U[k].l, __fadd2_rn(lo, hi));
-        b[k][0] = movm_t(pack_bf16(lo.x, lo.y));
-        b[k][1] = movm_t(pack_bf16(hi.x, hi.y));
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t a[4];
-        value_frag(x, j, a);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (kFirst)
-                mma16816_z(U[k].o[j], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
-            else
-                mma16816(U[k].o[j], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
-        }
-    }
-}
-
-// Rung tile of one pair.  ok: this thread's rung is an entry of its query;
-// t: the rung's fraction.
-__device__ __forceinline__ void rung_tile(const Tile& x, bool ok, float t, float sl2, Pair& U) {
-    float c[4];
-    scores(x, U, c);
-    const float u = 1.f - t;
-    const float2 tt = f2(t, t), uu = f2(u, u);
-    float2 s = __ffma2_rn(f2(t * sl2, t * sl2), f2(c[0], c[1]), __fmul2_rn(f2(u * sl2, u * sl2), f2(c[2], c[3])));
-    if (!ok) s = f2(-INFINITY, -INFINITY);
-    if (__any_sync(kFull, s.x > U.th.x || s.y > U.th.y)) raise(U, s);
-    s = __fadd2_rn(s, U.nm);
-    const float2 p = f2(fast_exp2(s.x), fast_exp2(s.y));
-    U.l = __fadd2_rn(U.l, p);
-    const float2 far_p = __fmul2_rn(p, tt), near_p = __fmul2_rn(p, uu);
-    const uint32_t b0 = movm_t(pack_bf16(far_p.x, far_p.y)), b1 = movm_t(pack_bf16(near_p.x, near_p.y));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t a[4];
-        value_frag(x, j, a);
-        mma16816(U.o[j], a[0], a[1], a[2], a[3], b0, b1);
-    }
-}
-
-struct Quad {
-    int s, t0, cnt, i0, last, g;
-    const int *rn, *rc;
-    const float* rt;
-};
-
-// All queries of the quad, or the query `only` alone; returns the queries
-// whose results are not finite (they are not written).
-template <bool kAlone>
-__device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, int only) {
-    const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
-    const int W = P.a.W, i0 = Q.i0, last = Q.last;
-    const float sl2 = P.a.scale * kLog2e;
-    const char* kb = static_cast<const char*>(P.c.k) + Q.g * (kD * 2);
-    const char* vb = static_cast<const char*>(P.c.v) + Q.g * (kD * 2);
-    // this lane's row of the window: position i0 - W + lane
-    bool want = lane < W + 4 && i0 - W + lane >= 0 && i0 - W + lane <= last && (!kAlone || (lane >= only && lane <= only + W));
-    int wrow = want ? paged::page_row(P.c, Q.s, i0 - W + lane) : -1;
-    bool bad = want && wrow < 0;
-    const int fill = kAlone ? -1 : max(__shfl_sync(kFull, wrow, W), 0);  // the first query's own row
-    // rungs that the last query uses: a prefix, four to a tile
-    const int nt = (__popc(__ballot_sync(kFull, Q.rc[lane] <= last)) + 3) >> 2;
-    // this lane's row of a rung tile: lanes 0-15 the first pair's, 16-31 the second's
-    const int my_q = 2 * (lane >> 4) + ((lane >> 2) & 1);
-    const bool near_row = lane & 8;
-    unsigned there = 0;  // rows of the tile that are there, where pages are bad
-    auto rung_rows = [&](int t) {
-        const int r = 4 * t + (lane & 3), i = i0 + my_q;
-        const bool w = i <= last && i >= Q.rc[r] && (near_row || Q.rt[r] > 0.f) && (!kAlone || my_q == only);
-        const int row = w ? paged::page_row(P.c, Q.s, i - Q.rn[r] - (near_row ? 0 : 1)) : -1;
-        bad |= w && row < 0;
-        return row;
-    };
-    Pair U[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int qt = Q.t0 + min(2 * k + (g8 >> 2), Q.cnt - 1);
-        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.q) + (size_t)qt * P.qs +
-                                                         (Q.g * kG + (g8 & 3)) * kD) + 2 * tig;
-        const uint4 a = __ldg(qp), b = __ldg(qp + 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            U[k].qf[j][0] = word(a, j);
-            U[k].qf[j][1] = word(b, j);
-        }
-    }
-    // window rows of this thread's queries
-    unsigned mask[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int R = 16 * (e >> 2) + 8 * (e & 1) + g8, d = R - 2 * ((e >> 1) & 1) - (tig >> 1);
-        if (d >= 0 && d <= W && R >= W - i0) mask[e >> 2] |= 1u << (e & 3);
-    }
-    if (__any_sync(kFull, bad)) {
-        const unsigned w = __ballot_sync(kFull, wrow >= 0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (!(w >> (16 * (e >> 2) + 8 * (e & 1) + g8) & 1u)) mask[e >> 2] &= ~(1u << (e & 3));
-    }
-    // two tiles in turn: one is loaded while the other is used
-    Tile A, B;
-    load_tile<kAlone>(kb, vb, wrow >= 0 ? wrow : fill, 0, A);
-    int row = nt > 0 ? rung_rows(0) : -1;
-    if (W > 12) {
-        load_tile<kAlone>(kb, vb, wrow >= 0 ? wrow : fill, 16, B);
-        window_tile<true>(A, mask[0], sl2, U);
-        if (nt > 0) load_tile<kAlone>(kb, vb, row >= 0 ? row : fill, 0, A);
-        window_tile<false>(B, mask[1], sl2, U);
-    } else {
-        if (nt > 0) load_tile<kAlone>(kb, vb, row >= 0 ? row : fill, 0, B);
-        window_tile<true>(A, mask[0], sl2, U);
-        A = B;
-    }
-    const int my_i = (g8 >> 2) == (tig >> 1) ? i0 + (tig >> 1) : -(1 << 30);  // its own rung's query, or none
-    for (int t = 0; t < nt; ++t) {
-        load_tile<kAlone>(kb, vb, row >= 0 ? row : fill, 16, B);
-        const bool holes = __any_sync(kFull, bad);
-        if (holes) there = __ballot_sync(kFull, row >= 0);
-        const float frac = Q.rt[4 * t + (g8 & 3)];
-        const int c = Q.rc[4 * t + (g8 & 3)];
-        bool ok[2] = {my_i >= c, my_i + 2 >= c};
-        if (holes) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                ok[k] = ok[k] && (there >> (16 * k + 8 + g8) & 1u) && ((there >> (16 * k + g8) & 1u) || frac == 0.f);
-        }
-        row = t + 1 < nt ? rung_rows(t + 1) : -1;
-        rung_tile(A, ok[0], frac, sl2, U[0]);
-        if (t + 1 < nt) load_tile<kAlone>(kb, vb, row >= 0 ? row : fill, 0, A);
-        rung_tile(B, ok[1], frac, sl2, U[1]);
-    }
-    if (__any_sync(kFull, bad) && lane == 0) paged::report(P.c.status);
-    unsigned redo = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        float2 l = U[k].l;
-#pragma unroll
-        for (int w = 4; w <= 16; w <<= 1)
-            l = __fadd2_rn(l, f2(__shfl_xor_sync(kFull, l.x, w), __shfl_xor_sync(kFull, l.y, w)));
-        const int qq = 2 * k + (tig >> 1);
-        const bool in = i0 + qq >= 0 && i0 + qq < P.c.cap;
-        if (!kAlone) {
-            float2 odd = f2(0.f, 0.f);  // stays 0 while every value is finite
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                odd = __ffma2_rn(f2(U[k].o[j][0], U[k].o[j][1]), f2(0.f, 0.f), odd);
-                odd = __ffma2_rn(f2(U[k].o[j][2], U[k].o[j][3]), f2(0.f, 0.f), odd);
-            }
-            // lanes with tig < 2 hold the pair's first query
-            const unsigned who = __ballot_sync(kFull, odd.x + odd.y != 0.f && qq < Q.cnt && in);
-            redo |= ((who & 0x33333333u ? 1u : 0u) | (who & 0xccccccccu ? 2u : 0u)) << (2 * k);
-        }
-        const bool stores = qq < Q.cnt && (kAlone ? qq == only : !(redo >> qq & 1u));
-        const unsigned who_stores = __ballot_sync(kFull, stores);
-        if (!stores) continue;
-        // l >= 2^-8 (the entry at the maximum, at most the margin below it), or 0 with no entry: zeros
-        const float2 f = f2(in && l.x != 0.f ? fast_rcp(l.x) : 0.f, in && l.y != 0.f ? fast_rcp(l.y) : 0.f);
-        const size_t at = (size_t)(Q.t0 + qq) * kHq + Q.g * kG + 2 * (tig & 1);
-        // dimensions 16 (g8 / 2) + g8 % 2 + 2 d, d = 0 .. 7, of both columns; lane ^ 4 has
-        // the others: the even one of the two takes the first eight, the odd one the last
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 a = __fmul2_rn(f2(U[k].o[j][0], U[k].o[j][1]), f), b = __fmul2_rn(f2(U[k].o[j][2], U[k].o[j][3]), f);
-            w[2 * j] = pack_bf16(a.x, a.y);
-            w[2 * j + 1] = pack_bf16(b.x, b.y);
-        }
-        const bool odd_row = g8 & 1;
-        uint32_t w0[4], w1[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const uint32_t mine = odd_row ? w[4 + d] : w[d];
-            const uint32_t got = __shfl_xor_sync(who_stores, odd_row ? w[d] : w[4 + d], 4);
-            const uint32_t even = odd_row ? got : mine, odd = odd_row ? mine : got;
-            w0[d] = __byte_perm(even, odd, 0x5410);
-            w1[d] = __byte_perm(even, odd, 0x7632);
-        }
-        uint4* o = static_cast<uint4*>(P.o) + at * (kD / 8) + g8;
-        o[0] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-        o[kD / 8] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-        if (P.lse && g8 == 0) {
-            const float y0 = l.x != 0.f ? (__log2f(l.x) - U[k].nm.x) * kLn2 : -INFINITY;
-            const float y1 = l.y != 0.f ? (__log2f(l.y) - U[k].nm.y) * kLn2 : -INFINITY;
-            *reinterpret_cast<float2*>(P.lse + at) = in ? f2(y0, y1) : f2(0.f, 0.f);
-        }
-    }
-    return redo;
-}
-
 // A call of its own, so that the rare pass takes no registers of the common one.
-__device__ __noinline__ void one_alone(const PagedFwd& P, const Quad& Q, int only) { quad_pass<true>(P, Q, only); }
+__device__ __noinline__ void one_alone(const PagedFwd& P, const Quad& Q, int only) {
+    quad_pass<true, false>(P, Q, only);
+}
 
 __global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_constant__ PagedFwd P) {
     __shared__ int rn[SFA_MAX_RUNGS], rc[SFA_MAX_RUNGS];
@@ -707,7 +352,8 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_c
     Q.rt = rt;
     if (__any_sync(kFull, lane < Q.cnt && (Q.i0 + lane < 0 || Q.i0 + lane >= P.c.cap)) && lane == 0)
         paged::report(P.c.status);
-    for (unsigned redo = quad_pass<false>(P, Q, -1); redo; redo &= redo - 1) one_alone(P, Q, __ffs(redo) - 1);
+    for (unsigned redo = quad_pass<false, false>(P, Q, -1); redo; redo &= redo - 1)
+        one_alone(P, Q, __ffs(redo) - 1);
 }
 
 cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
@@ -727,6 +373,7 @@ cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
 }
 
 constexpr int kQuadsFrom = 512;
+constexpr int kTilesFrom = 4096;
 
 }  // namespace
 
@@ -734,7 +381,7 @@ cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype d
                              float* lse, cudaStream_t s) {
     const PagedFwd P = {a, c, q, qs, o, lse};
     const bool quads = dt == SFA_BF16 && a.W <= 28 && c.N >= kQuadsFrom && c.N >= 2 * c.S;
-    if (quads) return launch_quads(P, s);
+    if (quads) return c.N >= kTilesFrom && c.N >= 28 * (long long)c.S && c.shift >= 4 ? launch_paged_tiles(P, s) : launch_quads(P, s);
     return dt == SFA_BF16 ? launch_rows<__nv_bfloat16>(P, s) : launch_rows<float>(P, s);
 }
 

@@ -1,0 +1,541 @@
+// sfa_paged_tile.cu -- attention over a paged cache for long chunks (bf16,
+// W <= 28; sfa_paged_forward in include/sfa.h): the arithmetic of
+// sfa_paged_quad.cuh with its rows in shared memory.
+//
+// A block takes tiles of 28 consecutive queries of one sequence and one
+// key/value head, a quad to each of seven warps.  The rows that a tile reads
+// are the window block, W + 28 rows, and 29 rows a rung, so a row is looked up
+// and fetched once a tile, where the quad kernel's warps each fetch their own.
+// An eighth warp does nothing else: it looks the blocks' pages up in the block
+// table and fetches the part of a block that lies in a page (pages of 16 rows
+// and more) with TMA boxes, rows of one head under the 128-byte swizzle, into a
+// ring of three stages, an item to a stage: a tile's window with its queries,
+// or four of its rungs.  Boxes are a power of two rows high; two that overlap
+// cover any other number.  A full barrier a stage counts the bytes, an empty
+// one the warps that are done with it; every wait is bounded, as in
+// sfa_ring.cuh.
+//
+// Rung p of an item starts at row 30 p of its stage, so the eight rows of an
+// ldmatrix phase (four rungs, two queries) lie in eight different phases of
+// the swizzle.  Rows that no query reads keep what the stage held before.
+//
+// Other ways to fill the ring, us for 32 x 1024 tokens in pages of 64 rows:
+// four-row gathers (tile::gather4) 59, one box of four rows a gather 55 -- a
+// TMA instruction costs some 45 cycles of its SM whatever it fetches, and a
+// tile took 153; 16-byte cp.async by all warps and a barrier an item 58 (26 M
+// instructions, a third of them copies and lookups).
+//
+// Queries whose result is not finite are kept in a list and redone from global
+// memory when the block's tiles are done (redo_query, with the score sums in
+// this kernel's order of the dimensions; a call inside the loop costs it 1 KB
+// of spills a thread).
+#include <cstring>
+
+#include "sfa_paged_quad.cuh"
+#include "sfa_ring.cuh"
+
+namespace sfa {
+
+namespace {
+
+using namespace mma;
+using paged::Pair;
+using paged::PagedFwd;
+using paged::Quad;
+using paged::kFloor;
+using paged::kLn2;
+using paged::kLog2e;
+using ring::warp_wait;
+
+constexpr int kWarps = 7, kTQ = 4 * kWarps, kThreads = 32 * (kWarps + 1);
+constexpr int kRowB = kD * 2;                   // bytes of a row of one head
+constexpr int kPitch = (kTQ + 2) * kRowB;       // from rung to rung of an item
+constexpr int kValues = 4 * kPitch + 4 * kRowB; // the values' part of a rung stage
+constexpr int kWinRows = 56;                    // rows of a window at most (W <= 28)
+constexpr int kWinValues = kWinRows * kRowB;    // the values' part of a window stage
+constexpr int kQueries = 2 * kWinValues;        // its queries: (query, head) rows
+constexpr int kQueryB = kTQ * kG * kRowB;
+constexpr int kStageB = 2 * kValues;
+constexpr int kStages = 3;
+constexpr int kRedo = 256;  // queries of a block that are not finite; past that, all of its queries are redone
+static_assert(kQueries + kQueryB <= kStageB && kQueries % 1024 == 0 && kStageB % 1024 == 0, "stage layout");
+static_assert((kPitch / kRowB) % 8 == 6, "rungs start in different swizzle phases");
+
+// A tile; cnt = 0: there is none (the end of the block's work).
+struct Work {
+    int s, g, t0, cnt, i0, last;
+    int used, groups;  // rungs that its last query uses, in groups of four
+};
+
+struct Shared {
+    unsigned char stage[kStages][kStageB];
+    unsigned char out[kWarps][8 * kRowB];  // a query pair's outputs on their way
+    unsigned long long full[kStages], empty[kStages];
+    // The tile of a window item.  The producer is at most three items ahead of
+    // a warp that is done with its tile's last item, so four places are enough.
+    Work work[4];
+    int holes[kStages];                    // an item has rows in bad pages
+    int redo[kRedo], redos;                // token rows x heads to redo alone
+    int rn[SFA_MAX_RUNGS], rc[SFA_MAX_RUNGS];
+    float rt[SFA_MAX_RUNGS];
+    int abort_flag;
+};
+
+constexpr int kHeights = 6;  // boxes of 1, 2, 4, ... 32 rows
+
+struct TileParams {
+    CUtensorMap kv[2][kHeights], q;  // keys, values
+    PagedFwd f;
+    int units;
+};
+
+// K and V rows of a tile in shared memory: the row addresses that this lane
+// gives to ldmatrix for keys and (transposed) values, swizzle folded in.
+struct SharedTile {
+    uint32_t k, v;
+};
+
+template <int kN>
+__device__ __forceinline__ void scores(const SharedTile& x, const Pair* U, float (*c)[4]) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        uint32_t a0, a1, a2, a3;
+        ldsm_x4(x.k ^ (uint32_t)(s << 5), a0, a1, a2, a3);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            if (s == 0)
+                mma16816_z(c[k], a0, a1, a2, a3, U[k].qf[0][0], U[k].qf[0][1]);
+            else
+                mma16816(c[k], a0, a1, a2, a3, U[k].qf[s][0], U[k].qf[s][1]);
+        }
+    }
+}
+__device__ __forceinline__ void value_frag(const SharedTile& x, int j, uint32_t (&a)[4]) {
+    ldsm_x4_t(x.v ^ (uint32_t)(j << 5), a[0], a[1], a[2], a[3]);
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+// Address of 16-byte chunk c of the row that starts at byte `row` of shared
+// memory (a multiple of 128) under the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(uint32_t row, int c) { return row + ((((uint32_t)c ^ (row >> 7)) & 7u) << 4); }
+
+// The tile of unit u (slot of 28 queries, head): sequence s starts at slot
+// cu[s] / 28 + s, which leaves room for ceil(tokens / 28) before the next's.
+__device__ __forceinline__ Work work_of(const PagedFwd& P, const int* rc, int u) {
+    const int lane = threadIdx.x & 31, slot = u / kHkv;
+    Work x;
+    x.g = u % kHkv;
+    x.s = paged::last_at_most(P.c.S, slot, [&](int i) { return __ldg(P.c.cu + i) / kTQ + i; });
+    const int start = __ldg(P.c.cu + x.s), end = __ldg(P.c.cu + x.s + 1);
+    x.t0 = start + kTQ * (slot - start / kTQ - x.s);
+    x.cnt = x.t0 < 0 || x.t0 >= P.c.N || x.t0 >= end ? 0 : min(kTQ, min(end, P.c.N) - x.t0);
+    x.i0 = __ldg(P.c.lens + x.s) - (end - x.t0);
+    x.last = min(x.i0 + x.cnt, P.c.cap) - 1;
+    x.used = __popc(__ballot_sync(kFull, rc[lane] <= x.last));
+    x.groups = (x.used + 3) >> 2;
+    return x;
+}
+
+// ------------------------------------------------------------- the producer
+
+// The part of a block of rows that a lane fetches: `rows` positions (0:
+// nothing) from row `row` of the pages on, to row `at` of the block.
+struct Part {
+    int row, rows, at;
+    bool bad;  // its page is
+};
+
+// Part `n` of the block whose row 0 is position `base` and of which the
+// positions lo .. hi are read: what lies in the n-th page from lo's.
+__device__ __forceinline__ Part part_of(const PagedFwd& P, int s, int base, int lo, int hi, int n) {
+    const int sh = P.c.shift, index = (max(lo, 0) >> sh) + n;
+    const int from = max(lo, index << sh), to = min(hi, ((index + 1) << sh) - 1);
+    if (from > to) return Part{0, 0, 0, false};
+    const int page = __ldg(P.c.table + (size_t)s * P.c.max_pages + index);
+    if ((unsigned)page >= (unsigned)P.c.num_pages) return Part{0, 0, 0, true};
+    return Part{(page << sh) + (from & ((1 << sh) - 1)), to - from + 1, from - base, false};
+}
+
+// Rung r's block: row j is position i0 - n - 1 + j, the far row of query j and
+// the near row of query j - 1.
+__device__ __forceinline__ Part rung_part(const PagedFwd& P, const Shared& S, const Work& x, int r, int n) {
+    const int c = r < SFA_MAX_RUNGS ? S.rc[r] : 0x7fffffff;
+    if (c > x.last) return Part{0, 0, 0, false};
+    const int back = S.rn[r] + 1, from = max(c, x.i0) + (S.rt[r] > 0.f ? 0 : 1);
+    return part_of(P, x.s, x.i0 - back, from - back, x.last + 1 - back, n);
+}
+
+__device__ void produce(const TileParams& T, Shared& S) {
+    const PagedFwd& P = T.f;
+    const int lane = threadIdx.x & 31, W = P.a.W;
+    const uint32_t stage0 = smem_u32(S.stage[0]), full0 = smem_u32(S.full), empty0 = smem_u32(S.empty);
+    int n = 0, tile = 0;  // items, tiles
+    bool ok = true;
+    auto wait = [&]() {
+        ok = warp_wait(empty0 + 8 * (n % kStages), ((n / kStages) & 1) ^ 1, &S.abort_flag);
+        return ok;
+    };
+    // The next item: every lane's part, to row 0 of its block at byte `block` of
+    // the stage; `more` bytes that lane 0 fetches besides.  The item's bytes are
+    // announced, and what goes with them published, before the first copy starts.
+    const int tensor = lane & 1;
+    auto fetch = [&](const Part& y, const Work& x, uint32_t block, uint32_t more) {
+        const uint32_t dst = stage0 + (uint32_t)(n % kStages) * kStageB, full = full0 + 8 * (n % kStages);
+        const int log = 31 - __clz(y.rows | 1), high = 1 << log;  // largest box within the part
+        const int boxes = y.rows == 0 ? 0 : y.rows > high ? 2 : 1;
+        const uint32_t bytes = __reduce_add_sync(kFull, (unsigned)(boxes * high * kRowB)) + more;
+        const bool bad = __any_sync(kFull, y.bad);
+        if (lane == 0) {
+            S.holes[n % kStages] = bad;
+            if (bad) paged::report(P.c.status);
+            mbar_arrive_expect_tx(full, bytes);
+        }
+        __syncwarp();
+        if (more && lane == 0) tma_load_3d(dst + kQueries, &T.q, 0, x.g * kG, x.t0, full);
+        const CUtensorMap* map = &T.kv[tensor][log];
+        const uint32_t to = dst + block + (uint32_t)y.at * kRowB;
+        if (boxes > 0) tma_load_2d(to, map, x.g * kD, y.row, full);
+        if (boxes > 1) tma_load_2d(to + (uint32_t)(y.rows - high) * kRowB, map, x.g * kD, y.row + y.rows - high, full);
+        ++n;
+    };
+    constexpr int kEarly = 4;  // groups that are looked up with the window
+    // Lanes (block p, part, tensor) of a group: 29 rows lie in three pages at
+    // most.  Lanes (part, tensor) of a window: 56 rows lie in five at most.
+    const int p = lane >> 3, part = (lane >> 1) & 3;
+    for (int u = blockIdx.x; ok && u < T.units; u += gridDim.x) {
+        const Work x = work_of(P, S.rc, u);
+        if (x.cnt == 0) continue;
+        const Part win = part_of(P, x.s, x.i0 - W, max(0, x.i0 - W), x.last, lane >> 1);
+        Part run[kEarly];
+#pragma unroll
+        for (int k = 0; k < kEarly; ++k) run[k] = rung_part(P, S, x, 4 * k + p, part);
+        if (lane < x.cnt && (x.i0 + lane < 0 || x.i0 + lane >= P.c.cap)) paged::report(P.c.status);
+        if (!wait()) break;
+        if (lane == 0) S.work[tile & 3] = x;
+        fetch(win, x, tensor * kWinValues, kQueryB);
+        ++tile;
+        const uint32_t block = tensor * kValues + p * kPitch;
+#pragma unroll
+        for (int k = 0; k < kEarly; ++k)
+            if (ok && k < x.groups && wait()) fetch(run[k], x, block, 0u);
+        for (int k = kEarly; k < x.groups; ++k) {
+            const Part y = rung_part(P, S, x, 4 * k + p, part);
+            if (ok && wait()) fetch(y, x, block, 0u);
+        }
+    }
+    if (ok && wait()) {  // the end
+        if (lane == 0) {
+            S.work[tile & 3].cnt = 0;
+            mbar_arrive(full0 + 8 * (n % kStages));
+        }
+        return;
+    }
+    if (lane == 0) {
+        S.abort_flag = 1;
+        if (P.c.status) atomicOr(P.c.status, SFA_DEVSTAT_WAIT_TIMEOUT);
+        // no copy of this block may land after it is gone
+        for (int i = max(0, n - kStages); i < n; ++i)
+            (void)mbar_wait(full0 + 8 * (i % kStages), (i / kStages) & 1, nullptr);
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------------ the consumers
+
+// One tile after another, until the end; false when a wait gave up.
+__device__ bool consume(const TileParams& T, Shared& S) {
+    const PagedFwd& P = T.f;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, tig = lane & 3;
+    const int W = P.a.W, u0 = 4 * warp;
+    const float sl2 = P.a.scale * kLog2e;
+    const uint32_t stage0 = smem_u32(S.stage[0]), full0 = smem_u32(S.full), empty0 = smem_u32(S.empty);
+    const uint32_t out = smem_u32(S.out[warp]);
+    // ldmatrix row of this lane: keys row (lane & 7) + 8 ((lane >> 3) & 1), half
+    // lane >> 4 of a 32-byte step; values row (lane & 7) + 8 (lane >> 4), half
+    // (lane >> 3) & 1.  Row m of a rung tile is rung m & 3, query (m >> 2) & 1,
+    // far row for m < 8.
+    const int km = (lane & 7) + (((lane >> 3) & 1) << 3), vm = (lane & 7) + ((lane >> 4) << 3);
+    const int kh = lane >> 4, vh = (lane >> 3) & 1;
+    auto rung_at = [&](int k, int np, uint32_t st) {
+        const int p = (lane & 3) < np ? (lane & 3) : 0, e = (lane >> 2) & 1, u = u0 + 2 * k;
+        auto row = [&](int j) { return st + p * kPitch + j * kRowB; };
+        return SharedTile{swizzled(row(u + e + (km >> 3)), kh), swizzled(row(u + e + (vm >> 3)) + kValues, vh)};
+    };
+    // stages start at multiples of 1024 bytes, so offsets carry the swizzle
+    const SharedTile whole[2] = {rung_at(0, 4, 0), rung_at(1, 4, 0)};
+    int n = 0;
+    for (int tile = 0;; ++tile) {
+        if (!warp_wait(full0 + 8 * (n % kStages), (n / kStages) & 1, &S.abort_flag)) return false;
+        const Work& x = S.work[tile & 3];
+        const int cnt = x.cnt, i0 = x.i0, groups = x.groups;
+        if (cnt == 0) return true;
+        const bool mine = u0 < cnt;
+        Pair U[2];
+        if (mine) {
+            const uint32_t st = stage0 + (uint32_t)(n % kStages) * kStageB;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                // column g8 of a pair is row 4 u + g8 of the queries; matrix i of the loads is chunk i
+                const uint32_t row = st + kQueries + (uint32_t)((4 * (u0 + 2 * k) + (lane & 7)) * kRowB);
+                const uint32_t at = swizzled(row, lane >> 3);
+                ldsm_x4(at, U[k].qf[0][0], U[k].qf[0][1], U[k].qf[1][0], U[k].qf[1][1]);
+                ldsm_x4(at ^ 64u, U[k].qf[2][0], U[k].qf[2][1], U[k].qf[3][0], U[k].qf[3][1]);
+            }
+            const bool holes = S.holes[n % kStages];
+#pragma unroll
+            for (int wt = 0; wt < 2; ++wt) {
+                if (wt == 1 && W <= 12) break;
+                const int kr = min(u0 + 16 * wt + km, W + kTQ - 1), vr = min(u0 + 16 * wt + vm, W + kTQ - 1);
+                const SharedTile X{swizzled(st + kr * kRowB, kh), swizzled(st + kWinValues + vr * kRowB, vh)};
+                unsigned mask = 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int R = 16 * wt + 8 * (e & 1) + g8, d = R - 2 * (e >> 1) - (tig >> 1);
+                    const int pos = i0 + u0 - W + R;
+                    if (d >= 0 && d <= W && pos >= 0 &&
+                        (!holes || (pos <= x.last && paged::page_row(P.c, x.s, pos) >= 0)))
+                        mask |= 1u << e;
+                }
+                if (wt == 0)
+                    paged::window_tile<true>(X, mask, sl2, U);
+                else
+                    paged::window_tile<false>(X, mask, sl2, U);
+            }
+        }
+        __syncwarp();
+        mbar_arrive_if(empty0 + 8 * (n % kStages), lane == 0);
+        ++n;
+        const int my_i = (g8 >> 2) == (tig >> 1) ? i0 + u0 + (tig >> 1) : -(1 << 30);
+        for (int k = 0; k < groups; ++k) {
+            if (!warp_wait(full0 + 8 * (n % kStages), (n / kStages) & 1, &S.abort_flag)) return false;
+            if (mine) {
+                const uint32_t st = stage0 + (uint32_t)(n % kStages) * kStageB;
+                const int r = 4 * k + (g8 & 3), np = x.used - 4 * k;
+                const float frac = S.rt[r];
+                const int c = S.rc[r];
+                const bool holes = S.holes[n % kStages];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    SharedTile X = whole[i];
+                    if (np < 4) X = rung_at(i, np, 0);  // absent rungs read the first one's rows, masked
+                    X.k += st;
+                    X.v += st;
+                    bool ok = my_i + 2 * i >= c;
+                    if (holes && ok) {
+                        const int pos = my_i + 2 * i - S.rn[r];
+                        ok = my_i + 2 * i <= x.last && paged::page_row(P.c, x.s, pos) >= 0 &&
+                             (frac == 0.f || paged::page_row(P.c, x.s, pos - 1) >= 0);
+                    }
+                    paged::rung_tile(X, ok, frac, sl2, U[i]);
+                }
+            }
+            __syncwarp();
+            mbar_arrive_if(empty0 + 8 * (n % kStages), lane == 0);
+            ++n;
+        }
+        if (!mine) continue;
+        unsigned redo = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float2 l = U[k].l;
+#pragma unroll
+            for (int w = 4; w <= 16; w <<= 1)
+                l = __fadd2_rn(l, make_float2(__shfl_xor_sync(kFull, l.x, w), __shfl_xor_sync(kFull, l.y, w)));
+            const int qq = u0 + 2 * k + (tig >> 1);
+            const bool in = i0 + qq >= 0 && i0 + qq < P.c.cap;
+            float2 odd = make_float2(0.f, 0.f);  // stays 0 while every value is finite
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                odd = __ffma2_rn(make_float2(U[k].o[j][0], U[k].o[j][1]), make_float2(0.f, 0.f), odd);
+                odd = __ffma2_rn(make_float2(U[k].o[j][2], U[k].o[j][3]), make_float2(0.f, 0.f), odd);
+            }
+            const unsigned who = __ballot_sync(kFull, odd.x + odd.y != 0.f && qq < cnt && in);
+            redo |= ((who & 0x33333333u ? 1u : 0u) | (who & 0xccccccccu ? 2u : 0u)) << (2 * k);
+            // l >= 2^-8 (the entry at the maximum, at most the margin below it), or 0 with no entry: zeros
+            const float2 f = make_float2(in && l.x != 0.f ? fast_rcp(l.x) : 0.f, in && l.y != 0.f ? fast_rcp(l.y) : 0.f);
+            uint32_t r[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 a = __fmul2_rn(make_float2(U[k].o[j][0], U[k].o[j][1]), f);
+                const float2 c = __fmul2_rn(make_float2(U[k].o[j][2], U[k].o[j][3]), f);
+                r[j][0] = in ? pack_bf16(a.x, a.y) : 0u;  // (a sum that is not finite would survive f = 0)
+                r[j][1] = in ? pack_bf16(c.x, c.y) : 0u;
+            }
+            // transposed into rows (query, head), then out in 16-byte pieces that cover a
+            // query's four heads
+            __syncwarp();
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+                const int row = lane & 7, mi = lane >> 3, cc = 2 * (2 * jj + (mi >> 1)) + (mi & 1);
+                stsm_x4_t(swizzled(out + row * kRowB, cc), r[2 * jj][0], r[2 * jj][1], r[2 * jj + 1][0], r[2 * jj + 1][1]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 4 * e + (lane >> 3), qe = 2 * k + e;
+                const uint4 v = ring::lds_u4(swizzled(out + row * kRowB, lane & 7));
+                if (u0 + qe < cnt && !(redo >> qe & 1u))
+                    *(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.o) +
+                                               ((size_t)(x.t0 + u0 + qe) * kHq + x.g * kG + (lane >> 3)) * kD) +
+                      (lane & 7)) = v;
+            }
+            if (P.lse && g8 == 0 && qq < cnt) {
+                const float y0 = l.x != 0.f ? (__log2f(l.x) - U[k].nm.x) * kLn2 : -INFINITY;
+                const float y1 = l.y != 0.f ? (__log2f(l.y) - U[k].nm.y) * kLn2 : -INFINITY;
+                *reinterpret_cast<float2*>(P.lse + (size_t)(x.t0 + qq) * kHq + x.g * kG + 2 * (tig & 1)) =
+                    in ? make_float2(y0, y1) : make_float2(0.f, 0.f);
+            }
+        }
+        if (lane < 4 && (redo >> lane & 1u)) {
+            const int at = atomicAdd(&S.redos, 1);
+            if (at < kRedo) S.redo[at] = (x.t0 + u0 + lane) * kHkv + x.g;
+        }
+    }
+}
+
+// Token row t alone, as the quad that it stands in computes it.
+__device__ __noinline__ void redo_query(const PagedFwd& P, const Shared& S, int t, int g) {
+    Quad Q;
+    Q.s = paged::sequence_of(P.c, t);
+    if (Q.s >= P.c.S) return;
+    const int start = __ldg(P.c.cu + Q.s), end = __ldg(P.c.cu + Q.s + 1);
+    const int only = (t - start) & 3;
+    Q.t0 = t - only;
+    Q.cnt = min(4, min(end, P.c.N) - Q.t0);
+    Q.i0 = __ldg(P.c.lens + Q.s) - (end - Q.t0);
+    Q.last = min(Q.i0 + Q.cnt, P.c.cap) - 1;
+    Q.g = g;
+    Q.rn = S.rn;
+    Q.rc = S.rc;
+    Q.rt = S.rt;
+    paged::quad_pass<true, true>(P, Q, only);
+}
+
+__global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant__ TileParams T) {
+    extern __shared__ unsigned char raw[];
+    Shared& S = *reinterpret_cast<Shared*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, warp = tid >> 5;
+    if (tid < SFA_MAX_RUNGS) {
+        const Rung r = T.f.a.r[tid];
+        S.rn[tid] = r.n;
+        S.rc[tid] = tid < T.f.a.nr ? r.c : 0x7fffffff;
+        S.rt[tid] = r.t;
+    }
+    // (finite) values for rows that are never fetched
+    for (uint32_t i = tid; i < sizeof(S.stage) / 16; i += kThreads)
+        reinterpret_cast<uint4*>(S.stage)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async();
+    if (tid == 0) {
+        S.redos = 0;
+        S.abort_flag = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&S.full[i]), 1);
+            mbar_init(smem_u32(&S.empty[i]), kWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == kWarps) {
+        produce(T, S);
+    } else if (!consume(T, S) && (tid & 31) == 0) {
+        S.abort_flag = 1;
+        if (T.f.c.status) atomicOr(T.f.c.status, SFA_DEVSTAT_WAIT_TIMEOUT);
+    }
+    __syncthreads();
+    const int redos = S.redos;
+    if (redos == 0 || S.abort_flag) return;
+    if (redos <= kRedo) {
+        for (int i = warp; i < redos; i += kWarps + 1) redo_query(T.f, S, S.redo[i] / kHkv, S.redo[i] % kHkv);
+        return;
+    }
+    for (int v = blockIdx.x; v < T.units; v += gridDim.x) {
+        const Work x = work_of(T.f, S.rc, v);
+        for (int i = warp; i < x.cnt; i += kWarps + 1) redo_query(T.f, S, x.t0 + i, x.g);
+    }
+}
+
+// Map over the pages as rows of both heads (innermost first: dimension, row),
+// box of `high` rows of one head.
+bool encode_pages(CUtensorMap* m, const void* base, long long rows, int high) {
+    auto fn = ring::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)(kHkv * kD), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(kHkv * kRowB)};
+    const cuuint32_t box[2] = {(cuuint32_t)kD, (cuuint32_t)high};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Map over the queries (innermost first: dimension, head, token), box of 4
+// heads x 28 tokens; tokens past the last are zeros.
+bool encode_queries(CUtensorMap* m, const void* base, int N, long long stride) {
+    auto fn = ring::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)kHq, (cuuint64_t)N};
+    const cuuint64_t strides[2] = {(cuuint64_t)kRowB, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)kD, (cuuint32_t)kG, (cuuint32_t)kTQ};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
+    static CtxSetting done[64];  // per device: dynamic shared memory allowed
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    constexpr size_t smem = sizeof(Shared) + 1024;
+    if (!ctx_setting_holds(done[dev & 63], smem)) {
+        e = cudaFuncSetAttribute(tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(tile_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e != cudaSuccess) return e;
+        ctx_setting_done(done[dev & 63], smem);
+    }
+    const long long units = ((long long)P.c.N / kTQ + P.c.S) * kHkv, most = 152 * 2;
+    TileParams T;
+    std::memset(&T, 0, sizeof(T));
+    T.f = P;
+    T.units = (int)units;
+    const long long rows = (long long)P.c.num_pages << P.c.shift;
+    for (int h = 0; h < kHeights; ++h)
+        if (!encode_pages(&T.kv[0][h], P.c.k, rows, 1 << h) || !encode_pages(&T.kv[1][h], P.c.v, rows, 1 << h))
+            return cudaErrorInvalidValue;
+    if (!encode_queries(&T.q, P.q, P.c.N, P.qs)) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units < most ? units : most));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tile_kernel, T);
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+}  // namespace sfa
