@@ -71,7 +71,7 @@ def _link_bind(obj: str) -> None:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BIND + f".{os.getpid()}.tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{BUILD}", "-l:libsfa.so", f"-L{lib}", "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stderr}")

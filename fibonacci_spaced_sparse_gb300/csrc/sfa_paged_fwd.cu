@@ -372,16 +372,27 @@ cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
     return e;
 }
 
+// Token rows from which the quad kernel is taken: it wins where sequences bring
+// more than a token (us, rows and quads: one chunk of 256 tokens 4.7 and 5.2,
+// of 512 6.3 and 5.4, 8 of 256 14.1 and 7.0), the rows kernel where they bring
+// one (2048 sequences 21.3 and 25.6): at least two a sequence.
 constexpr int kQuadsFrom = 512;
-constexpr int kTilesFrom = 4096;
+
+// Token rows from which the tile kernel is taken, in pages that hold 16 rows at
+// least: tiles of 28 want long chunks (us, quads and tiles: one chunk of 2048
+// tokens 6.9 and 7.3, of 4096 11.5 and 7.7, of 8192 17.7 and 12.1; 128 chunks
+// of 32 14.2 and 12.9, 256 of 16 15.1 and 15.6).
+constexpr int kTilesFrom = 4096, kTilesEach = 32;
 
 }  // namespace
 
 cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs, void* o,
                              float* lse, cudaStream_t s) {
     const PagedFwd P = {a, c, q, qs, o, lse};
-    const bool quads = dt == SFA_BF16 && a.W <= 28 && c.N >= kQuadsFrom && c.N >= 2 * c.S;
-    if (quads) return c.N >= kTilesFrom && c.N >= 28 * (long long)c.S && c.shift >= 4 ? launch_paged_tiles(P, s) : launch_quads(P, s);
+    if (dt == SFA_BF16 && a.W <= 28) {
+        if (c.N >= kTilesFrom && c.N >= kTilesEach * (long long)c.S && c.shift >= 4) return launch_paged_tiles(P, s);
+        if (c.N >= kQuadsFrom && c.N >= 2 * (long long)c.S) return launch_quads(P, s);
+    }
     return dt == SFA_BF16 ? launch_rows<__nv_bfloat16>(P, s) : launch_rows<float>(P, s);
 }
 
