@@ -94,10 +94,13 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const T*
         for (int j = 0; j < 8; ++j) acc[h][j] = 0.f;
     float m = kFloor, l = 0.f;  // of head (lane >> 1) & 3, this slot's entries
     bool bad = false;
-    for (int e0 = first; e0 < n; e0 += step) {
-        const int e = e0 + slot;
-        int ra = -1, rb = -1;
-        float wa = 1.f, wb = 0.f;
+    // row numbers and weights of entry e of the key list; ra < 0: none
+    int ra, rb;
+    float wa, wb;
+    auto entry = [&](int e) {
+        ra = rb = -1;
+        wa = 1.f;
+        wb = 0.f;
         if (e < nwin) {
             ra = paged::page_row(P.c, s, pos - e);
             bad |= ra < 0;
@@ -113,6 +116,9 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const T*
                 wb = R.t;
             }
         }
+    };
+    entry(first + slot);
+    for (int e0 = first; e0 < n; e0 += step) {
         float k[8], v[8];
         {
             Chunk<T> ka{}, va{}, kc{}, vc{};
@@ -137,6 +143,8 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const T*
                 }
             }
         }
+        const bool there = ra >= 0;
+        if (e0 + step < n) entry(e0 + step + slot);  // the next entries' pages are looked up meanwhile
         float d[kG];
 #pragma unroll
         for (int h = 0; h < kG; ++h) {
@@ -150,7 +158,7 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const T*
         float d1 = (up4 ? d[3] : d[1]) + __shfl_xor_sync(kFull, up4 ? d[1] : d[3], 4);
         float x = (up2 ? d1 : d0) + __shfl_xor_sync(kFull, up2 ? d0 : d1, 2);
         x += __shfl_xor_sync(kFull, x, 1);
-        if (ra < 0) x = -INFINITY;
+        if (!there) x = -INFINITY;
         if (__any_sync(kFull, x > m + kLazy)) {
             const float up = fmaxf(m, x);
             const float f = exp2f(m - up);

@@ -18,6 +18,8 @@ ONE = [(1, 0)]
 SINGLES = [(1, c) for c in (0, 1, 7, 8, 12, 13, 20, 21, 89, 144, 986, 987, 1300)]
 RAGGED = [(5, 0), (0, 33), (1, 21), (37, 95), (0, 0), (2, 1000), (130, 3), (1, 0)]
 CHUNK = [(203, 0)]
+# enough tokens for the kernel of long chunks (4096, and 32 a sequence)
+LONG = [(1803, 70), (0, 9), (2402, 0), (1, 1200), (33, 986)]
 MANY = [(0, 5)] * 3 + [(1, 40 + s) for s in range(40)] + [(3, 0)] * 5 + [(0, 0)] * 2
 
 
@@ -46,7 +48,7 @@ def _check(cache, got, ref, what=""):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("lens,page", [(ONE, 16), (SINGLES, 16), (SINGLES, 1), (RAGGED, 8), (RAGGED, 64), (CHUNK, 32),
-                                       (MANY, 16), (MANY, 256)])
+                                       (MANY, 16), (MANY, 256), (LONG, 16), (LONG, 64), (LONG, 8), (LONG, 2048)])
 def test_forward_against_definition(lens, page, dtype):
     cache = Cache(lens, page, dtype, seed=len(lens) + page)
     kw = dict(alpha=0.87, W=12, rungs=FIB)
@@ -63,6 +65,35 @@ def test_windows(W, dtype):
     got = _forward(cache, **kw)
     assert got[2] == 0
     _check(cache, got, attention64(cache, tensor_cores=dtype == "bf16", **kw))
+
+
+@pytest.mark.parametrize("W", [0, 1, 7, 12, 13, 28, 29])
+def test_windows_of_long_chunks(W):
+    cache = Cache([(4001, 37), (160, 0)], 32, "bf16", seed=W)
+    kw = dict(alpha=0.71, W=W, rungs=FIB)
+    got = _forward(cache, **kw)
+    assert got[2] == 0
+    _check(cache, got, attention64(cache, tensor_cores=True, **kw))
+
+
+@pytest.mark.parametrize("alpha,rungs,rounded", [(1.0, FIB, False), (0.77, FIB, True), (1.0, (), False),
+                                                 (1.1, tuple(13.0 + 0.4 * k for k in range(32)), False),
+                                                 (1.0, (30.0, 30.0, 14.25, 100.5, 31.5), False)])
+def test_rung_lists_of_long_chunks(alpha, rungs, rounded):
+    cache = Cache([(4100, 500)], 16, "bf16", seed=6)
+    kw = dict(alpha=alpha, W=12, rungs=rungs, round_offsets=rounded)
+    got = _forward(cache, **kw)
+    assert got[2] == 0
+    _check(cache, got, attention64(cache, tensor_cores=True, **kw))
+
+
+@pytest.mark.parametrize("n", [1, 2, 100, 153, 200, 310, 500, 640])
+def test_every_number_of_warps_a_token(n):
+    """Single tokens on 8, 4, 2 and 1 warps each."""
+    for dtype in ("bf16", "f32"):
+        cache = Cache([(1, (37 * s) % 400) for s in range(n)], 16, dtype, seed=n, behind=3)
+        kw = dict(alpha=0.87, W=12, rungs=FIB)
+        _check(cache, _forward(cache, **kw), attention64(cache, **kw))
 
 
 @pytest.mark.parametrize("alpha,rungs,rounded", [(1.0, FIB, False), (0.5, FIB, False), (1.5, api.pow2_base(2048), False),
@@ -110,7 +141,7 @@ def test_against_the_oracle(lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lens", [[(400, 200)], [(1, 300 + 7 * s) for s in range(20)], [(900, 0), (1, 500)]])
+@pytest.mark.parametrize("lens", [[(400, 200)], [(1, 300 + 7 * s) for s in range(20)], [(900, 0), (1, 500)], [(4200, 150)]])
 def test_bad_values_reach_only_the_queries_that_read_them(lens, dtype):
     """NaN and infinity in one key row and one value row of a sequence: the
     queries whose key lists hold the row get what the formula gives, and every
@@ -136,8 +167,25 @@ def test_bad_values_reach_only_the_queries_that_read_them(lens, dtype):
     within(torch.where(finite, o.double(), 0), torch.where(finite, want, 0), torch.from_numpy(ref[2][:used]).nan_to_num(0, 0, 0) + 1e-30)
 
 
+def test_more_bad_values_than_a_block_lists():
+    """Every fourth value row NaN and keys lists of one row: a query's output is
+    its own value row, NaN or not, in a chunk so long that a block meets more
+    queries beside a NaN row than it can list."""
+    n, page = 61000, 64
+    g = torch.Generator("cuda").manual_seed(3)
+    kp, vp = (torch.randn((n // page + 1, page, HKV, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    vp.view(-1, HKV, D)[::4, :, 11] = float("nan")
+    q = torch.randn((n, HQ, D), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.arange(n // page + 1, dtype=torch.int32, device="cuda")[None]
+    cu, seq = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [n]))
+    o, lse = api.sfa_paged_forward(q, kp, vp, table, cu, seq, alpha=1.0, W=0, rungs=())
+    own = vp.view(-1, HKV, D)[:n].repeat_interleave(HQ // HKV, 1)
+    assert torch.equal(o.isnan(), own.isnan()) and torch.equal(o.nan_to_num(9.0), own.nan_to_num(9.0))
+    assert bool(lse.isfinite().all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lens", [[(30, 70), (1, 90)], [(1, 99), (1, 40)], [(640, 60), (3, 5)]])
+@pytest.mark.parametrize("lens", [[(30, 70), (1, 90)], [(1, 99), (1, 40)], [(640, 60), (3, 5)], [(4200, 60), (3, 5)]])
 def test_bad_pages_are_left_out_and_reported(lens, dtype):
     """A page number out of range in the middle and one at the end of a
     sequence's table: entries with a row there leave the softmax, a query
@@ -155,7 +203,12 @@ def test_bad_pages_are_left_out_and_reported(lens, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_no_entry_left_gives_zeros(dtype):
-    cache = Cache([(3, 0), (600, 0)], 8, dtype, seed=16)
+    for more in (600, 4200):
+        _no_entry(dtype, more)
+
+
+def _no_entry(dtype, long):
+    cache = Cache([(3, 0), (long, 0)], 16, dtype, seed=16)
     cache.table[0, 0] = -1
     kw = dict(alpha=1.0, W=6, rungs=FIB)
     got = _forward(cache, **kw)
@@ -165,12 +218,12 @@ def test_no_entry_left_gives_zeros(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("more", [0, 700])
+@pytest.mark.parametrize("more", [0, 700, 4200])
 def test_bad_positions_give_zeros(dtype, more):
     """More new tokens than rows (negative positions), a length past the
     table's capacity, and a good sequence between them."""
-    cache = Cache([(4, 0), (20 + more, 10), (3, 60)], 8, dtype, seed=18)
-    cap = cache.max_pages * 8
+    cache = Cache([(4, 0), (20 + more, 10), (3, 60)], 16, dtype, seed=18)
+    cap = cache.max_pages * 16
     table, cu, _ = cache.meta()
     seq = torch.tensor([2, 30 + more, cap + 2], dtype=torch.int32).cuda()
     kp, vp = cache.pages()
@@ -186,8 +239,9 @@ def test_bad_positions_give_zeros(dtype, more):
     within(lse[4:end], ref[1][4:end], ref[3][4:end])
 
 
-def test_packed_queries_other_stream_and_no_lse():
-    cache = Cache(RAGGED, 16, "bf16", seed=41)
+@pytest.mark.parametrize("lens", [SINGLES, RAGGED, LONG])
+def test_packed_queries_other_stream_and_no_lse(lens):
+    cache = Cache(lens, 16, "bf16", seed=41)
     wide = torch.randn((cache.N, 12 * D)).to(torch.bfloat16).cuda()
     wide[:, :HQ * D] = cache.q.cuda().flatten(1)
     kp, vp = cache.pages()
@@ -208,7 +262,7 @@ def test_cache_rows_past_32_bits(dtype):
     """Pages whose elements lie past 2^31 (and bytes past 2^32)."""
     es = 2 if dtype == "bf16" else 4
     rows = (1 << 24) + (1 << 20)          # 128 elements a row: past 2^31 elements
-    cache = Cache([(70, 30), (1, 500), (600, 0)], 64, dtype, seed=5, num_pages=rows // 64)
+    cache = Cache([(70, 30), (1, 500), (600 if dtype == "f32" else 4100, 0)], 64, dtype, seed=5, num_pages=rows // 64)
     assert int(cache.table[0, 0]) * 64 * HKV * D > 1 << 31 and rows * HKV * D * es > 1 << 32
     kw = dict(alpha=0.87, W=12, rungs=FIB)
     got = _forward(cache, **kw)
@@ -241,7 +295,8 @@ def _append(cache, dtype, *, with_q, norm, packed, theta, k_in=None):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lens,page", [(ONE, 16), (SINGLES, 16), (SINGLES, 1), (RAGGED, 8), (CHUNK, 64), (MANY, 16)])
+@pytest.mark.parametrize("lens,page", [(ONE, 16), (SINGLES, 16), (SINGLES, 1), (RAGGED, 8), (CHUNK, 64), (MANY, 16),
+                                       (LONG, 16), (LONG + [(3900, 11), (0, 0), (5000, 0)], 64)])
 @pytest.mark.parametrize("with_q,norm,packed,theta", [(True, True, True, 1e4), (True, False, False, 1e4),
                                                       (False, True, True, 0.0), (False, False, False, 0.0)])
 def test_append_against_definition(lens, page, dtype, with_q, norm, packed, theta):
@@ -334,7 +389,7 @@ def test_serving_steps_equal_one_contiguous_pass(dtype):
             at += n
 
 
-@pytest.mark.parametrize("pad_to", [64, 900])
+@pytest.mark.parametrize("pad_to", [64, 900, 4200])
 def test_captured_step_replayed_with_other_lengths(pad_to):
     """One captured step (append, then attention) of a fixed number of token
     rows, replayed with other lengths, tables and inputs; two captured graphs
