@@ -8,22 +8,23 @@
 // and fetched once a tile, where the quad kernel's warps each fetch their own.
 // An eighth warp does nothing else: it looks the blocks' pages up in the block
 // table and fetches the part of a block that lies in a page (pages of 16 rows
-// and more) with TMA boxes, rows of one head under the 128-byte swizzle, into a
-// ring of three stages, an item to a stage: a tile's window with its queries,
-// or four of its rungs.  Boxes are a power of two rows high; two that overlap
-// cover any other number.  A full barrier a stage counts the bytes, an empty
-// one the warps that are done with it; every wait is bounded, as in
-// sfa_ring.cuh.
+// and more) with one TMA box, rows of one head under the 128-byte swizzle, into
+// a ring of three stages, an item to a stage: a tile's window with its queries,
+// or four of its rungs.  A full barrier a stage counts the bytes, an empty one
+// the warps that are done with it; every wait is bounded, as in sfa_ring.cuh.
 //
 // Rung p of an item starts at row 30 p of its stage, so the eight rows of an
 // ldmatrix phase (four rungs, two queries) lie in eight different phases of
 // the swizzle.  Rows that no query reads keep what the stage held before.
 //
 // Other ways to fill the ring, us for 32 x 1024 tokens in pages of 64 rows:
-// four-row gathers (tile::gather4) 59, one box of four rows a gather 55 -- a
-// TMA instruction costs some 45 cycles of its SM whatever it fetches, and a
-// tile took 153; 16-byte cp.async by all warps and a barrier an item 58 (26 M
-// instructions, a third of them copies and lookups).
+// four-row gathers (tile::gather4) 59, a box of four rows in each one's place 55
+// -- a TMA instruction costs some 45 cycles of its SM whatever it fetches, and
+// a tile took 153 of them; boxes of 1, 2, 4, ... 32 rows, two that overlap for
+// any other number, 37.8 (and 44.0 against 40.1 in pages of 16); a map for every
+// height, as here, 35.5, and 4 us of the host's time for the maps.  16-byte
+// cp.async by all warps with a barrier an item 58 (26 M instructions, a third of
+// them copies and lookups).  Pages of 256 rows 34.7.
 //
 // Queries whose result is not finite are kept in a list and redone from global
 // memory when the block's tiles are done (redo_query, with the score sums in
@@ -81,7 +82,7 @@ struct Shared {
     int abort_flag;
 };
 
-constexpr int kHeights = 6;  // boxes of 1, 2, 4, ... 32 rows
+constexpr int kHeights = kTQ + 1;  // boxes of 1 to 29 rows
 
 struct TileParams {
     CUtensorMap kv[2][kHeights], q;  // keys, values
@@ -196,7 +197,7 @@ __device__ void produce(const TileParams& T, Shared& S) {
     const int tensor = lane & 1;
     auto fetch = [&](const Part& y, const Work& x, uint32_t block, uint32_t more) {
         const uint32_t dst = stage0 + (uint32_t)(n % kStages) * kStageB, full = full0 + 8 * (n % kStages);
-        const int log = 31 - __clz(y.rows | 1), high = 1 << log;  // largest box within the part
+        const int high = min(max(y.rows, 1), kHeights);  // 56 rows at most: two boxes, the second may overlap
         const int boxes = y.rows == 0 ? 0 : y.rows > high ? 2 : 1;
         const uint32_t bytes = __reduce_add_sync(kFull, (unsigned)(boxes * high * kRowB)) + more;
         const bool bad = __any_sync(kFull, y.bad);
@@ -207,7 +208,7 @@ __device__ void produce(const TileParams& T, Shared& S) {
         }
         __syncwarp();
         if (more && lane == 0) tma_load_3d(dst + kQueries, &T.q, 0, x.g * kG, x.t0, full);
-        const CUtensorMap* map = &T.kv[tensor][log];
+        const CUtensorMap* map = &T.kv[tensor][high - 1];
         const uint32_t to = dst + block + (uint32_t)y.at * kRowB;
         if (boxes > 0) tma_load_2d(to, map, x.g * kD, y.row, full);
         if (boxes > 1) tma_load_2d(to + (uint32_t)(y.rows - high) * kRowB, map, x.g * kD, y.row + y.rows - high, full);
@@ -520,7 +521,7 @@ cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
     T.units = (int)units;
     const long long rows = (long long)P.c.num_pages << P.c.shift;
     for (int h = 0; h < kHeights; ++h)
-        if (!encode_pages(&T.kv[0][h], P.c.k, rows, 1 << h) || !encode_pages(&T.kv[1][h], P.c.v, rows, 1 << h))
+        if (!encode_pages(&T.kv[0][h], P.c.k, rows, h + 1) || !encode_pages(&T.kv[1][h], P.c.v, rows, h + 1))
             return cudaErrorInvalidValue;
     if (!encode_queries(&T.q, P.q, P.c.N, P.qs)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
