@@ -168,26 +168,36 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
     const float2 sl = f2(sl2, sl2);
     float c[2][4];
     scores<2>(x, U, c);
+    float2 lo[2], hi[2], top[2];
+    bool over = false;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        float2 lo = __fmul2_rn(f2(c[k][0], c[k][1]), sl), hi = __fmul2_rn(f2(c[k][2], c[k][3]), sl);
-        if (!(mask >> (2 * k) & 1u)) lo = f2(-INFINITY, -INFINITY);
-        if (!(mask >> (2 * k + 1) & 1u)) hi = f2(-INFINITY, -INFINITY);
-        const float2 top = f2(fmaxf(lo.x, hi.x), fmaxf(lo.y, hi.y));
+        lo[k] = __fmul2_rn(f2(c[k][0], c[k][1]), sl);
+        hi[k] = __fmul2_rn(f2(c[k][2], c[k][3]), sl);
+        if (!(mask >> (2 * k) & 1u)) lo[k] = f2(-INFINITY, -INFINITY);
+        if (!(mask >> (2 * k + 1) & 1u)) hi[k] = f2(-INFINITY, -INFINITY);
+        top[k] = f2(fmaxf(lo[k].x, hi[k].x), fmaxf(lo[k].y, hi[k].y));
         if (kFirst) {
-            const float2 m = column_max(top);
+            const float2 m = column_max(top[k]);
             U[k].nm = f2(-fmaxf(m.x, kFloor), -fmaxf(m.y, kFloor));
             U[k].th = f2(kLazy - U[k].nm.x, kLazy - U[k].nm.y);
-        } else if (__any_sync(kFull, top.x > U[k].th.x || top.y > U[k].th.y)) {
-            raise(U[k], top);
+        } else {
+            over = over || top[k].x > U[k].th.x || top[k].y > U[k].th.y;
         }
-        lo = __fadd2_rn(lo, U[k].nm);
-        hi = __fadd2_rn(hi, U[k].nm);
-        lo = f2(fast_exp2(lo.x), fast_exp2(lo.y));
-        hi = f2(fast_exp2(hi.x), fast_exp2(hi.y));
-        U[k].l = kFirst ? __fadd2_rn(lo, hi) : __fadd2_rn(U[k].l, __fadd2_rn(lo, hi));
-        b[k][0] = movm_t(pack_bf16(lo.x, lo.y));
-        b[k][1] = movm_t(pack_bf16(hi.x, hi.y));
+    }
+    if (!kFirst && __any_sync(kFull, over)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) raise(U[k], top[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        lo[k] = __fadd2_rn(lo[k], U[k].nm);
+        hi[k] = __fadd2_rn(hi[k], U[k].nm);
+        lo[k] = f2(fast_exp2(lo[k].x), fast_exp2(lo[k].y));
+        hi[k] = f2(fast_exp2(hi[k].x), fast_exp2(hi[k].y));
+        U[k].l = kFirst ? __fadd2_rn(lo[k], hi[k]) : __fadd2_rn(U[k].l, __fadd2_rn(lo[k], hi[k]));
+        b[k][0] = movm_t(pack_bf16(lo[k].x, lo[k].y));
+        b[k][1] = movm_t(pack_bf16(hi[k].x, hi[k].y));
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -203,29 +213,45 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
     }
 }
 
-// Rung tile of one pair.  ok: this thread's rung is an entry of its query;
-// t: the rung's fraction.
-template <class X>
-__device__ __forceinline__ void rung_tile(const X& x, bool ok, float t, float sl2, Pair& U) {
-    float cc[1][4];
-    scores<1>(x, &U, cc);
-    const float(&c)[4] = cc[0];
-    const float u = 1.f - t;
-    const float2 tt = f2(t, t), uu = f2(u, u);
-    float2 s = __ffma2_rn(f2(t * sl2, t * sl2), f2(c[0], c[1]), __fmul2_rn(f2(u * sl2, u * sl2), f2(c[2], c[3])));
-    if (!ok) s = f2(-INFINITY, -INFINITY);
-    if (__any_sync(kFull, s.x > U.th.x || s.y > U.th.y)) raise(U, s);
-    s = __fadd2_rn(s, U.nm);
-    const float2 p = f2(fast_exp2(s.x), fast_exp2(s.y));
-    U.l = __fadd2_rn(U.l, p);
-    const float2 far_p = __fmul2_rn(p, tt), near_p = __fmul2_rn(p, uu);
-    const uint32_t b0 = movm_t(pack_bf16(far_p.x, far_p.y)), b1 = movm_t(pack_bf16(near_p.x, near_p.y));
+// Rung tiles of kN pairs.  ok: this thread's rung is an entry of its query; t:
+// the rung's fraction.
+template <int kN, class X>
+__device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, float sl2, Pair* U) {
+    float c[kN][1][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t a[4];
-        value_frag(x, j, a);
-        mma16816(U.o[j], a[0], a[1], a[2], a[3], b0, b1);
+    for (int k = 0; k < kN; ++k) scores<1>(x[k], U + k, c[k]);
+    const float u = 1.f - t;
+    const float2 tt = f2(t, t), uu = f2(u, u), ts = f2(t * sl2, t * sl2), us = f2(u * sl2, u * sl2);
+    float2 s[kN];
+    bool over = false;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+        s[k] = __ffma2_rn(ts, f2(c[k][0][0], c[k][0][1]), __fmul2_rn(us, f2(c[k][0][2], c[k][0][3])));
+        if (!ok[k]) s[k] = f2(-INFINITY, -INFINITY);
+        over = over || s[k].x > U[k].th.x || s[k].y > U[k].th.y;
     }
+    if (__any_sync(kFull, over)) {
+#pragma unroll
+        for (int k = 0; k < kN; ++k) raise(U[k], s[k]);
+    }
+    uint32_t b[kN][2];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+        s[k] = __fadd2_rn(s[k], U[k].nm);
+        const float2 p = f2(fast_exp2(s[k].x), fast_exp2(s[k].y));
+        U[k].l = __fadd2_rn(U[k].l, p);
+        const float2 far_p = __fmul2_rn(p, tt), near_p = __fmul2_rn(p, uu);
+        b[k][0] = movm_t(pack_bf16(far_p.x, far_p.y));
+        b[k][1] = movm_t(pack_bf16(near_p.x, near_p.y));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            uint32_t a[4];
+            value_frag(x[k], j, a);
+            mma16816(U[k].o[j], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
+        }
 }
 
 struct Quad {
@@ -327,9 +353,9 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
                 ok[k] = ok[k] && (there >> (16 * k + 8 + g8) & 1u) && ((there >> (16 * k + g8) & 1u) || frac == 0.f);
         }
         row = t + 1 < nt ? rung_rows(t + 1) : -1;
-        rung_tile(A, ok[0], frac, sl2, U[0]);
+        rung_tiles<1>(&A, ok, frac, sl2, U);
         if (t + 1 < nt) load_tile<kAlone, kNatural>(kb, vb, row >= 0 ? row : fill, 0, A);
-        rung_tile(B, ok[1], frac, sl2, U[1]);
+        rung_tiles<1>(&B, ok + 1, frac, sl2, U + 1);
     }
     if (__any_sync(kFull, bad) && lane == 0) paged::report(P.c.status);
     unsigned redo = 0;

@@ -330,20 +330,22 @@ __device__ bool consume(const TileParams& T, Shared& S) {
                 const float frac = S.rt[r];
                 const int c = S.rc[r];
                 const bool holes = S.holes[n % kStages];
+                SharedTile X[2];
+                bool ok[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    SharedTile X = whole[i];
-                    if (np < 4) X = rung_at(i, np, 0);  // absent rungs read the first one's rows, masked
-                    X.k += st;
-                    X.v += st;
-                    bool ok = my_i + 2 * i >= c;
-                    if (holes && ok) {
+                    X[i] = whole[i];
+                    if (np < 4) X[i] = rung_at(i, np, 0);  // absent rungs read the first one's rows, masked
+                    X[i].k += st;
+                    X[i].v += st;
+                    ok[i] = my_i + 2 * i >= c;
+                    if (holes && ok[i]) {
                         const int pos = my_i + 2 * i - S.rn[r];
-                        ok = my_i + 2 * i <= x.last && paged::page_row(P.c, x.s, pos) >= 0 &&
-                             (frac == 0.f || paged::page_row(P.c, x.s, pos - 1) >= 0);
+                        ok[i] = my_i + 2 * i <= x.last && paged::page_row(P.c, x.s, pos) >= 0 &&
+                                (frac == 0.f || paged::page_row(P.c, x.s, pos - 1) >= 0);
                     }
-                    paged::rung_tile(X, ok, frac, sl2, U[i]);
                 }
+                paged::rung_tiles<2>(X, ok, frac, sl2, U);
             }
             __syncwarp();
             mbar_arrive_if(empty0 + 8 * (n % kStages), lane == 0);
