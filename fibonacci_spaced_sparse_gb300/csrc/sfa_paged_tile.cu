@@ -3,7 +3,8 @@
 // sfa_paged_quad.cuh with its rows in shared memory.
 //
 // A block takes tiles of 28 consecutive queries of one sequence and one
-// key/value head, a quad to each of seven warps.  The rows that a tile reads
+// key/value head, a quad to each of seven warps, the heads one after the other
+// (they read the same rows, so a slot of 28 queries is looked up once).  The rows that a tile reads
 // are the window block, W + 28 rows, and 29 rows a rung, so a row is looked up
 // and fetched once a tile, where the quad kernel's warps each fetch their own.
 // An eighth warp does nothing else: it looks the blocks' pages up in the block
@@ -87,7 +88,7 @@ constexpr int kHeights = kTQ + 1;  // boxes of 1 to 29 rows
 struct TileParams {
     CUtensorMap kv[2][kHeights], q;  // keys, values
     PagedFwd f;
-    int units;
+    int slots;
 };
 
 // K and V rows of a tile in shared memory: the row addresses that this lane
@@ -135,12 +136,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 // memory (a multiple of 128) under the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(uint32_t row, int c) { return row + ((((uint32_t)c ^ (row >> 7)) & 7u) << 4); }
 
-// The tile of unit u (slot of 28 queries, head): sequence s starts at slot
+// The first head's tile of a slot of 28 queries: sequence s starts at slot
 // cu[s] / 28 + s, which leaves room for ceil(tokens / 28) before the next's.
-__device__ __forceinline__ Work work_of(const PagedFwd& P, const int* rc, int u) {
-    const int lane = threadIdx.x & 31, slot = u / kHkv;
+__device__ __forceinline__ Work work_of(const PagedFwd& P, const int* rc, int slot) {
+    const int lane = threadIdx.x & 31;
     Work x;
-    x.g = u % kHkv;
+    x.g = 0;
     x.s = paged::last_at_most(P.c.S, slot, [&](int i) { return __ldg(P.c.cu + i) / kTQ + i; });
     const int start = __ldg(P.c.cu + x.s), end = __ldg(P.c.cu + x.s + 1);
     x.t0 = start + kTQ * (slot - start / kTQ - x.s);
@@ -214,30 +215,50 @@ __device__ void produce(const TileParams& T, Shared& S) {
         if (boxes > 1) tma_load_2d(to + (uint32_t)(y.rows - high) * kRowB, map, x.g * kD, y.row + y.rows - high, full);
         ++n;
     };
-    constexpr int kEarly = 4;  // groups that are looked up with the window
-    // Lanes (block p, part, tensor) of a group: 29 rows lie in three pages at
-    // most.  Lanes (part, tensor) of a window: 56 rows lie in five at most.
+    // What is fetched for a tile: lanes (part, tensor) of its window, 56 rows and
+    // five pages at most; lanes (block p, part, tensor) of its groups, 29 rows
+    // and three pages at most.  The first groups are looked up with the window.
+    constexpr int kEarly = 4;
     const int p = lane >> 3, part = (lane >> 1) & 3;
-    for (int u = blockIdx.x; ok && u < T.units; u += gridDim.x) {
-        const Work x = work_of(P, S.rc, u);
-        if (x.cnt == 0) continue;
-        const Part win = part_of(P, x.s, x.i0 - W, max(0, x.i0 - W), x.last, lane >> 1);
-        Part run[kEarly];
+    struct Plan {
+        Work x;
+        Part win, run[kEarly];
+    };
+    int slot = blockIdx.x;
+    auto plan = [&]() {
+        Plan y;
+        y.x.cnt = 0;
+        for (; slot < T.slots && y.x.cnt == 0; slot += gridDim.x) y.x = work_of(P, S.rc, slot);
+        if (y.x.cnt == 0) return y;
+        y.win = part_of(P, y.x.s, y.x.i0 - W, max(0, y.x.i0 - W), y.x.last, lane >> 1);
 #pragma unroll
-        for (int k = 0; k < kEarly; ++k) run[k] = rung_part(P, S, x, 4 * k + p, part);
-        if (lane < x.cnt && (x.i0 + lane < 0 || x.i0 + lane >= P.c.cap)) paged::report(P.c.status);
-        if (!wait()) break;
-        if (lane == 0) S.work[tile & 3] = x;
-        fetch(win, x, tensor * kWinValues, kQueryB);
-        ++tile;
-        const uint32_t block = tensor * kValues + p * kPitch;
+        for (int k = 0; k < kEarly; ++k) y.run[k] = rung_part(P, S, y.x, 4 * k + p, part);
+        if (lane < y.x.cnt && (y.x.i0 + lane < 0 || y.x.i0 + lane >= P.c.cap)) paged::report(P.c.status);
+        return y;
+    };
+    const uint32_t block = tensor * kValues + p * kPitch;
+    Plan y = plan(), z;
+    while (ok && y.x.cnt > 0) {
+        // the heads' tiles read the same rows
+        for (int g = 0; ok && g < kHkv; ++g) {
+            Work x = y.x;
+            x.g = g;
+            if (!wait()) break;
+            if (lane == 0) S.work[tile & 3] = x;
+            fetch(y.win, x, tensor * kWinValues, kQueryB);
+            ++tile;
+            if (x.groups > 0 && wait()) fetch(y.run[0], x, block, 0u);
+            // the next slot is looked up while the warps have these items to work on
+            if (g == kHkv - 1) z = plan();
 #pragma unroll
-        for (int k = 0; k < kEarly; ++k)
-            if (ok && k < x.groups && wait()) fetch(run[k], x, block, 0u);
-        for (int k = kEarly; k < x.groups; ++k) {
-            const Part y = rung_part(P, S, x, 4 * k + p, part);
-            if (ok && wait()) fetch(y, x, block, 0u);
+            for (int k = 1; k < kEarly; ++k)
+                if (ok && k < x.groups && wait()) fetch(y.run[k], x, block, 0u);
+            for (int k = kEarly; k < x.groups; ++k) {
+                const Part more = rung_part(P, S, x, 4 * k + p, part);
+                if (ok && wait()) fetch(more, x, block, 0u);
+            }
         }
+        y = z;
     }
     if (ok && wait()) {  // the end
         if (lane == 0) {
@@ -468,9 +489,9 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
         for (int i = warp; i < redos; i += kWarps + 1) redo_query(T.f, S, S.redo[i] / kHkv, S.redo[i] % kHkv);
         return;
     }
-    for (int v = blockIdx.x; v < T.units; v += gridDim.x) {
+    for (int v = blockIdx.x; v < T.slots; v += gridDim.x) {
         const Work x = work_of(T.f, S.rc, v);
-        for (int i = warp; i < x.cnt; i += kWarps + 1) redo_query(T.f, S, x.t0 + i, x.g);
+        for (int i = warp; i < x.cnt * kHkv; i += kWarps + 1) redo_query(T.f, S, x.t0 + i / kHkv, i % kHkv);
     }
 }
 
@@ -516,18 +537,18 @@ cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         ctx_setting_done(done[dev & 63], smem);
     }
-    const long long units = ((long long)P.c.N / kTQ + P.c.S) * kHkv, most = 152 * 2;
+    const long long slots = (long long)P.c.N / kTQ + P.c.S, most = 152 * 2;
     TileParams T;
     std::memset(&T, 0, sizeof(T));
     T.f = P;
-    T.units = (int)units;
+    T.slots = (int)slots;
     const long long rows = (long long)P.c.num_pages << P.c.shift;
     for (int h = 0; h < kHeights; ++h)
         if (!encode_pages(&T.kv[0][h], P.c.k, rows, h + 1) || !encode_pages(&T.kv[1][h], P.c.v, rows, h + 1))
             return cudaErrorInvalidValue;
     if (!encode_queries(&T.q, P.q, P.c.N, P.qs)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units < most ? units : most));
+    cfg.gridDim = dim3((unsigned)(slots < most ? slots : most));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
