@@ -22,10 +22,16 @@
 // four-row gathers (tile::gather4) 59, a box of four rows in each one's place 55
 // -- a TMA instruction costs some 45 cycles of its SM whatever it fetches, and
 // a tile took 153 of them; boxes of 1, 2, 4, ... 32 rows, two that overlap for
-// any other number, 37.8 (and 44.0 against 40.1 in pages of 16); a map for every
-// height, as here, 35.5, and 4 us of the host's time for the maps.  16-byte
-// cp.async by all warps with a barrier an item 58 (26 M instructions, a third of
-// them copies and lookups).  Pages of 256 rows 34.7.
+// any other number, 37.8 (44.0 in pages of 16); a map for every height, as here,
+// 35.2 (39.9), and 3 us of the host's time for the maps.  Looking a slot up for
+// both heads at once 34.4 (36.9), and the epilogue below, with both pairs
+// staged at once and fixed addresses, 31.9 (35.1; pages of 256 rows 31.2).
+// 16-byte cp.async by all warps with a barrier an item took 58 (26 M
+// instructions, a third of them copies and lookups).
+//
+// What bounds it: with the warps' arithmetic left out it takes 21 us (the ring's
+// latency: three stages a block, two blocks a SM), and the arithmetic, 1000
+// instructions a quad at 16 warps a SM, hides that only in part.
 //
 // Queries whose result is not finite are kept in a list and redone from global
 // memory when the block's tiles are done (redo_query, with the score sums in
@@ -71,7 +77,7 @@ struct Work {
 
 struct Shared {
     unsigned char stage[kStages][kStageB];
-    unsigned char out[kWarps][8 * kRowB];  // a query pair's outputs on their way
+    unsigned char out[kWarps][16 * kRowB];  // a quad's outputs on their way
     unsigned long long full[kStages], empty[kStages];
     // The tile of a window item.  The producer is at most three items ahead of
     // a warp that is done with its tile's last item, so four places are enough.
@@ -286,148 +292,179 @@ __device__ bool consume(const TileParams& T, Shared& S) {
     const int W = P.a.W, u0 = 4 * warp;
     const float sl2 = P.a.scale * kLog2e;
     const uint32_t stage0 = smem_u32(S.stage[0]), full0 = smem_u32(S.full), empty0 = smem_u32(S.empty);
-    const uint32_t out = smem_u32(S.out[warp]);
     // ldmatrix row of this lane: keys row (lane & 7) + 8 ((lane >> 3) & 1), half
     // lane >> 4 of a 32-byte step; values row (lane & 7) + 8 (lane >> 4), half
     // (lane >> 3) & 1.  Row m of a rung tile is rung m & 3, query (m >> 2) & 1,
-    // far row for m < 8.
+    // far row for m < 8.  Stages start at multiples of 1024 bytes, so offsets in
+    // a stage carry the swizzle.
     const int km = (lane & 7) + (((lane >> 3) & 1) << 3), vm = (lane & 7) + ((lane >> 4) << 3);
     const int kh = lane >> 4, vh = (lane >> 3) & 1;
-    auto rung_at = [&](int k, int np, uint32_t st) {
+    auto rung_at = [&](int k, int np) {
         const int p = (lane & 3) < np ? (lane & 3) : 0, e = (lane >> 2) & 1, u = u0 + 2 * k;
-        auto row = [&](int j) { return st + p * kPitch + j * kRowB; };
+        auto row = [&](int j) { return (uint32_t)(p * kPitch + j * kRowB); };
         return SharedTile{swizzled(row(u + e + (km >> 3)), kh), swizzled(row(u + e + (vm >> 3)) + kValues, vh)};
     };
-    // stages start at multiples of 1024 bytes, so offsets carry the swizzle
-    const SharedTile whole[2] = {rung_at(0, 4, 0), rung_at(1, 4, 0)};
-    int n = 0;
-    for (int tile = 0;; ++tile) {
-        if (!warp_wait(full0 + 8 * (n % kStages), (n / kStages) & 1, &S.abort_flag)) return false;
+    auto window_at = [&](int wt) {
+        const uint32_t kr = min(u0 + 16 * wt + km, W + kTQ - 1), vr = min(u0 + 16 * wt + vm, W + kTQ - 1);
+        return SharedTile{swizzled(kr * kRowB, kh), swizzled(kWinValues + vr * kRowB, vh)};
+    };
+    // bit e: row 16 wt + 8 (e & 1) + g8 of the window is at a distance 0 .. W of
+    // this thread's query of pair e / 2
+    auto window_mask = [&](int wt, auto there) {
+        unsigned m = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int R = 16 * wt + 8 * (e & 1) + g8, d = R - 2 * (e >> 1) - (tig >> 1);
+            if (d >= 0 && d <= W && there(R)) m |= 1u << e;
+        }
+        return m;
+    };
+    const SharedTile whole[2] = {rung_at(0, 4), rung_at(1, 4)}, first = window_at(0);
+    const unsigned mask0 = window_mask(0, [](int) { return true; });
+    // outputs: stmatrix rows of this lane in the staging buffer, its 16-byte piece
+    // of query row 8 k + 4 e + lane / 8 there
+    const uint32_t out = smem_u32(S.out[warp]);
+    const int mi = lane >> 3;
+    const uint32_t put = swizzled(out + (lane & 7) * kRowB, mi);           // chunks mi and 4 + mi
+    const uint32_t get = swizzled(out + (lane >> 3) * kRowB, lane & 7);    // row lane / 8; row + 4: chunk ^ 4
+    int st_index = 0, phase = 0, tile = 0;
+    auto done_with_stage = [&]() {
+        __syncwarp();
+        mbar_arrive_if(empty0 + 8 * st_index, lane == 0);
+        if (++st_index == kStages) {
+            st_index = 0;
+            phase ^= 1;
+        }
+    };
+    for (;; ++tile) {
+        if (!warp_wait(full0 + 8 * st_index, phase, &S.abort_flag)) return false;
         const Work& x = S.work[tile & 3];
         const int cnt = x.cnt, i0 = x.i0, groups = x.groups;
         if (cnt == 0) return true;
         const bool mine = u0 < cnt;
         Pair U[2];
         if (mine) {
-            const uint32_t st = stage0 + (uint32_t)(n % kStages) * kStageB;
+            const uint32_t st = stage0 + (uint32_t)st_index * kStageB;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 // column g8 of a pair is row 4 u + g8 of the queries; matrix i of the loads is chunk i
-                const uint32_t row = st + kQueries + (uint32_t)((4 * (u0 + 2 * k) + (lane & 7)) * kRowB);
-                const uint32_t at = swizzled(row, lane >> 3);
+                const uint32_t at = swizzled(st + kQueries + (uint32_t)((4 * (u0 + 2 * k) + (lane & 7)) * kRowB), mi);
                 ldsm_x4(at, U[k].qf[0][0], U[k].qf[0][1], U[k].qf[1][0], U[k].qf[1][1]);
                 ldsm_x4(at ^ 64u, U[k].qf[2][0], U[k].qf[2][1], U[k].qf[3][0], U[k].qf[3][1]);
             }
-            const bool holes = S.holes[n % kStages];
-#pragma unroll
-            for (int wt = 0; wt < 2; ++wt) {
-                if (wt == 1 && W <= 12) break;
-                const int kr = min(u0 + 16 * wt + km, W + kTQ - 1), vr = min(u0 + 16 * wt + vm, W + kTQ - 1);
-                const SharedTile X{swizzled(st + kr * kRowB, kh), swizzled(st + kWinValues + vr * kRowB, vh)};
-                unsigned mask = 0u;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int R = 16 * wt + 8 * (e & 1) + g8, d = R - 2 * (e >> 1) - (tig >> 1);
-                    const int pos = i0 + u0 - W + R;
-                    if (d >= 0 && d <= W && pos >= 0 &&
-                        (!holes || (pos <= x.last && paged::page_row(P.c, x.s, pos) >= 0)))
-                        mask |= 1u << e;
-                }
-                if (wt == 0)
-                    paged::window_tile<true>(X, mask, sl2, U);
-                else
-                    paged::window_tile<false>(X, mask, sl2, U);
+            const bool holes = S.holes[st_index];
+            const int lo = W - i0 - u0;  // rows before it lie before the sequence
+            auto there = [&](int R) {
+                if (R < lo) return false;
+                const int pos = R - lo;
+                return !holes || (pos <= x.last && paged::page_row(P.c, x.s, pos) >= 0);
+            };
+            const unsigned m = lo > 0 || holes ? window_mask(0, there) : mask0;
+            paged::window_tile<true>(SharedTile{first.k + st, first.v + st}, m, sl2, U);
+            if (W > 12) {
+                const SharedTile X = window_at(1);
+                paged::window_tile<false>(SharedTile{X.k + st, X.v + st}, window_mask(1, there), sl2, U);
             }
         }
-        __syncwarp();
-        mbar_arrive_if(empty0 + 8 * (n % kStages), lane == 0);
-        ++n;
+        done_with_stage();
         const int my_i = (g8 >> 2) == (tig >> 1) ? i0 + u0 + (tig >> 1) : -(1 << 30);
         for (int k = 0; k < groups; ++k) {
-            if (!warp_wait(full0 + 8 * (n % kStages), (n / kStages) & 1, &S.abort_flag)) return false;
+            if (!warp_wait(full0 + 8 * st_index, phase, &S.abort_flag)) return false;
             if (mine) {
-                const uint32_t st = stage0 + (uint32_t)(n % kStages) * kStageB;
+                const uint32_t st = stage0 + (uint32_t)st_index * kStageB;
                 const int r = 4 * k + (g8 & 3), np = x.used - 4 * k;
                 const float frac = S.rt[r];
                 const int c = S.rc[r];
-                const bool holes = S.holes[n % kStages];
-                SharedTile X[2];
-                bool ok[2];
+                bool ok[2] = {my_i >= c, my_i + 2 >= c};
+                if (S.holes[st_index]) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    X[i] = whole[i];
-                    if (np < 4) X[i] = rung_at(i, np, 0);  // absent rungs read the first one's rows, masked
-                    X[i].k += st;
-                    X[i].v += st;
-                    ok[i] = my_i + 2 * i >= c;
-                    if (holes && ok[i]) {
+                    for (int i = 0; i < 2; ++i) {
                         const int pos = my_i + 2 * i - S.rn[r];
-                        ok[i] = my_i + 2 * i <= x.last && paged::page_row(P.c, x.s, pos) >= 0 &&
+                        ok[i] = ok[i] && my_i + 2 * i <= x.last && paged::page_row(P.c, x.s, pos) >= 0 &&
                                 (frac == 0.f || paged::page_row(P.c, x.s, pos - 1) >= 0);
                     }
                 }
+                SharedTile X[2] = {whole[0], whole[1]};
+                if (np < 4) {  // absent rungs read the first one's rows, masked
+                    X[0] = rung_at(0, np);
+                    X[1] = rung_at(1, np);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    X[i].k += st;
+                    X[i].v += st;
+                }
                 paged::rung_tiles<2>(X, ok, frac, sl2, U);
             }
-            __syncwarp();
-            mbar_arrive_if(empty0 + 8 * (n % kStages), lane == 0);
-            ++n;
+            done_with_stage();
         }
         if (!mine) continue;
+        // positions that are out of range
+        const int live = min(4, cnt - u0), i1 = i0 + u0;
+        unsigned out_of = 0u;
+        if (i1 < 0 || i1 + live > P.c.cap)
+            for (int e = 0; e < 4; ++e) out_of |= (i1 + e < 0 || i1 + e >= P.c.cap ? 1u : 0u) << e;
         unsigned redo = 0;
+        float2 l[2] = {U[0].l, U[1].l}, f[2];
+#pragma unroll
+        for (int w = 4; w <= 16; w <<= 1)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                l[k] = __fadd2_rn(l[k], make_float2(__shfl_xor_sync(kFull, l[k].x, w), __shfl_xor_sync(kFull, l[k].y, w)));
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float2 l = U[k].l;
-#pragma unroll
-            for (int w = 4; w <= 16; w <<= 1)
-                l = __fadd2_rn(l, make_float2(__shfl_xor_sync(kFull, l.x, w), __shfl_xor_sync(kFull, l.y, w)));
-            const int qq = u0 + 2 * k + (tig >> 1);
-            const bool in = i0 + qq >= 0 && i0 + qq < P.c.cap;
             float2 odd = make_float2(0.f, 0.f);  // stays 0 while every value is finite
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 odd = __ffma2_rn(make_float2(U[k].o[j][0], U[k].o[j][1]), make_float2(0.f, 0.f), odd);
                 odd = __ffma2_rn(make_float2(U[k].o[j][2], U[k].o[j][3]), make_float2(0.f, 0.f), odd);
             }
-            const unsigned who = __ballot_sync(kFull, odd.x + odd.y != 0.f && qq < cnt && in);
+            const unsigned who = __ballot_sync(kFull, odd.x + odd.y != 0.f);
             redo |= ((who & 0x33333333u ? 1u : 0u) | (who & 0xccccccccu ? 2u : 0u)) << (2 * k);
             // l >= 2^-8 (the entry at the maximum, at most the margin below it), or 0 with no entry: zeros
-            const float2 f = make_float2(in && l.x != 0.f ? fast_rcp(l.x) : 0.f, in && l.y != 0.f ? fast_rcp(l.y) : 0.f);
+            f[k] = make_float2(l[k].x != 0.f ? fast_rcp(l[k].x) : 0.f, l[k].y != 0.f ? fast_rcp(l[k].y) : 0.f);
+        }
+        redo &= (1u << live) - 1u & ~out_of;
+        // transposed into rows (query, head), then out in 16-byte pieces that cover a
+        // query's four heads
+        __syncwarp();  // the tile before has been read
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
             uint32_t r[4][2];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 a = __fmul2_rn(make_float2(U[k].o[j][0], U[k].o[j][1]), f);
-                const float2 c = __fmul2_rn(make_float2(U[k].o[j][2], U[k].o[j][3]), f);
-                r[j][0] = in ? pack_bf16(a.x, a.y) : 0u;  // (a sum that is not finite would survive f = 0)
-                r[j][1] = in ? pack_bf16(c.x, c.y) : 0u;
+                const float2 a = __fmul2_rn(make_float2(U[k].o[j][0], U[k].o[j][1]), f[k]);
+                const float2 c = __fmul2_rn(make_float2(U[k].o[j][2], U[k].o[j][3]), f[k]);
+                r[j][0] = pack_bf16(a.x, a.y);
+                r[j][1] = pack_bf16(c.x, c.y);
             }
-            // transposed into rows (query, head), then out in 16-byte pieces that cover a
-            // query's four heads
-            __syncwarp();
+            if (out_of >> (2 * k + (tig >> 1)) & 1u) {  // zeros (a sum that is not finite would survive f = 0)
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                const int row = lane & 7, mi = lane >> 3, cc = 2 * (2 * jj + (mi >> 1)) + (mi & 1);
-                stsm_x4_t(swizzled(out + row * kRowB, cc), r[2 * jj][0], r[2 * jj][1], r[2 * jj + 1][0], r[2 * jj + 1][1]);
+                for (int j = 0; j < 4; ++j) r[j][0] = r[j][1] = 0u;
             }
-            __syncwarp();
+            stsm_x4_t(put + k * 8 * kRowB, r[0][0], r[0][1], r[1][0], r[1][1]);
+            stsm_x4_t((put ^ 64u) + k * 8 * kRowB, r[2][0], r[2][1], r[3][0], r[3][1]);
+        }
+        __syncwarp();
+        const size_t at = (size_t)(x.t0 + u0) * kHq + x.g * kG;
+        uint4* o = reinterpret_cast<uint4*>(P.o) + (at + (lane >> 3)) * (kD / 8) + (lane & 7);
+        const unsigned write = (1u << live) - 1u & ~redo;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = 4 * e + (lane >> 3), qe = 2 * k + e;
-                const uint4 v = ring::lds_u4(swizzled(out + row * kRowB, lane & 7));
-                if (u0 + qe < cnt && !(redo >> qe & 1u))
-                    *(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.o) +
-                                               ((size_t)(x.t0 + u0 + qe) * kHq + x.g * kG + (lane >> 3)) * kD) +
-                      (lane & 7)) = v;
-            }
-            if (P.lse && g8 == 0 && qq < cnt) {
-                const float y0 = l.x != 0.f ? (__log2f(l.x) - U[k].nm.x) * kLn2 : -INFINITY;
-                const float y1 = l.y != 0.f ? (__log2f(l.y) - U[k].nm.y) * kLn2 : -INFINITY;
-                *reinterpret_cast<float2*>(P.lse + (size_t)(x.t0 + qq) * kHq + x.g * kG + 2 * (tig & 1)) =
-                    in ? make_float2(y0, y1) : make_float2(0.f, 0.f);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const uint4 v = ring::lds_u4((get ^ (e & 1 ? 64u : 0u)) + e * 4 * kRowB);
+            if (write >> e & 1u) o[e * (kHq * kD / 8)] = v;
+        }
+        if (P.lse && g8 < 2) {  // lanes g8 = k: queries of pair k
+            const float2 s = g8 == 0 ? l[0] : l[1], nm = g8 == 0 ? U[0].nm : U[1].nm;
+            const int e = 2 * g8 + (tig >> 1);
+            float2 v = make_float2(s.x != 0.f ? (__log2f(s.x) - nm.x) * kLn2 : -INFINITY,
+                                   s.y != 0.f ? (__log2f(s.y) - nm.y) * kLn2 : -INFINITY);
+            if (out_of >> e & 1u) v = make_float2(0.f, 0.f);
+            if (e < live) *reinterpret_cast<float2*>(P.lse + at + e * kHq + 2 * (tig & 1)) = v;
         }
         if (lane < 4 && (redo >> lane & 1u)) {
-            const int at = atomicAdd(&S.redos, 1);
-            if (at < kRedo) S.redo[at] = (x.t0 + u0 + lane) * kHkv + x.g;
+            const int i = atomicAdd(&S.redos, 1);
+            if (i < kRedo) S.redo[i] = (x.t0 + u0 + lane) * kHkv + x.g;
         }
     }
 }
