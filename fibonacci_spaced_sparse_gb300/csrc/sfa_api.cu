@@ -206,7 +206,7 @@ sfa_status check_norm(const sfa_params* p, const void* Q, long long q_stride, co
         return SFA_ERR_INVALID_ARG;
     if (!aligned4(positions) || !aligned4(status)) return SFA_ERR_INVALID_ARG;
     if (p->rope_theta > 0.f) {
-        if (!rope_table || !aligned16(rope_table) || table_rows < 0 || table_rows > kMaxT) return SFA_ERR_INVALID_ARG;
+        if (!rope_table || !aligned16(rope_table) || table_rows < 1 || table_rows > kMaxT) return SFA_ERR_INVALID_ARG;
         if (!positions && table_rows < p->T) return SFA_ERR_INVALID_ARG;
     }
     std::memset(a, 0, sizeof(*a));
@@ -603,7 +603,8 @@ SFA_API sfa_status sfa_paged_forward(const sfa_params* p, const sfa_paged* c, co
     if (p->B == 0 || c->N == 0) return SFA_OK;
     sfa::PagedArgs a;
     if ((st = check_paged(p, c, status, &a)) != SFA_OK) return st;
-    if (!rows_ok(p, Q, q_stride, p->Hq) || !O || !aligned16(O) || !aligned4(lse)) return SFA_ERR_INVALID_ARG;
+    if (!rows_ok(p, Q, q_stride, p->Hq) || !O || !aligned16(O) || (reinterpret_cast<uintptr_t>(lse) & 7u))
+        return SFA_ERR_INVALID_ARG;
     LayerArgs l;
     fill_args(p, &l);
     if (sfa::fault_injected()) return SFA_ERR_CUDA;

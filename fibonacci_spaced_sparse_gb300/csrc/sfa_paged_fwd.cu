@@ -397,7 +397,9 @@ constexpr int kTilesFrom = 4096, kTilesEach = 32;
 cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs, void* o,
                              float* lse, cudaStream_t s) {
     const PagedFwd P = {a, c, q, qs, o, lse};
-    if (dt == SFA_BF16 && a.W <= 28) {
+    // the tensor-core kernels load 32 bytes of a row at a time
+    const bool wide = ((reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) & 31u) == 0;
+    if (dt == SFA_BF16 && a.W <= 28 && wide) {
         if (c.N >= kTilesFrom && c.N >= kTilesEach * (long long)c.S && c.shift >= 4) return launch_paged_tiles(P, s);
         if (c.N >= kQuadsFrom && c.N >= 2 * (long long)c.S) return launch_quads(P, s);
     }

@@ -369,8 +369,8 @@ SFA_API sfa_status sfa_backward(const sfa_params *p, const void *Q, const void *
  *     outside [0, table_rows) reads no table row, writes zeros to that
  *     token's outputs and sets SFA_DEVSTAT_BAD_INDEX in *status; not read
  *     without a rotation;
- *   rope_table: table_rows positions (from sfa_rope_table; at least T of them
- *     when positions is NULL);
+ *   rope_table: table_rows >= 1 positions (from sfa_rope_table; at least T of
+ *     them when positions is NULL);
  *   Qhat, Khat: [B][T][Hq][D] and [B][T][Hkv][D], contiguous; status: device
  *     word or NULL.
  * One launch; allocates nothing.  Asynchronous on stream. */
@@ -464,14 +464,14 @@ SFA_API sfa_status sfa_paged_append(const sfa_params *p, const sfa_paged *c, con
  *     used; rope_theta must be <= 0: Q is already rotated, as sfa_paged_append
  *     leaves it;
  *   Q [N][Hq][D] with a token stride as above; O [N][Hq][D] and lse [N][Hq]
- *     (or NULL), contiguous.
+ *     (8-byte aligned, or NULL), contiguous.
  * A token with a bad position gets zeros in O and lse.  An entry of a token's
  * key list with a row in a bad page is left out of its softmax; a token with
  * no entry left gets zeros in O and minus infinity in lse.  Rows outside a
  * token's key list never reach its output, whatever they hold.
- * One launch (bf16 with many tokens and W <= 28: tensor cores, fp32
- * accumulation, probabilities rounded to bf16 for the value product; else
- * fp32 arithmetic); allocates nothing.  Asynchronous on stream. */
+ * One launch (bf16 with many tokens, W <= 28 and pages aligned to 32 bytes:
+ * tensor cores, fp32 accumulation, probabilities rounded to bf16 for the value
+ * product; else fp32 arithmetic); allocates nothing.  Asynchronous on stream. */
 SFA_API sfa_status sfa_paged_forward(const sfa_params *p, const sfa_paged *c, const void *Q,
                                      long long q_stride, void *O, float *lse,
                                      unsigned int *status, cudaStream_t stream);

@@ -257,6 +257,31 @@ def test_packed_queries_other_stream_and_no_lse(lens):
     assert none is None and torch.equal(got[:used], want[:used])
 
 
+@pytest.mark.parametrize("lens", [SINGLES, [(700, 20)], LONG])
+def test_pages_16_bytes_off(lens):
+    """Pages that start 16 bytes past a 32-byte boundary (any fp32-arithmetic
+    path: the tensor-core kernels load 32 bytes at a time), packed queries and
+    outputs that start 16 bytes off too."""
+    cache = Cache(lens, 16, "bf16", seed=44)
+    kp, vp = cache.pages()
+
+    def off(t):
+        room = torch.zeros(t.numel() + 8, dtype=t.dtype, device="cuda")
+        room[8:] = t.flatten()
+        return room[8:].view(t.shape)
+
+    kw = dict(alpha=0.87, W=12, rungs=FIB)
+    o, lse = api.sfa_paged_forward(off(cache.q.cuda()), off(kp), off(vp), *cache.meta(), out=off(torch.full_like(cache.q, 7).cuda()),
+                                   lse=torch.full((cache.N, HQ), 7.0, device="cuda"), **kw)
+    _check(cache, (o, lse), attention64(cache, **kw))
+    new = [torch.randn((cache.N, HKV, D), device="cuda").to(torch.bfloat16) for _ in range(2)]
+    both = [(kp.clone(), vp.clone()), (off(kp), off(vp))]
+    for k_pages, v_pages in both:
+        api.sfa_paged_append(*(off(x) for x in new), k_pages, v_pages, *cache.meta())
+    for a, b in zip(*both):
+        assert torch.equal(a.nan_to_num(5.0), b.nan_to_num(5.0))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_cache_rows_past_32_bits(dtype):
     """Pages whose elements lie past 2^31 (and bytes past 2^32)."""

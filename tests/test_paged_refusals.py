@@ -68,7 +68,7 @@ def test_norm_refusals(lib, call):
     assert call(lib, qs=511) == BAD and call(lib, qs=516) == BAD      # inside a row; not a multiple of 16 bytes
     assert call(lib, ks=64) == BAD
     assert call(lib, rows=63) == BAD                                  # a table shorter than the sequence
-    assert call(lib, rows=-1, pos=FAKE) == BAD
+    assert call(lib, rows=-1, pos=FAKE) == BAD and call(lib, rows=0, pos=FAKE) == BAD
     assert call(lib, pos=FAKE + 2) == BAD
 
 
@@ -126,7 +126,7 @@ def test_forward_refusals(lib):
     c = _cache()
     assert _fwd(lib, c, p=_p()) == BAD                                # unrotated queries
     assert _fwd(lib, c, o=NULL) == BAD and _fwd(lib, c, o=FAKE + 4) == BAD
-    assert _fwd(lib, c, lse=FAKE + 2) == BAD and _fwd(lib, c, status=FAKE + 1) == BAD
+    assert _fwd(lib, c, lse=FAKE + 2) == BAD and _fwd(lib, c, lse=FAKE + 4) == BAD and _fwd(lib, c, status=FAKE + 1) == BAD
     assert _fwd(lib, c, p=_p(rope_theta=0.0, W=-1)) == BAD
     assert _fwd(lib, c, p=_p(rope_theta=0.0, alpha=0.0)) == BAD
 
@@ -141,7 +141,7 @@ empty = t._p(B=0)
 print(json.dumps([t._norm(lib), t._norm_bwd(lib), t._norm_bwd(lib, p=empty), t._append(lib, t._cache()),
                   t._append(lib, t._cache(), q=None, qh=None, wq=None, wk=None), t._fwd(lib, t._cache()),
                   t._fwd(lib, t._cache(), p=t._p(B=1 << 20, T=1 << 24, rope_theta=0.0)),
-                  t._norm(lib, rows=0, pos=t.FAKE), t._norm(lib, p=t._p(rope_theta=0.0), tab=None, rows=0)]))
+                  t._norm(lib, rows=1, pos=t.FAKE), t._norm(lib, p=t._p(rope_theta=0.0), tab=None, rows=0)]))
 print(json.dumps([t._norm(lib, q=None), t._append(lib, t._cache(k_pages=None)), t._fwd(lib, t._cache(N=0))]))
 """
 
