@@ -106,6 +106,7 @@ def launch_count() -> int:
 # ------------------------------------------------------------- RoPE table --
 
 _rope_cache: dict = {}
+_rope_outgrown: list = []  # captured graphs may still read them; at most as large together as the last one
 
 
 def rope_table(T: int, device, D: int = 64, rope_theta: float = 1e4, stream=None) -> torch.Tensor:
@@ -124,6 +125,8 @@ def rope_table(T: int, device, D: int = 64, rope_theta: float = 1e4, stream=None
         _lib.check(st, "sfa_rope_table")
         # the table is shared by later calls on any stream: finish building it
         (stream if stream is not None else torch.cuda.current_stream(device)).synchronize()
+        if key in _rope_cache:
+            _rope_outgrown.append(_rope_cache[key])
         _rope_cache[key] = tab
     return tab
 

@@ -244,3 +244,21 @@ def test_autograd_takes_broadcast_gradients():
     one = torch.ones_like(qh)
     want = api.sfa_qk_norm_rope_backward(q.detach(), k.detach(), wq.detach(), wk, one, torch.zeros_like(kh))
     assert torch.equal(q.grad, want[0]) and torch.equal(wq.grad, want[2]) and bool((k.grad == 0).all())
+
+
+def test_captured_call_outlives_a_grown_table():
+    """A graph captured with the shared RoPE table, replayed after the table has
+    grown and the memory it might have left has been written over."""
+    theta = 12345.0  # a table of its own
+    q, k, wq, wk, _ = _draw(2, 40, "bf16", False, seed=31)
+    want = api.sfa_qk_norm_rope(q, k, wq, wk, rope_theta=theta)
+    rows = api.rope_table(1, "cuda", rope_theta=theta).shape[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = api.sfa_qk_norm_rope(q, k, wq, wk, rope_theta=theta)
+    grown = api.rope_table(rows + 1, "cuda", rope_theta=theta)
+    assert grown.shape[0] > rows
+    junk = [torch.full((rows, 32, 2), float("nan"), device="cuda") for _ in range(8)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want)) and len(junk) == 8
