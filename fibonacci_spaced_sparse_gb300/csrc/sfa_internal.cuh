@@ -110,46 +110,6 @@ cudaError_t launch_qkv_rope(int M, int T, int dm, const void* x, const void* w, 
 
 cudaError_t launch_wait_selftest(unsigned* status, cudaStream_t s);
 
-// Norm with rotation (sfa_norm.cu).  Token strides in elements.
-struct NormArgs {
-    int N, T;              // tokens; tokens per sequence (position = index % T)
-    int table_rows;
-    float eps;
-    long long qs, ks;      // token strides
-    const void *q, *k;
-    const float *wq, *wk;
-    const int* positions;  // nullptr: the index in the sequence
-    const float2* rope;    // nullptr: no rotation
-    unsigned* status;
-};
-cudaError_t launch_norm_fwd(const NormArgs& a, sfa_dtype dt, void* qhat, void* khat, cudaStream_t s);
-size_t norm_bwd_workspace();
-cudaError_t launch_norm_bwd(const NormArgs& a, sfa_dtype dt, const void* dqhat, const void* dkhat, void* dq, void* dk,
-                            float* dwq, float* dwk, void* ws, cudaStream_t s);
-
-// A paged cache and one step's tokens (sfa_paged in sfa.h).
-struct PagedArgs {
-    void *k, *v;
-    const int *table, *cu, *lens;
-    unsigned* status;
-    int S, N;
-    int max_pages, num_pages;
-    int shift;             // log2 of the page size
-    int cap;               // positions [0, cap) exist
-};
-struct AppendArgs {
-    PagedArgs c;
-    const void *q, *kn, *vn;  // new queries (nullptr: none), keys, values
-    long long qs, ks, vs;     // token strides in elements
-    const float *wq, *wk;     // nullptr: no norm
-    const float2* rope;       // nullptr: no rotation
-    void* qhat;
-    float eps;
-};
-cudaError_t launch_paged_append(const AppendArgs& a, sfa_dtype dt, cudaStream_t s);
-cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs, void* o,
-                             float* lse, cudaStream_t s);
-
 size_t bwd_simple_workspace(const LayerArgs& a);
 cudaError_t launch_bwd_simple(const LayerArgs& a, sfa_dtype dt, const void* q, const void* k,
                               const void* v, const void* o, const void* dO, const float* lse,

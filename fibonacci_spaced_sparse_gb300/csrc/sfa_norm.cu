@@ -13,6 +13,7 @@
 // position are read once for two rows.  Packed fp32 arithmetic and one
 // approximate root a row keep the instructions well below the memory time.
 #include "sfa_heads.cuh"
+#include "sfa_ops.cuh"
 
 namespace sfa {
 

@@ -4,7 +4,7 @@
 // an error bit and never to an access out of range.  Private to the library.
 #pragma once
 
-#include "sfa_internal.cuh"
+#include "sfa_ops.cuh"
 
 namespace sfa {
 namespace paged {
