@@ -388,9 +388,12 @@ constexpr int kQuadsFrom = 512;
 
 // Token rows from which the tile kernel is taken, in pages that hold 16 rows at
 // least: tiles of 28 want long chunks (us, quads and tiles: one chunk of 2048
-// tokens 6.9 and 7.3, of 4096 11.5 and 7.7, of 8192 17.7 and 12.1; 128 chunks
-// of 32 14.2 and 12.9, 256 of 16 15.1 and 15.6).
-constexpr int kTilesFrom = 4096, kTilesEach = 32;
+// tokens 7.0 and 6.8, of 3500 7.1 and 6.9, of 4096 11.6 and 7.1, of 8192 17.9
+// and 10.6 -- below the quads' second wave the tiles' maps cost the host more
+// than they save; 128 chunks of 32 14.2 and 11.2, 300 of 24 25.2 and 21.7, 256
+// of 16 15.2 and 15.5; 8 chunks of 512 beside 56 single tokens 13.2 and 11.4,
+// beside 192 13.4 and 17.1).
+constexpr int kTilesFrom = 3200, kTilesEach = 28;
 
 }  // namespace
 

@@ -65,7 +65,8 @@ constexpr int kQueries = 2 * kWinValues;        // its queries: (query, head) ro
 constexpr int kQueryB = kTQ * kG * kRowB;
 constexpr int kStageB = 2 * kValues;
 constexpr int kStages = 3;
-constexpr int kRedo = 256;  // queries of a block that are not finite; past that, all of its queries are redone
+constexpr int kRedo = 256;  // queries of a block that are not finite (at least a slot's); past that, all of its queries are redone
+static_assert(kRedo >= kTQ, "a block with one tile never runs over");
 static_assert(kQueries + kQueryB <= kStageB && kQueries % 1024 == 0 && kStageB % 1024 == 0, "stage layout");
 static_assert((kPitch / kRowB) % 8 == 6, "rungs start in different swizzle phases");
 
@@ -95,6 +96,7 @@ struct TileParams {
     CUtensorMap kv[2][kHeights], q;  // keys, values
     PagedFwd f;
     int slots;
+    bool split;  // a block takes one head only
 };
 
 // K and V rows of a tile in shared memory: the row addresses that this lane
@@ -230,11 +232,13 @@ __device__ void produce(const TileParams& T, Shared& S) {
         Work x;
         Part win, run[kEarly];
     };
-    int slot = blockIdx.x;
+    const int g0 = T.split ? blockIdx.x % kHkv : 0, g1 = T.split ? g0 + 1 : kHkv;
+    int slot = T.split ? blockIdx.x / kHkv : blockIdx.x;
+    const int step = T.split ? gridDim.x / kHkv : gridDim.x;
     auto plan = [&]() {
         Plan y;
         y.x.cnt = 0;
-        for (; slot < T.slots && y.x.cnt == 0; slot += gridDim.x) y.x = work_of(P, S.rc, slot);
+        for (; slot < T.slots && y.x.cnt == 0; slot += step) y.x = work_of(P, S.rc, slot);
         if (y.x.cnt == 0) return y;
         y.win = part_of(P, y.x.s, y.x.i0 - W, max(0, y.x.i0 - W), y.x.last, lane >> 1);
 #pragma unroll
@@ -246,7 +250,7 @@ __device__ void produce(const TileParams& T, Shared& S) {
     Plan y = plan(), z;
     while (ok && y.x.cnt > 0) {
         // the heads' tiles read the same rows
-        for (int g = 0; ok && g < kHkv; ++g) {
+        for (int g = g0; ok && g < g1; ++g) {
             Work x = y.x;
             x.g = g;
             if (!wait()) break;
@@ -255,7 +259,7 @@ __device__ void produce(const TileParams& T, Shared& S) {
             ++tile;
             if (x.groups > 0 && wait()) fetch(y.run[0], x, block, 0u);
             // the next slot is looked up while the warps have these items to work on
-            if (g == kHkv - 1) z = plan();
+            if (g == g1 - 1) z = plan();
 #pragma unroll
             for (int k = 1; k < kEarly; ++k)
                 if (ok && k < x.groups && wait()) fetch(y.run[k], x, block, 0u);
@@ -526,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
         for (int i = warp; i < redos; i += kWarps + 1) redo_query(T.f, S, S.redo[i] / kHkv, S.redo[i] % kHkv);
         return;
     }
+    // more than the list holds: only a block that goes through many slots, both heads of each
     for (int v = blockIdx.x; v < T.slots; v += gridDim.x) {
         const Work x = work_of(T.f, S.rc, v);
         for (int i = warp; i < x.cnt * kHkv; i += kWarps + 1) redo_query(T.f, S, x.t0 + i / kHkv, i % kHkv);
@@ -579,13 +584,14 @@ cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
     std::memset(&T, 0, sizeof(T));
     T.f = P;
     T.slots = (int)slots;
+    T.split = slots * kHkv <= most;  // fewer slots than blocks: the heads side by side
     const long long rows = (long long)P.c.num_pages << P.c.shift;
     for (int h = 0; h < kHeights; ++h)
         if (!encode_pages(&T.kv[0][h], P.c.k, rows, h + 1) || !encode_pages(&T.kv[1][h], P.c.v, rows, h + 1))
             return cudaErrorInvalidValue;
     if (!encode_queries(&T.q, P.q, P.c.N, P.qs)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(slots < most ? slots : most));
+    cfg.gridDim = dim3((unsigned)(T.split ? slots * kHkv : slots < most ? slots : most));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;

@@ -18,7 +18,7 @@ ONE = [(1, 0)]
 SINGLES = [(1, c) for c in (0, 1, 7, 8, 12, 13, 20, 21, 89, 144, 986, 987, 1300)]
 RAGGED = [(5, 0), (0, 33), (1, 21), (37, 95), (0, 0), (2, 1000), (130, 3), (1, 0)]
 CHUNK = [(203, 0)]
-# enough tokens for the kernel of long chunks (4096, and 32 a sequence)
+# enough tokens for the kernel of long chunks (3200, and 28 a sequence)
 LONG = [(1803, 70), (0, 9), (2402, 0), (1, 1200), (33, 986)]
 MANY = [(0, 5)] * 3 + [(1, 40 + s) for s in range(40)] + [(3, 0)] * 5 + [(0, 0)] * 2
 
