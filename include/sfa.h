@@ -50,9 +50,9 @@
  * process) every entry point that would launch work or read the status word
  * checks its arguments as usual and then returns SFA_ERR_CUDA without
  * launching, so that a caller's error handling can be exercised without
- * faulting a GPU.  Calls with nothing to launch (B * T = 0) still return
- * SFA_OK, except sfa_backward, which then still zeroes dalpha and dtheta and
- * so fails too.
+ * faulting a GPU.  Calls with nothing to launch (B * T = 0, no token rows) still
+ * return SFA_OK, except sfa_backward and sfa_qk_norm_rope_backward, which then
+ * still zero dalpha and dtheta (dwq and dwk) and so fail too.
  */
 #ifndef SFA_H
 #define SFA_H
