@@ -486,7 +486,9 @@ class SparseAttention(torch.autograd.Function):
 class QKNormRope(torch.autograd.Function):
     """Autograd wrapper of sfa_qk_norm_rope: (qhat, khat) = norm and rotation of
     (q, k) with the weights wq, wk (fp32 [64]).  SparseAttention with
-    rope_theta=0 takes the results."""
+    rope_theta=0 takes the results.  Forward and backward can be captured into a
+    CUDA graph once no eager graph of the same leaves is alive any more (torch's
+    own rule: the leaves' accumulation would run on the eager graph's stream)."""
 
     @staticmethod
     def forward(ctx, q, k, wq, wk, eps=1e-6, rope_theta=1e4, positions=None, rope=None):

@@ -47,10 +47,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     // the sequence of the warp's first token, then forward to this lane's
     int s = paged::sequence_of(a.c, warp_t);
     if (s >= a.c.S) return;  // it lies behind the last sequence, and so do the others
-    int end = __ldg(a.c.cu + s + 1);
-    while (end <= tt && s + 1 < a.c.S) end = __ldg(a.c.cu + ++s + 1);
+    int end = fresh(a.c.cu + s + 1);
+    while (end <= tt && s + 1 < a.c.S) end = fresh(a.c.cu + ++s + 1);
     if (!in_n || tt >= end) return;
-    const int pos = __ldg(a.c.lens + s) - (end - tt);
+    const int pos = fresh(a.c.lens + s) - (end - tt);
     const bool good = pos >= 0 && pos < a.c.cap;
     if (!good && c == 0 && role == kKey) paged::report(a.c.status);
     T* dst;

@@ -8,7 +8,7 @@
 // shuffles, and a bf16 row is two 16-byte loads a lane.
 #pragma once
 
-#include "sfa_internal.cuh"
+#include "sfa_ops.cuh"
 
 namespace sfa {
 namespace heads {
@@ -37,15 +37,15 @@ struct Raw<float> {
 
 __device__ __forceinline__ void fetch(const __nv_bfloat16* row, int c, Raw<__nv_bfloat16>& r) {
     const uint4* p = reinterpret_cast<const uint4*>(row);
-    r.x = __ldg(p + c);
-    r.y = __ldg(p + 4 + c);
+    r.x = fresh(p + c);
+    r.y = fresh(p + 4 + c);
 }
 __device__ __forceinline__ void fetch(const float* row, int c, Raw<float>& r) {
     const float4* p = reinterpret_cast<const float4*>(row);
-    r.x0 = __ldg(p + 2 * c);
-    r.x1 = __ldg(p + 2 * c + 1);
-    r.y0 = __ldg(p + 8 + 2 * c);
-    r.y1 = __ldg(p + 9 + 2 * c);
+    r.x0 = fresh(p + 2 * c);
+    r.x1 = fresh(p + 2 * c + 1);
+    r.y0 = fresh(p + 8 + 2 * c);
+    r.y1 = fresh(p + 9 + 2 * c);
 }
 
 __device__ __forceinline__ void put(__nv_bfloat16* row, int c, const Raw<__nv_bfloat16>& r) {
@@ -164,12 +164,12 @@ __device__ __forceinline__ Row weights(const float* w, int c) {
 struct Angles {
     float2 c[kP], s[kP];
 };
-__device__ __forceinline__ Angles angles(const float2* __restrict__ rope, int pos, int c) {
+__device__ __forceinline__ Angles angles(const float2* rope, int pos, int c) {
     const float4* p = reinterpret_cast<const float4*>(rope + (size_t)pos * kPairs + 8 * c);
     Angles a;
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
-        const float4 v = __ldg(p + j);
+        const float4 v = fresh(p + j);
         a.c[j] = make_float2(v.x, v.z);
         a.s[j] = make_float2(v.y, v.w);
     }

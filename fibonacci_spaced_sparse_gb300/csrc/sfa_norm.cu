@@ -28,7 +28,7 @@ constexpr int kThreads = kTok * kPairsOfHeads * 4;
 // Position of token t; -1 when it lies outside the table.
 __device__ __forceinline__ int position(const NormArgs& a, int t) {
     if (!a.rope) return 0;
-    const int pos = a.positions ? __ldg(a.positions + t) : t % a.T;
+    const int pos = a.positions ? fresh(a.positions + t) : t % a.T;
     return pos >= 0 && pos < a.table_rows ? pos : -1;
 }
 
@@ -63,8 +63,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, Row& x, const Row& w
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) norm_fwd_kernel(const NormArgs a, T* __restrict__ qhat,
-                                                               T* __restrict__ khat) {
+__global__ void __launch_bounds__(kThreads, 4) norm_fwd_kernel(const NormArgs a, T* qhat, T* khat) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int quad = threadIdx.x >> 2, c = threadIdx.x & 3, hp = quad % kPairsOfHeads;
@@ -100,7 +99,7 @@ constexpr int kPipedBlocks = 152 * 3;
 constexpr size_t kPipedSmem = (size_t)kAhead * kSlots * kThreads * sizeof(uint4);
 
 __global__ void __launch_bounds__(kThreads, 3)
-    norm_fwd_piped_kernel(const NormArgs a, __nv_bfloat16* __restrict__ qhat, __nv_bfloat16* __restrict__ khat) {
+    norm_fwd_piped_kernel(const NormArgs a, __nv_bfloat16* qhat, __nv_bfloat16* khat) {
     using T = __nv_bfloat16;
     extern __shared__ uint4 slots[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -165,8 +164,7 @@ constexpr int kPartial = 2 * kD;     // floats of one: dwq, dwk
 // 48 us in fp32.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks<T> / 152)
-    norm_bwd_kernel(const NormArgs a, const T* __restrict__ dqhat, const T* __restrict__ dkhat, T* __restrict__ dq,
-                    T* __restrict__ dk, float* __restrict__ partial) {
+    norm_bwd_kernel(const NormArgs a, const T* dqhat, const T* dkhat, T* dq, T* dk, float* partial) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float sums[kTok * kPairsOfHeads][kD + 1];
@@ -242,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks<T> / 152)
 // dwq, dwk: the sum of the blocks' parts.  A block sums kFinCols columns,
 // kFinRows threads a column, each with all of its loads in flight at once.
 constexpr int kFinCols = 8, kFinRows = 64, kFinEach = (kMaxBlocks + kFinRows - 1) / kFinRows;
-__global__ void __launch_bounds__(kFinCols* kFinRows) norm_dw_kernel(const float* __restrict__ partial, int blocks,
-                                                                     float* __restrict__ dwq, float* __restrict__ dwk) {
+__global__ void __launch_bounds__(kFinCols* kFinRows) norm_dw_kernel(const float* partial, int blocks, float* dwq,
+                                                                     float* dwk) {
     __shared__ float sums[kFinRows / 4][kFinCols + 1];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -253,7 +251,7 @@ __global__ void __launch_bounds__(kFinCols* kFinRows) norm_dw_kernel(const float
 #pragma unroll
     for (int i = 0; i < kFinEach; ++i) {
         const int b = row + i * kFinRows;
-        part[i] = b < blocks ? __ldg(partial + (size_t)b * kPartial + d) : 0.f;
+        part[i] = b < blocks ? fresh(partial + (size_t)b * kPartial + d) : 0.f;
     }
     float s = 0.f;
 #pragma unroll

@@ -31,15 +31,15 @@ __device__ __forceinline__ int last_at_most(int n, int x, F first) {
 // whole warp asks for the same t).  A step in which every sequence brings one
 // token is found at once.
 __device__ __forceinline__ int sequence_of(const PagedArgs& c, int t) {
-    if (t < c.S && __ldg(c.cu + t) == t && __ldg(c.cu + t + 1) == t + 1) return t;
-    const int s = last_at_most(c.S, t, [&](int i) { return __ldg(c.cu + i); });
-    return __ldg(c.cu + s) <= t && t < __ldg(c.cu + s + 1) ? s : c.S;
+    if (t < c.S && fresh(c.cu + t) == t && fresh(c.cu + t + 1) == t + 1) return t;
+    const int s = last_at_most(c.S, t, [&](int i) { return fresh(c.cu + i); });
+    return fresh(c.cu + s) <= t && t < fresh(c.cu + s + 1) ? s : c.S;
 }
 
 // Row of the pages that holds position pos >= 0 of sequence s; -1 for a page
 // number out of range.  pos < c.cap.
 __device__ __forceinline__ int page_row(const PagedArgs& c, int s, int pos) {
-    const int page = __ldg(c.table + (size_t)s * c.max_pages + (pos >> c.shift));
+    const int page = fresh(c.table + (size_t)s * c.max_pages + (pos >> c.shift));
     return (unsigned)page < (unsigned)c.num_pages ? (page << c.shift) + (pos & ((1 << c.shift) - 1)) : -1;
 }
 

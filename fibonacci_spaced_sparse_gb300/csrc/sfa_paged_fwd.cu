@@ -33,11 +33,11 @@ struct Chunk<float> {
     float4 u, v;
 };
 __device__ __forceinline__ void load(const __nv_bfloat16* p, Chunk<__nv_bfloat16>& x) {
-    x.u = __ldg(reinterpret_cast<const uint4*>(p));
+    x.u = fresh(reinterpret_cast<const uint4*>(p));
 }
 __device__ __forceinline__ void load(const float* p, Chunk<float>& x) {
-    x.u = __ldg(reinterpret_cast<const float4*>(p));
-    x.v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    x.u = fresh(reinterpret_cast<const float4*>(p));
+    x.v = fresh(reinterpret_cast<const float4*>(p) + 1);
 }
 __device__ __forceinline__ void open(const Chunk<__nv_bfloat16>& x, float (&f)[8]) {
     const uint32_t w[4] = {x.u.x, x.u.y, x.u.z, x.u.w};
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kRowThreads<kNW>, 512 / kRowThreads<kNW>) rows
     if (t >= P.c.N) return;  // with kNW > 1 the whole block, here and below
     const int s = paged::sequence_of(P.c, t);
     if (s >= P.c.S) return;
-    const int pos = __ldg(P.c.lens + s) - (__ldg(P.c.cu + s + 1) - t);
+    const int pos = fresh(P.c.lens + s) - (fresh(P.c.cu + s + 1) - t);
     if (pos < 0 || pos >= P.c.cap) {
         const int i = kNW > 1 ? threadIdx.x : lane;
         if (i == 0 && g == 0) paged::report(P.c.status);
@@ -348,12 +348,12 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_c
     const int slot = (int)(blockIdx.x / kHkv) * kQuadWarps + warp;
     Quad Q;
     Q.g = blockIdx.x % kHkv;
-    Q.s = paged::last_at_most(P.c.S, slot, [&](int i) { return (__ldg(P.c.cu + i) >> 2) + i; });
-    const int start = __ldg(P.c.cu + Q.s), end = __ldg(P.c.cu + Q.s + 1);
+    Q.s = paged::last_at_most(P.c.S, slot, [&](int i) { return (fresh(P.c.cu + i) >> 2) + i; });
+    const int start = fresh(P.c.cu + Q.s), end = fresh(P.c.cu + Q.s + 1);
     Q.t0 = start + 4 * (slot - (start >> 2) - Q.s);
     if (Q.t0 < 0 || Q.t0 >= P.c.N || Q.t0 >= end) return;
     Q.cnt = min(4, min(end, P.c.N) - Q.t0);
-    Q.i0 = __ldg(P.c.lens + Q.s) - (end - Q.t0);       // position of the first query
+    Q.i0 = fresh(P.c.lens + Q.s) - (end - Q.t0);       // position of the first query
     Q.last = min(Q.i0 + Q.cnt, P.c.cap) - 1;           // no row behind it is read
     Q.rn = rn;
     Q.rc = rc;

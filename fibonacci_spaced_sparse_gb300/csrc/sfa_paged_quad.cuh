@@ -69,7 +69,7 @@ __device__ __forceinline__ float2 f2(float x, float y) { return make_float2(x, y
 __device__ __forceinline__ uint32_t word(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 
 __device__ __forceinline__ void load32(const char* p, uint32_t (&w)[8]) {
-    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
         : "l"(p));
 }
@@ -79,15 +79,15 @@ __device__ __forceinline__ void load32(const char* p, uint32_t (&w)[8]) {
 __device__ __forceinline__ void load32_natural(const char* row, int tig, uint32_t (&w)[8]) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-        w[s] = __ldg(reinterpret_cast<const uint32_t*>(row + 32 * s) + tig);
-        w[4 + s] = __ldg(reinterpret_cast<const uint32_t*>(row + 32 * s + 16) + tig);
+        w[s] = fresh(reinterpret_cast<const uint32_t*>(row + 32 * s) + tig);
+        w[4 + s] = fresh(reinterpret_cast<const uint32_t*>(row + 32 * s + 16) + tig);
     }
 }
 
 // The tile whose 16 row numbers lanes base .. base + 15 hold in `row`; in a
 // kAlone pass rows that are not there (-1) are zeros.
 template <bool kAlone, bool kNatural>
-__device__ __forceinline__ void load_tile(const char* __restrict__ k, const char* __restrict__ v, int row, int base,
+__device__ __forceinline__ void load_tile(const char* k, const char* v, int row, int base,
                                           Tile& x) {
     constexpr int kStride = kHkv * kD * 2;  // bytes of a page row
     const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
@@ -298,8 +298,8 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
         if (kNatural) {
             load32_natural(qp, tig, w);
         } else {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(qp) + 2 * tig);
-            const uint4 b = __ldg(reinterpret_cast<const uint4*>(qp) + 2 * tig + 1);
+            const uint4 a = fresh(reinterpret_cast<const uint4*>(qp) + 2 * tig);
+            const uint4 b = fresh(reinterpret_cast<const uint4*>(qp) + 2 * tig + 1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 w[j] = word(a, j);

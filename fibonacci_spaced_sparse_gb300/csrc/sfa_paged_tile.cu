@@ -150,11 +150,11 @@ __device__ __forceinline__ Work work_of(const PagedFwd& P, const int* rc, int sl
     const int lane = threadIdx.x & 31;
     Work x;
     x.g = 0;
-    x.s = paged::last_at_most(P.c.S, slot, [&](int i) { return __ldg(P.c.cu + i) / kTQ + i; });
-    const int start = __ldg(P.c.cu + x.s), end = __ldg(P.c.cu + x.s + 1);
+    x.s = paged::last_at_most(P.c.S, slot, [&](int i) { return fresh(P.c.cu + i) / kTQ + i; });
+    const int start = fresh(P.c.cu + x.s), end = fresh(P.c.cu + x.s + 1);
     x.t0 = start + kTQ * (slot - start / kTQ - x.s);
     x.cnt = x.t0 < 0 || x.t0 >= P.c.N || x.t0 >= end ? 0 : min(kTQ, min(end, P.c.N) - x.t0);
-    x.i0 = __ldg(P.c.lens + x.s) - (end - x.t0);
+    x.i0 = fresh(P.c.lens + x.s) - (end - x.t0);
     x.last = min(x.i0 + x.cnt, P.c.cap) - 1;
     x.used = __popc(__ballot_sync(kFull, rc[lane] <= x.last));
     x.groups = (x.used + 3) >> 2;
@@ -176,7 +176,7 @@ __device__ __forceinline__ Part part_of(const PagedFwd& P, int s, int base, int 
     const int sh = P.c.shift, index = (max(lo, 0) >> sh) + n;
     const int from = max(lo, index << sh), to = min(hi, ((index + 1) << sh) - 1);
     if (from > to) return Part{0, 0, 0, false};
-    const int page = __ldg(P.c.table + (size_t)s * P.c.max_pages + index);
+    const int page = fresh(P.c.table + (size_t)s * P.c.max_pages + index);
     if ((unsigned)page >= (unsigned)P.c.num_pages) return Part{0, 0, 0, true};
     return Part{(page << sh) + (from & ((1 << sh) - 1)), to - from + 1, from - base, false};
 }
@@ -478,11 +478,11 @@ __device__ __noinline__ void redo_query(const PagedFwd& P, const Shared& S, int 
     Quad Q;
     Q.s = paged::sequence_of(P.c, t);
     if (Q.s >= P.c.S) return;
-    const int start = __ldg(P.c.cu + Q.s), end = __ldg(P.c.cu + Q.s + 1);
+    const int start = fresh(P.c.cu + Q.s), end = fresh(P.c.cu + Q.s + 1);
     const int only = (t - start) & 3;
     Q.t0 = t - only;
     Q.cnt = min(4, min(end, P.c.N) - Q.t0);
-    Q.i0 = __ldg(P.c.lens + Q.s) - (end - Q.t0);
+    Q.i0 = fresh(P.c.lens + Q.s) - (end - Q.t0);
     Q.last = min(Q.i0 + Q.cnt, P.c.cap) - 1;
     Q.g = g;
     Q.rn = S.rn;

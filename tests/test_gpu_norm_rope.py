@@ -262,3 +262,57 @@ def test_captured_call_outlives_a_grown_table():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want)) and len(junk) == 8
+
+
+def test_two_backward_calls_at_once():
+    """Two streams at the same time, workspaces from the allocator: the results
+    of one call after the other, bit for bit."""
+    given = []
+    for seed in (41, 42):
+        q, k, wq, wk, g = _draw(3, 2000, "bf16", True, seed=seed)
+        up = [torch.randn((3, 2000, h, D), generator=g).to(torch.bfloat16).cuda() for h in (HQ, HKV)]
+        given.append((q, k, wq, wk, *up))
+    want = [api.sfa_qk_norm_rope_backward(*x) for x in given]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [None, None]
+    for i in (0, 1) * 4:
+        got[i] = api.sfa_qk_norm_rope_backward(*given[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+
+
+def test_captured_training_step():
+    """Forward and backward of QKNormRope and SparseAttention captured together,
+    replayed on new inputs, against the eager gradients: those that no atomic
+    sum enters bit for bit, dV to one step of bf16 (its fp32 sums run in a free
+    order, which may move the value before the rounding by 2^-12 of the largest)."""
+    q, k, wq, wk, g = _draw(2, 150, "bf16", False, seed=43)
+    v = torch.randn((2, 150, HKV, D), generator=g).to(torch.bfloat16).cuda()
+    theta = torch.tensor(0.2)  # on the host: read there when the call is made
+
+    def step(*leaves):
+        o = api.SparseAttention.apply(*api.QKNormRope.apply(*leaves[:4]), leaves[4], theta, 12, api.FIBONACCI_BASE, 0.0)
+        return torch.autograd.grad(o.float().square().sum(), leaves)
+
+    leaves = [x.detach().clone().requires_grad_() for x in (q, k, wq, wk, v)]
+    want = step(*leaves)
+    static = [x.detach().clone().requires_grad_() for x in leaves]
+    with torch.no_grad():
+        for x in static[:2]:
+            x.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*static)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*static)
+    with torch.no_grad():
+        for x, y in zip(static[:2], leaves[:2]):
+            x.copy_(y)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    b = want[4].double().cpu()
+    within(got[4], b, 2.0 ** -7 * b.abs() + 2.0 ** -12 * b.abs().max(), "dv")

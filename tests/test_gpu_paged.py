@@ -497,3 +497,87 @@ def test_shared_pages_of_a_common_prefix():
     cache.table[1, :4] = cache.table[0, :4]
     kw = dict(alpha=0.87, W=12, rungs=FIB)
     _check(cache, _forward(cache, **kw), attention64(cache, tensor_cores=True, **kw))
+
+
+@pytest.mark.parametrize("W", [-1, -2 ** 31, 8 - 2 ** 32])
+def test_negative_windows_are_refused(W):
+    cache = Cache(SINGLES, 16, "bf16")
+    kp, vp = cache.pages()
+    with pytest.raises(RuntimeError):
+        api.sfa_paged_forward(cache.q.cuda(), kp, vp, *cache.meta(), alpha=0.87, W=W)
+
+
+@pytest.mark.parametrize("W", [2 ** 31 - 1, 2 ** 31 + 8, 2 ** 40])
+def test_windows_wider_than_any_sequence(W):
+    """Every row of the sequence, as with a window that just holds it."""
+    cache = Cache(RAGGED, 16, "bf16")
+    a, b = (_forward(cache, alpha=0.87, W=w, rungs=FIB) for w in (W, 2000))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and a[2] == 0
+
+
+@pytest.mark.parametrize("lens", [MANY, [(120, 9), (500, 0)], LONG])
+def test_two_calls_at_once(lens):
+    """The same entry points on two streams at the same time, each on its own
+    cache: the results of one call after the other, bit for bit."""
+    caches = [Cache(lens, 16, "bf16", seed=s) for s in (31, 32)]
+    wk = torch.linspace(0.5, 1.5, D, device="cuda")
+    given = []
+    for c in caches:
+        new = [torch.cat([x[s][n0:] for s, (_, n0) in enumerate(c.lens)] + [torch.zeros((7, HKV, D), dtype=DT["bf16"])])
+               .cuda() for x in (c.k, c.v)]
+        given.append((c.q.cuda(), *new, *c.pages(rows_before=True), *c.meta()))
+    rope = api.rope_table(4096, "cuda")
+
+    def step(q, k, v, kp, vp, *meta):
+        kp, vp = kp.clone(), vp.clone()
+        for _ in range(4):
+            qo = torch.zeros_like(q)
+            api.sfa_paged_append(k, v, kp, vp, *meta, q=q, wq=wk, wk=wk, q_out=qo, rope=rope)
+            o, lse = api.sfa_paged_forward(qo, kp, vp, *meta, alpha=0.87, W=12, out=torch.zeros_like(q),
+                                           lse=torch.zeros(q.shape[:2], device="cuda"))
+        return qo, o, lse
+
+    want = [step(*g) for g in given]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for s, g in zip(streams, given):
+        with torch.cuda.stream(s):
+            got.append(step(*g))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+
+
+def test_lookups_written_by_the_launch_before():
+    """Each call reads what the launch right before it wrote: queries, pages and
+    metadata, in a captured chain with no other work between them."""
+    sets = [Cache([(1, 40 + 7 * s + t) for s in range(6)], 16, "bf16", seed=60 + t, behind=0, num_pages=128) for t in range(2)]
+    width = min(c.max_pages for c in sets)
+    kw = dict(alpha=0.87, W=12, rungs=FIB)
+    want = []
+    for c in sets:
+        kp, vp = c.pages()
+        want.append(api.sfa_paged_forward(c.q.cuda(), kp, vp, *c.meta(), **kw)[0])
+    src = [(c.q.cuda(), c.table[:, :width].contiguous().cuda(), c.cu.cuda(), c.seq.cuda()) for c in sets]
+    pages = [c.pages() for c in sets]
+    q, table, cu, seq = (torch.empty_like(x) for x in src[0])
+    outs = [[torch.empty_like(q), torch.empty_like(q)] for _ in range(8)]
+
+    def chain():
+        for o in outs:
+            for t in range(2):
+                for dst, x in zip((table, cu, q, seq), (src[t][1], src[t][2], src[t][0], src[t][3])):
+                    dst.copy_(x)
+                api.sfa_paged_forward(q, *pages[t], table, cu, seq, out=o[t], need_lse=False, **kw)
+
+    chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(5):
+        for o in outs:
+            o[0].fill_(7), o[1].fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o[t], want[t]) for o in outs for t in range(2))
