@@ -10,6 +10,7 @@
 // stream of the tensors' device; outputs come from torch's allocator on it.
 #include <Python.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <string>
 
@@ -163,7 +164,7 @@ int64_t integer(PyObject* o) {
     return x;
 }
 
-int small(int64_t x) { return x > 0x7fffffff ? 0x7fffffff : (int)x; }  // the library refuses it
+int small(int64_t x) { return (int)std::clamp<int64_t>(x, -1, 0x7fffffff); }  // the library refuses both
 
 sfa_params params(int64_t B, int64_t T, sfa_dtype dt, double theta) {
     sfa_params p = {};
