@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     if (warp_t >= a.c.N) return;
     const bool in_n = t < a.c.N;
     const int tt = in_n ? t : a.c.N - 1;
-    // the row's loads go out before the lookups
+    // what does not depend on the lookups is loaded before them
     const T* src;
     if (role == kValue)
         src = static_cast<const T*>(a.vn) + (size_t)tt * a.vs;
@@ -44,19 +44,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     Raw<T> raw[2];
     fetch(src, c, raw[0]);
     fetch(src + kD, c, raw[1]);
+    const float* wp = role == kKey ? a.wk : a.wq;
+    Row w{};
+    if (wp && role != kValue) w = weights(wp, c);
     // the sequence of the warp's first token, then forward to this lane's
-    int s = paged::sequence_of(a.c, warp_t);
-    if (s >= a.c.S) return;  // it lies behind the last sequence, and so do the others
-    int end = fresh(a.c.cu + s + 1);
-    while (end <= tt && s + 1 < a.c.S) end = fresh(a.c.cu + ++s + 1);
-    if (!in_n || tt >= end) return;
-    const int pos = fresh(a.c.lens + s) - (end - tt);
+    paged::Where x = paged::sequence_of(a.c, warp_t);
+    if (x.s >= a.c.S) return;  // it lies behind the last sequence, and so do the others
+    while (x.end <= tt && x.s + 1 < a.c.S) {
+        x.end = fresh(a.c.cu + ++x.s + 1);
+        x.len = fresh(a.c.lens + x.s);
+    }
+    if (!in_n || tt >= x.end) return;
+    const int pos = x.len - (x.end - tt);
     const bool good = pos >= 0 && pos < a.c.cap;
+    Angles rot;
+    if (a.rope && good && role != kValue) rot = angles(a.rope, pos, c);
     if (!good && c == 0 && role == kKey) paged::report(a.c.status);
     T* dst;
     if (role >= kKey) {
         if (!good) return;
-        const int row = paged::page_row(a.c, s, pos);
+        const int row = paged::page_row(a.c, x.s, pos);
         if (row < 0) {
             if (c == 0 && role == kKey) paged::report(a.c.status);
             return;
@@ -70,19 +77,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     } else {
         dst = static_cast<T*>(a.qhat) + (size_t)t * (kHq * kD) + role * 2 * kD;
     }
-    const float* wp = role == kKey ? a.wk : a.wq;
     const unsigned mask = 0xfu << (threadIdx.x & 28);
-    Row w;
-    if (wp) w = weights(wp, c);
-    Angles rot;
-    if (a.rope && good) rot = angles(a.rope, pos, c);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        Row x = open(raw[h]);
-        if (wp) scale(x, inv_rms(x, a.eps, mask), w);
-        if (a.rope && good) rotate(x, rot);
-        if (!good) x = Row{};
-        store(dst + h * kD, c, x);
+        Row y = open(raw[h]);
+        if (wp) scale(y, inv_rms(y, a.eps, mask), w);
+        if (a.rope && good) rotate(y, rot);
+        if (!good) y = Row{};
+        store(dst + h * kD, c, y);
     }
 }
 

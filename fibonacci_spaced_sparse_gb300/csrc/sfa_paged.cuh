@@ -27,13 +27,29 @@ __device__ __forceinline__ int last_at_most(int n, int x, F first) {
     return lo;
 }
 
-// The sequence that token row t belongs to, or S when it belongs to none (the
-// whole warp asks for the same t).  A step in which every sequence brings one
-// token is found at once.
-__device__ __forceinline__ int sequence_of(const PagedArgs& c, int t) {
-    if (t < c.S && fresh(c.cu + t) == t && fresh(c.cu + t + 1) == t + 1) return t;
-    const int s = last_at_most(c.S, t, [&](int i) { return fresh(c.cu + i); });
-    return fresh(c.cu + s) <= t && t < fresh(c.cu + s + 1) ? s : c.S;
+// The sequence that token row t belongs to, or S when it belongs to none, with
+// its last row's successor and its length (the whole warp asks for the same t).
+// A step in which every sequence brings one token is found at once.  The three
+// words are loaded together, used or not: a chain of dependent lookups is what
+// a decode step's time consists of.
+struct Where {
+    int s, end, len;
+};
+__device__ __forceinline__ Where sequence_of(const PagedArgs& c, int t) {
+    auto there = [&](int s, int& start) {
+        start = fresh(c.cu + s);
+        const Where x = {s, fresh(c.cu + s + 1), fresh(c.lens + s)};
+        asm volatile("" ::"r"(start), "r"(x.end), "r"(x.len));  // none of the loads moves behind a branch
+        return x;
+    };
+    int start;
+    if (t < c.S) {
+        const Where x = there(t, start);
+        if (start == t && x.end == t + 1) return x;
+    }
+    Where x = there(last_at_most(c.S, t, [&](int i) { return fresh(c.cu + i); }), start);
+    if (t < start || t >= x.end) x.s = c.S;
+    return x;
 }
 
 // Row of the pages that holds position pos >= 0 of sequence s; -1 for a page

@@ -70,17 +70,8 @@ struct Partial {
 };
 
 template <typename T>
-__device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const T* qrow, int first, int step) {
+__device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Chunk<T> (&raw)[kG], int first, int step) {
     const int lane = threadIdx.x & 31, slot = lane >> 3, ch = lane & 7;
-    float q[kG][8];
-#pragma unroll
-    for (int h = 0; h < kG; ++h) {
-        Chunk<T> x;
-        load(qrow + h * kD + 8 * ch, x);
-        open(x, q[h]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[h][j] *= P.a.scale * kLog2e;
-    }
     const int nwin = min(P.a.W, pos) + 1;
     int nrung = 0;
     for (int r = 0; r < P.a.nr; ++r) nrung += P.a.r[r].c <= pos ? 1 : 0;  // sorted: a prefix
@@ -118,6 +109,13 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const T*
         }
     };
     entry(first + slot);
+    float q[kG][8];
+#pragma unroll
+    for (int h = 0; h < kG; ++h) {
+        open(raw[h], q[h]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[h][j] *= P.a.scale * kLog2e;
+    }
     for (int e0 = first; e0 < n; e0 += step) {
         float k[8], v[8];
         {
@@ -242,30 +240,34 @@ __global__ void __launch_bounds__(kRowThreads<kNW>, 512 / kRowThreads<kNW>) rows
     const unsigned unit = blockIdx.x * kUnits + (kNW > 1 ? 0 : warp);
     const int t = (int)(unit / kHkv), g = (int)(unit % kHkv);
     if (t >= P.c.N) return;  // with kNW > 1 the whole block, here and below
-    const int s = paged::sequence_of(P.c, t);
-    if (s >= P.c.S) return;
-    const int pos = fresh(P.c.lens + s) - (fresh(P.c.cu + s + 1) - t);
+    // the query's loads go out before the lookups
+    Chunk<T> raw[kG];
+    const T* qrow = static_cast<const T*>(P.q) + (size_t)t * P.qs + g * kG * kD + 8 * (lane & 7);
+#pragma unroll
+    for (int h = 0; h < kG; ++h) load(qrow + h * kD, raw[h]);
+    const paged::Where x = paged::sequence_of(P.c, t);
+    if (x.s >= P.c.S) return;
+    const int pos = x.len - (x.end - t);
     if (pos < 0 || pos >= P.c.cap) {
         const int i = kNW > 1 ? threadIdx.x : lane;
         if (i == 0 && g == 0) paged::report(P.c.status);
         zero_out<T>(P, t, g, i, kNW > 1 ? kThreads : 32);
         return;
     }
-    const T* qrow = static_cast<const T*>(P.q) + (size_t)t * P.qs + g * kG * kD;
-    const Partial x = query_part<T>(P, s, pos, g, qrow, kNW > 1 ? 4 * warp : 0, 4 * kNW);
+    const Partial y = query_part<T>(P, x.s, pos, g, raw, kNW > 1 ? 4 * warp : 0, 4 * kNW);
     const int h = lane >> 3, ch = lane & 7;
     if (kNW == 1) {
-        write_part<T>(P, t, g, h, ch, x);
+        write_part<T>(P, t, g, h, ch, y);
         return;
     }
     if (ch == 0) {
-        top[warp][h] = x.m;
-        sum[warp][h] = x.l;
+        top[warp][h] = y.m;
+        sum[warp][h] = y.l;
     }
     float* mine = part[kNW > 1 ? warp : 0] + (kNW > 1 ? h * kD + 8 * ch : 0);
     if (kNW > 1) {
-        reinterpret_cast<float4*>(mine)[0] = make_float4(x.acc[0], x.acc[1], x.acc[2], x.acc[3]);
-        reinterpret_cast<float4*>(mine)[1] = make_float4(x.acc[4], x.acc[5], x.acc[6], x.acc[7]);
+        reinterpret_cast<float4*>(mine)[0] = make_float4(y.acc[0], y.acc[1], y.acc[2], y.acc[3]);
+        reinterpret_cast<float4*>(mine)[1] = make_float4(y.acc[4], y.acc[5], y.acc[6], y.acc[7]);
     }
     __syncthreads();
     T* o = static_cast<T*>(P.o) + ((size_t)t * kHq + g * kG) * kD;

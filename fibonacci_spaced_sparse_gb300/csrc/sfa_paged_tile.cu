@@ -475,14 +475,14 @@ __device__ bool consume(const TileParams& T, Shared& S) {
 
 // Token row t alone, as the quad that it stands in computes it.
 __device__ __noinline__ void redo_query(const PagedFwd& P, const Shared& S, int t, int g) {
+    const paged::Where x = paged::sequence_of(P.c, t);
+    if (x.s >= P.c.S) return;
     Quad Q;
-    Q.s = paged::sequence_of(P.c, t);
-    if (Q.s >= P.c.S) return;
-    const int start = fresh(P.c.cu + Q.s), end = fresh(P.c.cu + Q.s + 1);
-    const int only = (t - start) & 3;
+    Q.s = x.s;
+    const int only = (t - fresh(P.c.cu + x.s)) & 3;
     Q.t0 = t - only;
-    Q.cnt = min(4, min(end, P.c.N) - Q.t0);
-    Q.i0 = fresh(P.c.lens + Q.s) - (end - Q.t0);
+    Q.cnt = min(4, min(x.end, P.c.N) - Q.t0);
+    Q.i0 = x.len - (x.end - Q.t0);
     Q.last = min(Q.i0 + Q.cnt, P.c.cap) - 1;
     Q.g = g;
     Q.rn = S.rn;
