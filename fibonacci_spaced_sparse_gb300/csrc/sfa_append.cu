@@ -3,12 +3,15 @@
 // (sfa_paged_append in include/sfa.h).
 //
 // A copy with arithmetic, bound by memory when there are many tokens and by
-// the latency of its lookups (cu_q -> seq_lens -> block_table) in a decode
-// step.  Blocks that go through consecutive tokens and copy the next step's rows
-// ahead, as the norm does for many tokens, are slower here (14.9 against
-// 13.0 us for 16 prompts of up to 2048 tokens, 26.5 against 22.5 us for 32768
-// tokens): the lookups of a step stand in line with its copies.  Four lanes hold a head row (sfa_heads.cuh); a quad of lanes handles
-// two rows of one token: queries 0-1, 2-3, 4-5, 6-7, keys 0-1, values 0-1.
+// the latency of its lookups (cu_q and seq_lens -> block_table and the rotation's
+// angles) in a decode step: what does not depend on a lookup is loaded before it
+// (256 tokens 2.4 us; with the weights and angles loaded last 2.6).  Blocks that
+// go through consecutive tokens and copy the next step's rows ahead, as the norm
+// does for many tokens, are slower here (14.9 against 13.0 us for 16 prompts of
+// up to 2048 tokens, 26.5 against 22.5 us for 32768 tokens, before the order of
+// the loads; 12.5 us now): the lookups of a step stand in line with its copies.
+// Four lanes hold a head row (sfa_heads.cuh); a quad of lanes handles two rows
+// of one token: queries 0-1, 2-3, 4-5, 6-7, keys 0-1, values 0-1.
 #include "sfa_heads.cuh"
 #include "sfa_paged.cuh"
 

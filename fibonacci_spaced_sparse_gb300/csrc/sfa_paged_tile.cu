@@ -4,9 +4,10 @@
 //
 // A block takes tiles of 28 consecutive queries of one sequence and one
 // key/value head, a quad to each of seven warps, the heads one after the other
-// (they read the same rows, so a slot of 28 queries is looked up once).  The rows that a tile reads
-// are the window block, W + 28 rows, and 29 rows a rung, so a row is looked up
-// and fetched once a tile, where the quad kernel's warps each fetch their own.
+// (they read the same rows, so a slot of 28 queries is looked up once).  The
+// rows that a tile reads are the window block, W + 28 rows, and 29 rows a rung,
+// so a row is looked up and fetched once a tile, where the quad kernel's warps
+// each fetch their own.
 // An eighth warp does nothing else: it looks the blocks' pages up in the block
 // table and fetches the part of a block that lies in a page (pages of 16 rows
 // and more) with one TMA box, rows of one head under the 128-byte swizzle, into
