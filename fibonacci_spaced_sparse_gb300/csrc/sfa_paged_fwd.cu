@@ -69,7 +69,9 @@ struct Partial {
     float m, l;
 };
 
-template <typename T>
+// kAhead: the rows of the next entries are loaded while the current ones are
+// used.
+template <typename T, bool kAhead>
 __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Chunk<T> (&raw)[kG], int first, int step) {
     const int lane = threadIdx.x & 31, slot = lane >> 3, ch = lane & 7;
     const int nwin = min(P.a.W, pos) + 1;
@@ -85,12 +87,11 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
         for (int j = 0; j < 8; ++j) acc[h][j] = 0.f;
     float m = kFloor, l = 0.f;  // of head (lane >> 1) & 3, this slot's entries
     bool bad = false;
-    // row numbers and weights of entry e of the key list; ra < 0: none
+    // row numbers of entry e of the key list; ra < 0: none
     int ra, rb;
-    float wa, wb;
+    float wb;  // the second row's weight
     auto entry = [&](int e) {
         ra = rb = -1;
-        wa = 1.f;
         wb = 0.f;
         if (e < nwin) {
             ra = paged::page_row(P.c, s, pos - e);
@@ -103,12 +104,34 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
                 rb = paged::page_row(P.c, s, pos - R.n - 1);
                 bad |= rb < 0;
                 if (rb < 0) ra = -1;  // an entry needs both of its rows
-                wa = 1.f - R.t;
                 wb = R.t;
             }
         }
     };
+    // rows of four entries on their way (an entry without a second row: zeros)
+    struct Rows {
+        Chunk<T> ka, va, kc, vc;
+        float t;  // weight of the second row; < 0: no entry
+    };
+    auto rows = [&]() {
+        Rows x{};
+        x.t = ra < 0 ? -1.f : wb;
+        if (ra >= 0) {
+            load(kb + (size_t)ra * (kHkv * kD), x.ka);
+            load(vb + (size_t)ra * (kHkv * kD), x.va);
+            if (rb >= 0) {
+                load(kb + (size_t)rb * (kHkv * kD), x.kc);
+                load(vb + (size_t)rb * (kHkv * kD), x.vc);
+            }
+        }
+        return x;
+    };
     entry(first + slot);
+    Rows next;
+    if (kAhead) {
+        next = rows();
+        if (first + step < n) entry(first + step + slot);
+    }
     float q[kG][8];
 #pragma unroll
     for (int h = 0; h < kG; ++h) {
@@ -117,32 +140,31 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
         for (int j = 0; j < 8; ++j) q[h][j] *= P.a.scale * kLog2e;
     }
     for (int e0 = first; e0 < n; e0 += step) {
-        float k[8], v[8];
-        {
-            Chunk<T> ka{}, va{}, kc{}, vc{};
-            if (ra >= 0) {
-                load(kb + (size_t)ra * (kHkv * kD), ka);
-                load(vb + (size_t)ra * (kHkv * kD), va);
-                if (rb >= 0) {
-                    load(kb + (size_t)rb * (kHkv * kD), kc);
-                    load(vb + (size_t)rb * (kHkv * kD), vc);
-                }
+        Rows now;
+        if (kAhead) {
+            now = next;
+            if (e0 + step < n) {
+                next = rows();
+                if (e0 + 2 * step < n) entry(e0 + 2 * step + slot);
             }
-            open(ka, k);
-            open(va, v);
-            if (rb >= 0 && ra >= 0) {
-                float x[8], y[8];
-                open(kc, x);
-                open(vc, y);
+        } else {
+            now = rows();
+        }
+        float k[8], v[8];
+        open(now.ka, k);
+        open(now.va, v);
+        if (now.t > 0.f) {
+            float x[8], y[8];
+            open(now.kc, x);
+            open(now.vc, y);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    k[j] = wa * k[j] + wb * x[j];
-                    v[j] = wa * v[j] + wb * y[j];
-                }
+            for (int j = 0; j < 8; ++j) {
+                k[j] = (1.f - now.t) * k[j] + now.t * x[j];
+                v[j] = (1.f - now.t) * v[j] + now.t * y[j];
             }
         }
-        const bool there = ra >= 0;
-        if (e0 + step < n) entry(e0 + step + slot);  // the next entries' pages are looked up meanwhile
+        const bool there = now.t >= 0.f;
+        if (!kAhead && e0 + step < n) entry(e0 + step + slot);  // the next entries' pages are looked up meanwhile
         float d[kG];
 #pragma unroll
         for (int h = 0; h < kG; ++h) {
@@ -257,7 +279,12 @@ __global__ void __launch_bounds__(kRowThreads<kNW>, 512 / kRowThreads<kNW>) rows
         zero_out<T>(P, t, g, i, kNW > 1 ? kThreads : 32);
         return;
     }
-    const Partial y = query_part<T>(P, x.s, pos, g, raw, kNW > 1 ? 4 * warp : 0, 4 * kNW);
+    // With several warps a token there are one or two rounds of loads; with one
+    // there are six, and loads ahead pay (us, without and with, 1024 single
+    // tokens 7.9 and 7.2, 2048 18.7 and 16.0).  fp32 rows do not fit the
+    // registers twice (128 spill 90 bytes: 1024 single tokens 10.6 and 11.8).
+    constexpr bool kAhead = kNW == 1 && sizeof(T) == 2;
+    const Partial y = query_part<T, kAhead>(P, x.s, pos, g, raw, kNW > 1 ? 4 * warp : 0, 4 * kNW);
     const int h = lane >> 3, ch = lane & 7;
     if (kNW == 1) {
         write_part<T>(P, t, g, h, ch, y);
