@@ -39,18 +39,17 @@ __device__ __forceinline__ void load(const float* p, Chunk<float>& x) {
     x.u = fresh(reinterpret_cast<const float4*>(p));
     x.v = fresh(reinterpret_cast<const float4*>(p) + 1);
 }
-__device__ __forceinline__ void open(const Chunk<__nv_bfloat16>& x, float (&f)[8]) {
+// As pairs for the packed two-lane fp32 instructions.
+__device__ __forceinline__ void open(const Chunk<__nv_bfloat16>& x, float2 (&f)[4]) {
     const uint32_t w[4] = {x.u.x, x.u.y, x.u.z, x.u.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+    for (int j = 0; j < 4; ++j) f[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
 }
-__device__ __forceinline__ void open(const Chunk<float>& x, float (&f)[8]) {
-    f[0] = x.u.x, f[1] = x.u.y, f[2] = x.u.z, f[3] = x.u.w;
-    f[4] = x.v.x, f[5] = x.v.y, f[6] = x.v.z, f[7] = x.v.w;
+__device__ __forceinline__ void open(const Chunk<float>& x, float2 (&f)[4]) {
+    f[0] = make_float2(x.u.x, x.u.y), f[1] = make_float2(x.u.z, x.u.w);
+    f[2] = make_float2(x.v.x, x.v.y), f[3] = make_float2(x.v.z, x.v.w);
 }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
@@ -80,11 +79,11 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
     const int n = nwin + nrung;
     const T* kb = static_cast<const T*>(P.c.k) + g * kD + 8 * ch;
     const T* vb = static_cast<const T*>(P.c.v) + g * kD + 8 * ch;
-    float acc[kG][8];
+    float2 acc[kG][4];
 #pragma unroll
     for (int h = 0; h < kG; ++h)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[h][j] = 0.f;
+        for (int j = 0; j < 4; ++j) acc[h][j] = both(0.f);
     float m = kFloor, l = 0.f;  // of head (lane >> 1) & 3, this slot's entries
     bool bad = false;
     // row numbers of entry e of the key list; ra < 0: none
@@ -132,12 +131,12 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
         next = rows();
         if (first + step < n) entry(first + step + slot);
     }
-    float q[kG][8];
+    float2 q[kG][4];
 #pragma unroll
     for (int h = 0; h < kG; ++h) {
         open(raw[h], q[h]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[h][j] *= P.a.scale * kLog2e;
+        for (int j = 0; j < 4; ++j) q[h][j] = __fmul2_rn(q[h][j], both(P.a.scale * kLog2e));
     }
     for (int e0 = first; e0 < n; e0 += step) {
         Rows now;
@@ -150,17 +149,18 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
         } else {
             now = rows();
         }
-        float k[8], v[8];
+        float2 k[4], v[4];
         open(now.ka, k);
         open(now.va, v);
         if (now.t > 0.f) {
-            float x[8], y[8];
+            float2 x[4], y[4];
             open(now.kc, x);
             open(now.vc, y);
+            const float2 near = both(1.f - now.t), far = both(now.t);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                k[j] = (1.f - now.t) * k[j] + now.t * x[j];
-                v[j] = (1.f - now.t) * v[j] + now.t * y[j];
+            for (int j = 0; j < 4; ++j) {
+                k[j] = __ffma2_rn(far, x[j], __fmul2_rn(near, k[j]));
+                v[j] = __ffma2_rn(far, y[j], __fmul2_rn(near, v[j]));
             }
         }
         const bool there = now.t >= 0.f;
@@ -168,9 +168,10 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
         float d[kG];
 #pragma unroll
         for (int h = 0; h < kG; ++h) {
-            d[h] = 0.f;
+            float2 s = __fmul2_rn(q[h][0], k[0]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[h] = fmaf(q[h][j], k[j], d[h]);
+            for (int j = 1; j < 4; ++j) s = __ffma2_rn(q[h][j], k[j], s);
+            d[h] = s.x + s.y;
         }
         // sum over the slot's eight lanes; head h ends in lanes 2h, 2h + 1
         const bool up4 = lane & 4, up2 = lane & 2;
@@ -188,7 +189,7 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
             for (int h = 0; h < kG; ++h) {
                 const float fh = __shfl_sync(kFull, f, (lane & 24) + 2 * h);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[h][j] *= fh;
+                for (int j = 0; j < 4; ++j) acc[h][j] = __fmul2_rn(acc[h][j], both(fh));
             }
         }
         const float p = exp2f(x - m);
@@ -197,7 +198,7 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
         for (int h = 0; h < kG; ++h) {
             const float ph = __shfl_sync(kFull, p, (lane & 24) + 2 * h);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[h][j] = fmaf(ph, v[j], acc[h][j]);
+            for (int j = 0; j < 4; ++j) acc[h][j] = __ffma2_rn(both(ph), v[j], acc[h][j]);
         }
     }
     if (__any_sync(kFull, bad) && lane == 0) paged::report(P.c.status);
@@ -212,14 +213,15 @@ __device__ Partial query_part(const PagedFwd& P, int s, int pos, int g, const Ch
     for (int h = 0; h < kG; ++h) {
         const float fh = __shfl_sync(kFull, f, (lane & 24) + 2 * h);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[h][j] *= fh;
+        for (int j = 0; j < 4; ++j) acc[h][j] = __fmul2_rn(acc[h][j], both(fh));
     }
     const bool up16 = lane & 16, up8 = lane & 8;
     Partial out;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float a0 = (up16 ? acc[2][j] : acc[0][j]) + __shfl_xor_sync(kFull, up16 ? acc[0][j] : acc[2][j], 16);
-        const float a1 = (up16 ? acc[3][j] : acc[1][j]) + __shfl_xor_sync(kFull, up16 ? acc[1][j] : acc[3][j], 16);
+        auto at = [&](int h) { return j & 1 ? acc[h][j / 2].y : acc[h][j / 2].x; };
+        const float a0 = (up16 ? at(2) : at(0)) + __shfl_xor_sync(kFull, up16 ? at(0) : at(2), 16);
+        const float a1 = (up16 ? at(3) : at(1)) + __shfl_xor_sync(kFull, up16 ? at(1) : at(3), 16);
         out.acc[j] = (up8 ? a1 : a0) + __shfl_xor_sync(kFull, up8 ? a0 : a1, 8);
     }
     out.m = __shfl_sync(kFull, top, 2 * slot);
