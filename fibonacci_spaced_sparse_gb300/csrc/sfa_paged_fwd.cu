@@ -251,11 +251,11 @@ __device__ __forceinline__ void write_part(const PagedFwd& P, int t, int g, int 
 }
 
 template <int kNW>
-constexpr int kRowThreads = kNW > 1 ? 32 * kNW : 256;  // one unit a block, or eight of one warp each
+constexpr int kRowThreads = kNW > 1 ? 32 * kNW : 64;  // one unit a block, or two of one warp each (of eight: 2048 single tokens 15.9 and 15.5 us, 16 x 1024 in fp32 50.1 and 45.8)
 
 template <typename T, int kNW>
 __global__ void __launch_bounds__(kRowThreads<kNW>, 512 / kRowThreads<kNW>) rows_kernel(const __grid_constant__ PagedFwd P) {
-    constexpr int kThreads = kRowThreads<kNW>, kUnits = kNW > 1 ? 1 : 8;  // (token, head) of a block
+    constexpr int kThreads = kRowThreads<kNW>, kUnits = kNW > 1 ? 1 : 2;  // (token, head) of a block
     __shared__ __align__(16) float part[kNW > 1 ? kNW : 1][kNW > 1 ? kG * kD : 4];
     __shared__ float top[kNW][kG], sum[kNW][kG];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kRowThreads<kNW>, 512 / kRowThreads<kNW>) rows
 
 template <typename T, int kNW>
 cudaError_t launch_rows_nw(const PagedFwd& P, cudaStream_t s) {
-    constexpr int kUnits = kNW > 1 ? 1 : 8;
+    constexpr int kUnits = kNW > 1 ? 1 : 2;
     const long long units = (long long)P.c.N * kHkv;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((units + kUnits - 1) / kUnits));
@@ -344,8 +344,8 @@ cudaError_t launch_rows_nw(const PagedFwd& P, cudaStream_t s) {
 // As many warps a (token, head) as keep all of them resident at once (16 a SM
 // at 128 registers, 152 SMs): a decode step is then one wave of one or two
 // rounds of loads.  us for N single tokens over 3000 rows, bf16, with 8, 4, 2
-// and 1 warps: N = 128 3.9, 4.6, 5.6, 6.6; 256 6.9, 4.8, 6.2, 6.9; 1024 22.7,
-// 16.0, 12.0, 8.6.
+// and 1 warps: N = 128 3.6, 4.2, 5.0, 4.8; 256 6.2, 4.3, 5.7, 5.5; 500 10.7, 7.5,
+// 5.8, 6.5; 1024 19.8, 14.0, 10.7, 6.9.
 template <typename T>
 cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
     const long long most = 152 * 16 / ((long long)P.c.N * kHkv);
@@ -414,11 +414,12 @@ cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
     return e;
 }
 
-// Token rows from which the quad kernel is taken: it wins where sequences bring
-// more than a token (us, rows and quads: one chunk of 256 tokens 4.7 and 5.2,
-// of 512 6.3 and 5.4, 8 of 256 14.1 and 7.0), the rows kernel where they bring
-// one (2048 sequences 21.3 and 25.6): at least two a sequence.
-constexpr int kQuadsFrom = 512;
+// Token rows from which the quad kernel is taken, if there are two a sequence at
+// least: where the rows kernel has less than four warps a token (us, rows and
+// quads: 300 tokens in chunks of 2 4.6 and 5.1, in one 4.3 and 4.3; 320 5.8 and
+// 5.5, 5.4 and 4.5; 500 6.1 and 5.9, 5.5 and 4.3; 8 chunks of 256 11.5 and 6.9).
+// Single tokens stay with the rows kernel (2048 of them 15.4 and 24.1).
+constexpr int kQuadsFrom = 305;
 
 // Token rows from which the tile kernel is taken, in pages that hold 16 rows at
 // least: tiles of 28 want long chunks (us, quads and tiles: one chunk of 2048

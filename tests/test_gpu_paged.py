@@ -581,3 +581,13 @@ def test_lookups_written_by_the_launch_before():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o[t], want[t]) for o in outs for t in range(2))
+
+
+@pytest.mark.parametrize("lens,behind", [([(304, 5)], 0), ([(304, 5)], 1), ([(2, 30 + 5 * s) for s in range(152)], 0),
+                                         ([(2, 30 + 5 * s) for s in range(153)], 0),
+                                         ([(1, 0)] * 20 + [(290, 100)] + [(1, 5)] * 9, 2), ([(500, 9)], 0)])
+def test_where_the_kernels_change(lens, behind):
+    """Token rows on both sides of where the kernels take over from one another."""
+    cache = Cache(lens, 16, "bf16", seed=70 + len(lens) + behind, behind=behind)
+    kw = dict(alpha=0.87, W=12, rungs=FIB)
+    _check(cache, _forward(cache, **kw), attention64(cache, tensor_cores=True, **kw))
