@@ -53,10 +53,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     // the sequence of the warp's first token, then forward to this lane's
     paged::Where x = paged::sequence_of(a.c, warp_t);
     if (x.s >= a.c.S) return;  // it lies behind the last sequence, and so do the others
-    while (x.end <= tt && x.s + 1 < a.c.S) {
-        x.end = fresh(a.c.cu + ++x.s + 1);
-        x.len = fresh(a.c.lens + x.s);
-    }
+    while (x.end <= tt && x.s + 1 < a.c.S) x = paged::look(a.c, x.s + 1);
     if (!in_n || tt >= x.end) return;
     const int pos = x.len - (x.end - tt);
     const bool good = pos >= 0 && pos < a.c.cap;

@@ -9,46 +9,49 @@
 namespace sfa {
 namespace paged {
 
-// The last index s in [0, n) with first(s) <= x, where first() does not
-// decrease and first(0) <= x is assumed (0 otherwise); the whole warp asks for
-// the same x.  A 32-way search: two rounds of loads up to 1024 entries.
-template <typename F>
-__device__ __forceinline__ int last_at_most(int n, int x, F first) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, len = n;
-    while (len > 1) {
-        const int step = (len + 31) >> 5;
-        const int at = lane * step;
-        const bool le = at < len && first(lo + at) <= x;
-        const int last = max(31 - __clz(__ballot_sync(kFull, le)), 0);  // -1 with no lane set
-        lo += last * step;
-        len = min(step, len - last * step);
-    }
-    return lo;
+// A sequence, its first and its last row's successor and its length.
+struct Where {
+    int s, start, end, len;
+};
+
+// Those of sequence s, loaded together, used or not: a chain of dependent
+// lookups is what a short step's time consists of.
+__device__ __forceinline__ Where look(const PagedArgs& c, int s) {
+    const Where x = {s, fresh(c.cu + s), fresh(c.cu + s + 1), fresh(c.lens + s)};
+    asm volatile("" ::"r"(x.start), "r"(x.end), "r"(x.len));  // none of the loads moves behind a branch
+    return x;
 }
 
-// The sequence that token row t belongs to, or S when it belongs to none, with
-// its last row's successor and its length (the whole warp asks for the same t).
-// A step in which every sequence brings one token is found at once.  The three
-// words are loaded together, used or not: a chain of dependent lookups is what
-// a decode step's time consists of.
-struct Where {
-    int s, end, len;
-};
-__device__ __forceinline__ Where sequence_of(const PagedArgs& c, int t) {
-    auto there = [&](int s, int& start) {
-        start = fresh(c.cu + s);
-        const Where x = {s, fresh(c.cu + s + 1), fresh(c.lens + s)};
-        asm volatile("" ::"r"(start), "r"(x.end), "r"(x.len));  // none of the loads moves behind a branch
-        return x;
-    };
-    int start;
-    if (t < c.S) {
-        const Where x = there(t, start);
-        if (start == t && x.end == t + 1) return x;
+// The last sequence s with first(cu[s], s) <= x, where first() does not
+// decrease with s and is at most x for s = 0 (sequence 0 otherwise); the whole
+// warp asks for the same x.  A 32-way search: one round of loads up to 32
+// sequences, two up to 1024.
+template <typename F>
+__device__ __forceinline__ Where last_at_most(const PagedArgs& c, int x, F first) {
+    const int lane = threadIdx.x & 31;
+    auto last = [](bool le) { return max(31 - __clz(__ballot_sync(kFull, le)), 0); };  // -1 with no lane set
+    int lo = 0, len = c.S;
+    while (len > 32) {
+        const int step = (len + 31) >> 5, at = lane * step;
+        const int k = last(at < len && first(fresh(c.cu + lo + min(at, len - 1)), lo + at) <= x);
+        lo += k * step;
+        len = min(step, len - k * step);
     }
-    Where x = there(last_at_most(c.S, t, [&](int i) { return fresh(c.cu + i); }), start);
-    if (t < start || t >= x.end) x.s = c.S;
+    const Where y = look(c, lo + min(lane, len - 1));
+    const int k = last(lane < len && first(y.start, lo + lane) <= x);
+    return Where{lo + k, __shfl_sync(kFull, y.start, k), __shfl_sync(kFull, y.end, k), __shfl_sync(kFull, y.len, k)};
+}
+
+// The sequence that token row t belongs to, or S when it belongs to none (the
+// whole warp asks for the same t).  A step in which every sequence brings one
+// token is found at once.
+__device__ __forceinline__ Where sequence_of(const PagedArgs& c, int t) {
+    if (t < c.S) {
+        const Where x = look(c, t);
+        if (x.start == t && x.end == t + 1) return x;
+    }
+    Where x = last_at_most(c, t, [](int start, int) { return start; });
+    if (t < x.start || t >= x.end) x.s = c.S;
     return x;
 }
 

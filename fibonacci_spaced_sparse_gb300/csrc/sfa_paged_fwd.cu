@@ -382,12 +382,13 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_c
     const int slot = (int)(blockIdx.x / kHkv) * kQuadWarps + warp;
     Quad Q;
     Q.g = blockIdx.x % kHkv;
-    Q.s = paged::last_at_most(P.c.S, slot, [&](int i) { return (fresh(P.c.cu + i) >> 2) + i; });
-    const int start = fresh(P.c.cu + Q.s), end = fresh(P.c.cu + Q.s + 1);
-    Q.t0 = start + 4 * (slot - (start >> 2) - Q.s);
+    const paged::Where x = paged::last_at_most(P.c, slot, [](int start, int s) { return (start >> 2) + s; });
+    const int end = x.end;
+    Q.s = x.s;
+    Q.t0 = x.start + 4 * (slot - (x.start >> 2) - x.s);
     if (Q.t0 < 0 || Q.t0 >= P.c.N || Q.t0 >= end) return;
     Q.cnt = min(4, min(end, P.c.N) - Q.t0);
-    Q.i0 = fresh(P.c.lens + Q.s) - (end - Q.t0);       // position of the first query
+    Q.i0 = x.len - (end - Q.t0);                       // position of the first query
     Q.last = min(Q.i0 + Q.cnt, P.c.cap) - 1;           // no row behind it is read
     Q.rn = rn;
     Q.rc = rc;

@@ -151,11 +151,12 @@ __device__ __forceinline__ Work work_of(const PagedFwd& P, const int* rc, int sl
     const int lane = threadIdx.x & 31;
     Work x;
     x.g = 0;
-    x.s = paged::last_at_most(P.c.S, slot, [&](int i) { return fresh(P.c.cu + i) / kTQ + i; });
-    const int start = fresh(P.c.cu + x.s), end = fresh(P.c.cu + x.s + 1);
+    const paged::Where w = paged::last_at_most(P.c, slot, [](int start, int s) { return start / kTQ + s; });
+    const int start = w.start, end = w.end;
+    x.s = w.s;
     x.t0 = start + kTQ * (slot - start / kTQ - x.s);
     x.cnt = x.t0 < 0 || x.t0 >= P.c.N || x.t0 >= end ? 0 : min(kTQ, min(end, P.c.N) - x.t0);
-    x.i0 = fresh(P.c.lens + x.s) - (end - x.t0);
+    x.i0 = w.len - (end - x.t0);
     x.last = min(x.i0 + x.cnt, P.c.cap) - 1;
     x.used = __popc(__ballot_sync(kFull, rc[lane] <= x.last));
     x.groups = (x.used + 3) >> 2;
@@ -480,7 +481,7 @@ __device__ __noinline__ void redo_query(const PagedFwd& P, const Shared& S, int 
     if (x.s >= P.c.S) return;
     Quad Q;
     Q.s = x.s;
-    const int only = (t - fresh(P.c.cu + x.s)) & 3;
+    const int only = (t - x.start) & 3;
     Q.t0 = t - only;
     Q.cnt = min(4, min(x.end, P.c.N) - Q.t0);
     Q.i0 = x.len - (x.end - Q.t0);
