@@ -62,6 +62,15 @@ __device__ __forceinline__ int page_row(const PagedArgs& c, int s, int pos) {
     return (unsigned)page < (unsigned)c.num_pages ? (page << c.shift) + (pos & ((1 << c.shift) - 1)) : -1;
 }
 
+// The same where it is wanted, -1 elsewhere (pos may be anything there).  No
+// branch, so that several lookups are on their way together; an unwanted one
+// reads the sequence's first entry.
+__device__ __forceinline__ int page_row_if(const PagedArgs& c, int s, int pos, bool want) {
+    const int page = fresh(c.table + (size_t)s * c.max_pages + (want ? pos >> c.shift : 0));
+    const bool in = want && (unsigned)page < (unsigned)c.num_pages;
+    return in ? (page << c.shift) + (pos & ((1 << c.shift) - 1)) : -1;
+}
+
 __device__ __forceinline__ void report(unsigned* status) {
     if (status) atomicOr(status, SFA_DEVSTAT_BAD_INDEX);
 }

@@ -357,14 +357,19 @@ cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
 
 // ------------------------------------------------- many tokens: tensor cores
 
-constexpr int kQuadWarps = 4;
+// Two tiles of rows on their way or in use, at 168 registers (12 warps a SM), or
+// four (kDeep) at 255 (8 warps).
+constexpr int kQuadWarps = 4, kDeepSlots = 152 * 2 * kQuadWarps / kHkv;
 
-// A call of its own, so that the rare pass takes no registers of the common one.
+// A call of its own, so that the rare pass takes no registers of the common one
+// (and one for each kernel: they differ in their registers).
+template <bool kDeep>
 __device__ __noinline__ void one_alone(const PagedFwd& P, const Quad& Q, int only) {
     quad_pass<true, false>(P, Q, only);
 }
 
-__global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_constant__ PagedFwd P) {
+template <bool kDeep>
+__global__ void __launch_bounds__(kQuadWarps * 32, kDeep ? 2 : 3) quad_kernel(const __grid_constant__ PagedFwd P) {
     __shared__ int rn[SFA_MAX_RUNGS], rc[SFA_MAX_RUNGS];
     __shared__ float rt[SFA_MAX_RUNGS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -395,8 +400,8 @@ __global__ void __launch_bounds__(kQuadWarps * 32, 3) quad_kernel(const __grid_c
     Q.rt = rt;
     if (__any_sync(kFull, lane < Q.cnt && (Q.i0 + lane < 0 || Q.i0 + lane >= P.c.cap)) && lane == 0)
         paged::report(P.c.status);
-    for (unsigned redo = quad_pass<false, false>(P, Q, -1); redo; redo &= redo - 1)
-        one_alone(P, Q, __ffs(redo) - 1);
+    for (unsigned redo = quad_pass<false, false, kDeep>(P, Q, -1); redo; redo &= redo - 1)
+        one_alone<kDeep>(P, Q, __ffs(redo) - 1);
 }
 
 cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
@@ -410,7 +415,8 @@ cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, quad_kernel, P);
+    void (*const kernel)(PagedFwd) = slots <= kDeepSlots ? quad_kernel<true> : quad_kernel<false>;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
     if (e == cudaSuccess) count_launch();
     return e;
 }

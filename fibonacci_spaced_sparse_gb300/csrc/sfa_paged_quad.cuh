@@ -260,10 +260,18 @@ struct Quad {
     const float* rt;
 };
 
+// A rung tile's entry as a thread sees it: the fraction, and for its query of
+// each pair whether the rung is an entry of it.
+struct Entry {
+    float frac;
+    bool ok[2];
+};
+
 // All queries of the quad, or the query `only` alone; returns the queries
 // whose results are not finite (they are not written).  kNatural: the sums of
-// the scores run over the dimensions in their natural order.
-template <bool kAlone, bool kNatural>
+// the scores run over the dimensions in their natural order.  kDeep: four tiles
+// of rows in registers instead of two.
+template <bool kAlone, bool kNatural, bool kDeep = false>
 __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, int only) {
     const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
     const int W = P.a.W, i0 = Q.i0, last = Q.last;
@@ -272,22 +280,22 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
     const char* vb = static_cast<const char*>(P.c.v) + Q.g * (kD * 2);
     // this lane's row of the window: position i0 - W + lane
     bool want = lane < W + 4 && i0 - W + lane >= 0 && i0 - W + lane <= last && (!kAlone || (lane >= only && lane <= only + W));
-    int wrow = want ? paged::page_row(P.c, Q.s, i0 - W + lane) : -1;
+    const int wrow = paged::page_row_if(P.c, Q.s, i0 - W + lane, want);
     bool bad = want && wrow < 0;
-    const int fill = kAlone ? -1 : max(__shfl_sync(kFull, wrow, W), 0);  // the first query's own row
     // rungs that the last query uses: a prefix, four to a tile
     const int nt = (__popc(__ballot_sync(kFull, Q.rc[lane] <= last)) + 3) >> 2;
     // this lane's row of a rung tile: lanes 0-15 the first pair's, 16-31 the second's
     const int my_q = 2 * (lane >> 4) + ((lane >> 2) & 1);
     const bool near_row = lane & 8;
-    unsigned there = 0;  // rows of the tile that are there, where pages are bad
     auto rung_rows = [&](int t) {
         const int r = 4 * t + (lane & 3), i = i0 + my_q;
         const bool w = i <= last && i >= Q.rc[r] && (near_row || Q.rt[r] > 0.f) && (!kAlone || my_q == only);
-        const int row = w ? paged::page_row(P.c, Q.s, i - Q.rn[r] - (near_row ? 0 : 1)) : -1;
+        const int row = paged::page_row_if(P.c, Q.s, i - Q.rn[r] - (near_row ? 0 : 1), w);
         bad |= w && row < 0;
         return row;
     };
+    int row = nt > 0 ? rung_rows(0) : -1, next = kDeep && nt > 1 ? rung_rows(1) : -1;
+    const int fill = kAlone ? -1 : max(__shfl_sync(kFull, wrow, W), 0);  // the first query's own row
     Pair U[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -325,37 +333,68 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
         for (int e = 0; e < 8; ++e)
             if (!(w >> (16 * (e >> 2) + 8 * (e & 1) + g8) & 1u)) mask[e >> 2] &= ~(1u << (e & 3));
     }
-    // two tiles in turn: one is loaded while the other is used
-    Tile A, B;
-    load_tile<kAlone, kNatural>(kb, vb, wrow >= 0 ? wrow : fill, 0, A);
-    int row = nt > 0 ? rung_rows(0) : -1;
-    if (W > 12) {
-        load_tile<kAlone, kNatural>(kb, vb, wrow >= 0 ? wrow : fill, 16, B);
-        window_tile<true>(A, mask[0], sl2, U);
-        if (nt > 0) load_tile<kAlone, kNatural>(kb, vb, row >= 0 ? row : fill, 0, A);
-        window_tile<false>(B, mask[1], sl2, U);
-    } else {
-        if (nt > 0) load_tile<kAlone, kNatural>(kb, vb, row >= 0 ? row : fill, 0, B);
-        window_tile<true>(A, mask[0], sl2, U);
-        A = B;
-    }
     const int my_i = (g8 >> 2) == (tig >> 1) ? i0 + (tig >> 1) : -(1 << 30);  // its own rung's query, or none
-    for (int t = 0; t < nt; ++t) {
-        load_tile<kAlone, kNatural>(kb, vb, row >= 0 ? row : fill, 16, B);
-        const bool holes = __any_sync(kFull, bad);
-        if (holes) there = __ballot_sync(kFull, row >= 0);
-        const float frac = Q.rt[4 * t + (g8 & 3)];
+    auto load = [&](int r, int half, Tile& x) { load_tile<kAlone, kNatural>(kb, vb, r >= 0 ? r : fill, 16 * half, x); };
+    // of rung tile t with the rows r
+    auto entry_of = [&](int t, int r) {
+        Entry y;
+        y.frac = Q.rt[4 * t + (g8 & 3)];
         const int c = Q.rc[4 * t + (g8 & 3)];
-        bool ok[2] = {my_i >= c, my_i + 2 >= c};
-        if (holes) {
+        y.ok[0] = my_i >= c;
+        y.ok[1] = my_i + 2 >= c;
+        if (__any_sync(kFull, bad)) {
+            const unsigned there = __ballot_sync(kFull, r >= 0);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                ok[k] = ok[k] && (there >> (16 * k + 8 + g8) & 1u) && ((there >> (16 * k + g8) & 1u) || frac == 0.f);
+                y.ok[k] = y.ok[k] && (there >> (16 * k + 8 + g8) & 1u) && ((there >> (16 * k + g8) & 1u) || y.frac == 0.f);
         }
-        row = t + 1 < nt ? rung_rows(t + 1) : -1;
-        rung_tiles<1>(&A, ok, frac, sl2, U);
-        if (t + 1 < nt) load_tile<kAlone, kNatural>(kb, vb, row >= 0 ? row : fill, 0, A);
-        rung_tiles<1>(&B, ok + 1, frac, sl2, U + 1);
+        return y;
+    };
+    if constexpr (kDeep) {
+        // both pairs' tiles of four rungs are loaded while those before are used
+        Tile A[2], B[2];
+        auto use = [&](const Tile(&x)[2], int t, int r) {
+            const Entry y = entry_of(t, r);
+            rung_tiles<2>(x, y.ok, y.frac, sl2, U);
+        };
+        load(wrow, 0, B[0]);
+        if (W > 12) load(wrow, 1, B[1]);
+        if (nt > 0) load(row, 0, A[0]), load(row, 1, A[1]);
+        window_tile<true>(B[0], mask[0], sl2, U);
+        if (W > 12) window_tile<false>(B[1], mask[1], sl2, U);
+        for (int t = 0; t < nt; t += 2) {
+            if (t + 1 < nt) load(next, 0, B[0]), load(next, 1, B[1]);
+            const int after = t + 2 < nt ? rung_rows(t + 2) : -1;
+            use(A, t, row);
+            if (t + 1 >= nt) break;
+            if (t + 2 < nt) load(after, 0, A[0]), load(after, 1, A[1]);
+            row = after;
+            const int r = next;
+            next = t + 3 < nt ? rung_rows(t + 3) : -1;
+            use(B, t + 1, r);
+        }
+    } else {
+        // two tiles in turn: one is loaded while the other is used
+        Tile A, B;
+        load(wrow, 0, A);
+        if (W > 12) {
+            load(wrow, 1, B);
+            window_tile<true>(A, mask[0], sl2, U);
+            if (nt > 0) load(row, 0, A);
+            window_tile<false>(B, mask[1], sl2, U);
+        } else {
+            if (nt > 0) load(row, 0, B);
+            window_tile<true>(A, mask[0], sl2, U);
+            A = B;
+        }
+        for (int t = 0; t < nt; ++t) {
+            load(row, 1, B);
+            const Entry y = entry_of(t, row);
+            row = t + 1 < nt ? rung_rows(t + 1) : -1;
+            rung_tiles<1>(&A, y.ok, y.frac, sl2, U);
+            if (t + 1 < nt) load(row, 0, A);
+            rung_tiles<1>(&B, y.ok + 1, y.frac, sl2, U + 1);
+        }
     }
     if (__any_sync(kFull, bad) && lane == 0) paged::report(P.c.status);
     unsigned redo = 0;
