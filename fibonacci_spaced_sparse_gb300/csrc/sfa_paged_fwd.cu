@@ -358,7 +358,9 @@ cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
 // ------------------------------------------------- many tokens: tensor cores
 
 // Two tiles of rows on their way or in use, at 168 registers (12 warps a SM), or
-// four (kDeep) at 255 (8 warps).
+// four (kDeep) at 242 (8 warps), where that keeps every warp resident (us, two and
+// four: one chunk of 512 tokens 4.4 and 4.2, of 2048 7.0 and 5.6; of 3100 6.8 and
+// 9.3, 512 chunks of 2 5.7 and 8.2, 1000 of 16 43 and 49).
 constexpr int kQuadWarps = 4, kDeepSlots = 152 * 2 * kQuadWarps / kHkv;
 
 // A call of its own, so that the rare pass takes no registers of the common one
@@ -404,8 +406,11 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kDeep ? 2 : 3) quad_kernel(co
         one_alone<kDeep>(P, Q, __ffs(redo) - 1);
 }
 
+// Slots of four queries at most (quad_kernel has their places).
+long long quad_slots(const PagedArgs& c) { return (long long)c.N / 4 + c.S; }
+
 cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
-    const long long slots = (long long)P.c.N / 4 + P.c.S;
+    const long long slots = quad_slots(P.c);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((slots + kQuadWarps - 1) / kQuadWarps * kHkv));
     cfg.blockDim = dim3(kQuadWarps * 32);
@@ -423,19 +428,20 @@ cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
 
 // Token rows from which the quad kernel is taken, if there are two a sequence at
 // least: where the rows kernel has less than four warps a token (us, rows and
-// quads: 300 tokens in chunks of 2 4.6 and 5.1, in one 4.3 and 4.3; 320 5.8 and
-// 5.5, 5.4 and 4.5; 500 6.1 and 5.9, 5.5 and 4.3; 8 chunks of 256 11.5 and 6.9).
+// quads: 300 tokens in chunks of 2 4.6 and 4.7, in one 4.2 and 3.9; 320 5.8 and
+// 4.7, 5.4 and 3.9; 8 chunks of 256 11.5 and 5.4).
 // Single tokens stay with the rows kernel (2048 of them 15.4 and 24.1).
 constexpr int kQuadsFrom = 305;
 
-// Token rows from which the tile kernel is taken, in pages that hold 16 rows at
-// least: tiles of 28 want long chunks (us, quads and tiles: one chunk of 2048
-// tokens 7.0 and 6.8, of 3500 7.1 and 6.9, of 4096 11.6 and 7.1, of 8192 17.9
-// and 10.6 -- below the quads' second wave the tiles' maps cost the host more
-// than they save; 128 chunks of 32 14.2 and 11.2, 300 of 24 25.2 and 21.7, 256
-// of 16 15.2 and 15.5; 8 chunks of 512 beside 56 single tokens 13.2 and 11.4,
-// beside 192 13.4 and 17.1).
-constexpr int kTilesFrom = 3200, kTilesEach = 28;
+// The tile kernel is taken, in pages that hold 16 rows at least, where the quad
+// kernel's slots are more than one wave of its blocks and chunks are long: tiles
+// of 28 want 32 tokens a sequence (us, quads and tiles: one chunk of 2048 tokens
+// 5.5 and 6.5, of 3500 6.7 and 7.0, of 4096 10.0 and 7.1, of 8192 16.2 and 10.6;
+// after 1000 rows each, 128 chunks of 32 11.0 and 10.2, 1000 of 40 82 and 50, 200
+// of 28 14.6 and 16.5, 256 of 16 12.2 and 13.1; 8 chunks of 512 beside 56 single
+// tokens 8.7 and 8.9, beside 192 9.1 and 13.3).  A smaller call would wait for
+// the host besides, which makes the tiles' maps in 3 us.
+constexpr int kQuadsWave = 152 * 3 * kQuadWarps / kHkv, kTilesEach = 32;
 
 }  // namespace
 
@@ -445,7 +451,8 @@ cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype d
     // the tensor-core kernels load 32 bytes of a row at a time
     const bool wide = ((reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) & 31u) == 0;
     if (dt == SFA_BF16 && a.W <= 28 && wide) {
-        if (c.N >= kTilesFrom && c.N >= kTilesEach * (long long)c.S && c.shift >= 4) return launch_paged_tiles(P, s);
+        if (quad_slots(c) > kQuadsWave && c.N >= kTilesEach * (long long)c.S && c.shift >= 4)
+            return launch_paged_tiles(P, s);
         if (c.N >= kQuadsFrom && c.N >= 2 * (long long)c.S) return launch_quads(P, s);
     }
     return dt == SFA_BF16 ? launch_rows<__nv_bfloat16>(P, s) : launch_rows<float>(P, s);

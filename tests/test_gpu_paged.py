@@ -18,7 +18,7 @@ ONE = [(1, 0)]
 SINGLES = [(1, c) for c in (0, 1, 7, 8, 12, 13, 20, 21, 89, 144, 986, 987, 1300)]
 RAGGED = [(5, 0), (0, 33), (1, 21), (37, 95), (0, 0), (2, 1000), (130, 3), (1, 0)]
 CHUNK = [(203, 0)]
-# enough tokens for the kernel of long chunks (3200, and 28 a sequence)
+# enough tokens for the kernel of long chunks (more than 3648, and 32 a sequence)
 LONG = [(1803, 70), (0, 9), (2402, 0), (1, 1200), (33, 986)]
 MANY = [(0, 5)] * 3 + [(1, 40 + s) for s in range(40)] + [(3, 0)] * 5 + [(0, 0)] * 2
 
@@ -585,7 +585,8 @@ def test_lookups_written_by_the_launch_before():
 
 @pytest.mark.parametrize("lens,behind", [([(304, 5)], 0), ([(304, 5)], 1), ([(2, 30 + 5 * s) for s in range(152)], 0),
                                          ([(2, 30 + 5 * s) for s in range(153)], 0),
-                                         ([(1, 0)] * 20 + [(290, 100)] + [(1, 5)] * 9, 2), ([(500, 9)], 0)])
+                                         ([(1, 0)] * 20 + [(290, 100)] + [(1, 5)] * 9, 2), ([(500, 9)], 0),
+                                         ([(2428, 40)], 0), ([(2432, 40)], 0), ([(3644, 9)], 0), ([(3648, 9)], 0)])
 def test_where_the_kernels_change(lens, behind):
     """Token rows on both sides of where the kernels take over from one another."""
     cache = Cache(lens, 16, "bf16", seed=70 + len(lens) + behind, behind=behind)
