@@ -265,12 +265,14 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const void* dqhat = dense(tensor(a[8], "dqhat"), "dqhat", x.q.sizes(), type, x.q);
         const void* dkhat = dense(tensor(a[9], "dkhat"), "dkhat", x.k.sizes(), type, x.q);
         Tensor scratch;
-        void* ws;
+        void* ws = nullptr;
         size_t bytes;
         if (a[10] == Py_None) {
             bytes = sfa_qk_norm_rope_backward_workspace_size(&x.p);
-            scratch = empty({(int64_t)bytes}, at::kByte, x.q);
-            ws = scratch.data_ptr();
+            if (bytes) {
+                scratch = empty({(int64_t)bytes}, at::kByte, x.q);
+                ws = scratch.data_ptr();
+            }
         } else {
             const Tensor& t = tensor(a[10], "workspace");
             if (t.device() != x.q.device() || !t.is_contiguous())

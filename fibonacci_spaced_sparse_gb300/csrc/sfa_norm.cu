@@ -157,17 +157,31 @@ constexpr int kBwdBlocks = 152 * (sizeof(T) == 2 ? 3 : 2);
 constexpr int kMaxBlocks = 152 * 3;  // partial sums of dw
 constexpr int kPartial = 2 * kD;     // floats of one: dwq, dwk
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at this address in the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ float cluster_load(const float* p, unsigned rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
 // Block b writes dx of its tokens (b, b + gridDim, ... in groups of kTok) and
 // its part of dwq, dwk to partial[b]; dw is summed by the launch after it, in
 // a fixed order.  (Copies ahead through shared memory, as in the forward, are
 // no faster here: 27.3 against 26.4 us for 32 x 1024 bf16 tokens, 75 against
 // 48 us in fp32.)
-template <typename T>
+// kCluster: the grid is one cluster of blocks, whose parts are summed through
+// distributed shared memory by its first block, dw = partial: one launch.
+template <typename T, bool kCluster>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks<T> / 152)
-    norm_bwd_kernel(const NormArgs a, const T* dqhat, const T* dkhat, T* dq, T* dk, float* partial) {
+    norm_bwd_kernel(const NormArgs a, const T* dqhat, const T* dkhat, T* dq, T* dk, float* partial, float* dwk) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ float sums[kTok * kPairsOfHeads][kD + 1];
+    __shared__ float sums[kTok * kPairsOfHeads][kD + 1], part[kCluster ? kPartial : 1];
     const int quad = threadIdx.x >> 2, c = threadIdx.x & 3, hp = quad % kPairsOfHeads;
     const Rows<const T> in = inputs<T>(a, hp), up = dense(dqhat, dkhat, hp);
     const Rows<T> out = dense(dq, dk, hp);
@@ -233,7 +247,19 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks<T> / 152)
                 s += sums[tk * kPairsOfHeads + kHq / 2][d];
             }
         }
-        partial[(size_t)blockIdx.x * kPartial + threadIdx.x] = s;
+        if (kCluster)
+            part[threadIdx.x] = s;
+        else
+            partial[(size_t)blockIdx.x * kPartial + threadIdx.x] = s;
+    }
+    if (kCluster) {
+        cluster_sync();
+        if (blockIdx.x == 0 && threadIdx.x < kPartial) {
+            float s = 0.f;
+            for (unsigned b = 0; b < gridDim.x; ++b) s += cluster_load(&part[threadIdx.x], b);
+            (threadIdx.x < kD ? partial : dwk)[threadIdx.x & (kD - 1)] = s;
+        }
+        cluster_sync();  // no block's shared memory goes before it has been read
     }
 }
 
@@ -269,18 +295,21 @@ __global__ void __launch_bounds__(kFinCols* kFinRows) norm_dw_kernel(const float
     }
 }
 
-template <typename... P, typename... A>
+// cluster: the grid is one cluster.
+template <bool kCluster = false, typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {grid, 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = kCluster ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e == cudaSuccess) count_launch();
     return e;
@@ -318,22 +347,41 @@ cudaError_t launch_norm_fwd(const NormArgs& a, sfa_dtype dt, void* qhat, void* k
                   (__nv_bfloat16*)khat);
 }
 
-size_t norm_bwd_workspace() { return (size_t)kMaxBlocks * kPartial * sizeof(float); }
+// Tokens up to which one cluster of blocks does the backward pass in one launch:
+// a step of eight blocks (us, two launches and one: 8 tokens 3.5 and 2.9, 64 3.5
+// and 3.2, 128 3.6 and 4.4; the host's 3 us for the other launch and the
+// workspace come to it).
+constexpr int kClusterBlocks = 8, kClusterTo = kClusterBlocks * kTok;
 
-cudaError_t launch_norm_bwd(const NormArgs& a, sfa_dtype dt, const void* dqhat, const void* dkhat, void* dq, void* dk,
-                            float* dwq, float* dwk, void* ws, cudaStream_t s) {
-    const unsigned most = (unsigned)(dt == SFA_BF16 ? kBwdBlocks<__nv_bfloat16> : kBwdBlocks<float>);
-    const unsigned blocks = steps_of(a.N) < most ? steps_of(a.N) : most;
+size_t norm_bwd_workspace(long long N) {
+    return N <= kClusterTo ? 0 : (size_t)kMaxBlocks * kPartial * sizeof(float);
+}
+
+namespace {
+
+template <typename T>
+cudaError_t launch_bwd(const NormArgs& a, const void* dqhat, const void* dkhat, void* dq, void* dk, float* dwq,
+                       float* dwk, void* ws, cudaStream_t s) {
+    const T *gq = static_cast<const T*>(dqhat), *gk = static_cast<const T*>(dkhat);
+    T *oq = static_cast<T*>(dq), *ok = static_cast<T*>(dk);
+    const unsigned steps = steps_of(a.N);
+    if (a.N <= kClusterTo)
+        return launch<true>(norm_bwd_kernel<T, true>, steps, kThreads, 0, s, a, gq, gk, oq, ok, dwq, dwk);
+    const unsigned blocks = steps < (unsigned)kBwdBlocks<T> ? steps : (unsigned)kBwdBlocks<T>;
     float* partial = static_cast<float*>(ws);
     const cudaError_t e =
-        dt == SFA_BF16
-            ? launch(norm_bwd_kernel<__nv_bfloat16>, blocks, kThreads, 0, s, a, (const __nv_bfloat16*)dqhat,
-                     (const __nv_bfloat16*)dkhat, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, partial)
-            : launch(norm_bwd_kernel<float>, blocks, kThreads, 0, s, a, (const float*)dqhat, (const float*)dkhat,
-                     (float*)dq, (float*)dk, partial);
+        launch(norm_bwd_kernel<T, false>, blocks, kThreads, 0, s, a, gq, gk, oq, ok, partial, (float*)nullptr);
     if (e != cudaSuccess) return e;
     return launch(norm_dw_kernel, (unsigned)(kPartial / kFinCols), (unsigned)(kFinCols * kFinRows), 0, s,
                   (const float*)partial, (int)blocks, dwq, dwk);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_bwd(const NormArgs& a, sfa_dtype dt, const void* dqhat, const void* dkhat, void* dq, void* dk,
+                            float* dwq, float* dwk, void* ws, cudaStream_t s) {
+    return dt == SFA_BF16 ? launch_bwd<__nv_bfloat16>(a, dqhat, dkhat, dq, dk, dwq, dwk, ws, s)
+                          : launch_bwd<float>(a, dqhat, dkhat, dq, dk, dwq, dwk, ws, s);
 }
 
 }  // namespace sfa

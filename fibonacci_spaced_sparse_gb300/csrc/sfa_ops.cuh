@@ -28,7 +28,7 @@ struct NormArgs {
     unsigned* status;
 };
 cudaError_t launch_norm_fwd(const NormArgs& a, sfa_dtype dt, void* qhat, void* khat, cudaStream_t s);
-size_t norm_bwd_workspace();
+size_t norm_bwd_workspace(long long N);  // N tokens; 0: none
 cudaError_t launch_norm_bwd(const NormArgs& a, sfa_dtype dt, const void* dqhat, const void* dkhat, void* dq, void* dk,
                             float* dwq, float* dwk, void* ws, cudaStream_t s);
 

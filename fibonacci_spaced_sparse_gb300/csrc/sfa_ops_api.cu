@@ -147,7 +147,7 @@ SFA_API sfa_status sfa_qk_norm_rope(const sfa_params* p, const void* Q, long lon
 
 SFA_API size_t sfa_qk_norm_rope_backward_workspace_size(const sfa_params* p) {
     if (validate(p) != SFA_OK || p->B == 0 || p->T == 0) return 0;
-    return sfa::norm_bwd_workspace();
+    return sfa::norm_bwd_workspace((long long)p->B * p->T);
 }
 
 SFA_API sfa_status sfa_qk_norm_rope_backward(const sfa_params* p, const void* Q, long long q_stride, const void* K,
@@ -173,7 +173,8 @@ SFA_API sfa_status sfa_qk_norm_rope_backward(const sfa_params* p, const void* Q,
     const void* ptrs[] = {dQhat, dKhat, dQ, dK};
     for (const void* x : ptrs)
         if (!x || !aligned16(x)) return SFA_ERR_INVALID_ARG;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < sfa::norm_bwd_workspace())
+    const size_t need = sfa::norm_bwd_workspace(a.N);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need))
         return SFA_ERR_INVALID_ARG;
     if (sfa::fault_injected()) return SFA_ERR_CUDA;
     return launched(sfa::launch_norm_bwd(a, p->dtype, dQhat, dKhat, dQ, dK, dwq, dwk, workspace, stream));

@@ -380,7 +380,7 @@ SFA_API sfa_status sfa_qk_norm_rope(const sfa_params *p, const void *Q, long lon
                                     const float *rope_table, int table_rows, void *Qhat,
                                     void *Khat, unsigned int *status, cudaStream_t stream);
 
-/* Bytes of device workspace sfa_qk_norm_rope_backward needs. */
+/* Bytes of device workspace sfa_qk_norm_rope_backward needs (0: none, few tokens). */
 SFA_API size_t sfa_qk_norm_rope_backward_workspace_size(const sfa_params *p);
 
 /* Gradients of a scalar loss through sfa_qk_norm_rope, given dQhat and dKhat
@@ -392,10 +392,11 @@ SFA_API size_t sfa_qk_norm_rope_backward_workspace_size(const sfa_params *p);
  *     forward; dQ, dK: contiguous, p->dtype, fully overwritten;
  *   dwq, dwk: D fp32 each, overwritten (zeros when B * T = 0);
  *   workspace: device, 256-byte aligned, contents ignored on entry and
- *     clobbered; two calls that may overlap need one each.
+ *     clobbered; two calls that may overlap need one each; NULL where none is
+ *     needed.
  * A token whose position lies outside the table contributes nothing and gets
  * zero gradients.  Sums are fp32 in a fixed order, so results do not change
- * from run to run on one GPU model.  Two launches; allocates nothing.
+ * from run to run on one GPU model.  One or two launches; allocates nothing.
  * Asynchronous on stream. */
 SFA_API sfa_status sfa_qk_norm_rope_backward(const sfa_params *p, const void *Q,
                                              long long q_stride, const void *K,

@@ -51,7 +51,8 @@ def _check_bwd(got, x, w, up, eps, pos, theta, dtype, what):
 
 
 CASES = [(1, 1, "bf16", False), (1, 1, "f32", True), (2, 3, "f32", False), (3, 17, "bf16", True), (1, 255, "bf16", False),
-         (5, 64, "f32", True), (2, 1021, "bf16", True), (257, 1, "bf16", True), (1, 16, "bf16", False)]
+         (5, 64, "f32", True), (2, 1021, "bf16", True), (257, 1, "bf16", True), (1, 16, "bf16", False),
+         (1, 64, "f32", False), (8, 8, "bf16", True), (5, 13, "bf16", False), (65, 1, "f32", True)]
 
 
 @pytest.mark.parametrize("theta", [1e4, 0.0])

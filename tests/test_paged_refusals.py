@@ -87,6 +87,8 @@ def test_norm_backward_refusals(lib):
     p = _p()
     need = lib.sfa_qk_norm_rope_backward_workspace_size(p.ref())
     assert need > 0 and lib.sfa_qk_norm_rope_backward_workspace_size(_p(B=0).ref()) == 0
+    few, more = (lib.sfa_qk_norm_rope_backward_workspace_size(_p(B=1, T=n).ref()) for n in (64, 65))
+    assert few == 0 and more == need
     assert _norm_bwd(lib, nbytes=need - 1) == BAD
     assert _norm_bwd(lib, ws=NULL) == BAD and _norm_bwd(lib, ws=FAKE + 16) == BAD
     assert _norm_bwd(lib, up=NULL) == BAD and _norm_bwd(lib, dq=FAKE + 2) == BAD
@@ -141,7 +143,7 @@ empty = t._p(B=0)
 print(json.dumps([t._norm(lib), t._norm_bwd(lib), t._norm_bwd(lib, p=empty), t._append(lib, t._cache()),
                   t._append(lib, t._cache(), q=None, qh=None, wq=None, wk=None), t._fwd(lib, t._cache()),
                   t._fwd(lib, t._cache(), p=t._p(B=1 << 20, T=1 << 24, rope_theta=0.0)),
-                  t._norm(lib, rows=1, pos=t.FAKE), t._norm(lib, p=t._p(rope_theta=0.0), tab=None, rows=0)]))
+                  t._norm(lib, rows=1, pos=t.FAKE), t._norm(lib, p=t._p(rope_theta=0.0), tab=None, rows=0), t._norm_bwd(lib, p=t._p(B=1), ws=None)]))
 print(json.dumps([t._norm(lib, q=None), t._append(lib, t._cache(k_pages=None)), t._fwd(lib, t._cache(N=0))]))
 """
 
@@ -153,7 +155,7 @@ def test_accepted_calls_reach_the_launch(lib):
     r = subprocess.run([sys.executable, "-c", CHILD], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
     got = [json.loads(x) for x in r.stdout.strip().splitlines()[-2:]]
-    assert got[0] == [_lib.SFA_ERR_CUDA] * 9 and got[1] == [BAD, BAD, OK]
+    assert got[0] == [_lib.SFA_ERR_CUDA] * 10 and got[1] == [BAD, BAD, OK]
 
 
 def test_binding_refuses_before_the_library(lib):
