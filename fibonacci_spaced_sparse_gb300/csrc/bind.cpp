@@ -133,14 +133,26 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& ref) {
     return Tensor(at::detail::empty_cuda(shape, type, ref.device(), std::nullopt));
 }
 
+// Part `i` of `whole`, n values, as a tensor of its own on the same storage (half
+// the price of another allocation).
+Tensor part(const Tensor& whole, int64_t i, int64_t n) {
+    auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                  whole.dtype());
+    t->set_sizes_contiguous({n});
+    t->set_storage_offset(i * n);
+    return Tensor(std::move(t));
+}
+
 // An output: the given one, checked, or a new one.
 struct Out {
     Tensor made;
     PyObject* given;
     void* ptr;
-    Out(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const Tensor& ref) : given(o) {
+    // fresh: the new one, if there is one already
+    Out(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const Tensor& ref, Tensor fresh = {})
+        : given(o) {
         if (o == Py_None) {
-            made = empty(shape, type, ref);
+            made = fresh.defined() ? std::move(fresh) : empty(shape, type, ref);
             ptr = made.data_ptr();
         } else {
             ptr = dense(tensor(o, name), name, shape, type, ref);
@@ -281,7 +293,12 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             bytes = (size_t)t.nbytes();
         }
         Out dq(a[11], "out[0]", x.q.sizes(), type, x.q), dk(a[12], "out[1]", x.k.sizes(), type, x.q);
-        Out dwq(a[13], "out[2]", {kD}, at::kFloat, x.q), dwk(a[14], "out[3]", {kD}, at::kFloat, x.q);
+        Tensor dw[2];
+        if (a[13] == Py_None && a[14] == Py_None) {
+            const Tensor whole = empty({2 * kD}, at::kFloat, x.q);
+            for (int i = 0; i < 2; ++i) dw[i] = part(whole, i, kD);
+        }
+        Out dwq(a[13], "out[2]", {kD}, at::kFloat, x.q, dw[0]), dwk(a[14], "out[3]", {kD}, at::kFloat, x.q, dw[1]);
         check(sfa_qk_norm_rope_backward(&x.p, x.q.data_ptr(), x.qs, x.k.data_ptr(), x.ks, x.wq, x.wk, (float)x.eps,
                                         x.positions, x.rope, small(x.rows), dqhat, dkhat, dq.ptr, dk.ptr,
                                         static_cast<float*>(dwq.ptr), static_cast<float*>(dwk.ptr), ws, bytes,
