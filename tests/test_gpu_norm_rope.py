@@ -317,3 +317,25 @@ def test_captured_training_step():
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
     b = want[4].double().cpu()
     within(got[4], b, 2.0 ** -7 * b.abs() + 2.0 ** -12 * b.abs().max(), "dv")
+
+
+@pytest.mark.parametrize("T", [1, 64, 65])
+def test_few_tokens_captured(T):
+    """The backward pass of few tokens (one launch) and of one more (two), captured
+    with the launch that writes its input and replayed: the eager results."""
+    q, k, wq, wk, g = _draw(1, T, "bf16", True, seed=47)
+    up = [torch.randn((1, T, h, D), generator=g).to(torch.bfloat16).cuda() for h in (HQ, HKV)]
+    want = api.sfa_qk_norm_rope_backward(q, k, wq, wk, *up)
+    given = [torch.zeros_like(x) for x in up]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            for x, y in zip(given, up):
+                x.copy_(y)
+            got = api.sfa_qk_norm_rope_backward(q, k, wq, wk, *given)
+            for x in given:
+                x.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
