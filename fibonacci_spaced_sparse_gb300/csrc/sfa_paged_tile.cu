@@ -26,7 +26,8 @@
 // any other number, 37.8 (44.0 in pages of 16); a map for every height, as here,
 // 35.2 (39.9), and 3 us of the host's time for the maps.  Looking a slot up for
 // both heads at once 34.4 (36.9), and the epilogue below, with both pairs
-// staged at once and fixed addresses, 31.9 (35.1; pages of 256 rows 31.2).
+// staged at once and fixed addresses, 31.9 (35.1; pages of 256 rows 31.2); a
+// search that ends with a sequence's metadata in hand 31.0.
 // 16-byte cp.async by all warps with a barrier an item took 58 (26 M
 // instructions, a third of them copies and lookups).
 //
@@ -66,6 +67,7 @@ constexpr int kQueries = 2 * kWinValues;        // its queries: (query, head) ro
 constexpr int kQueryB = kTQ * kG * kRowB;
 constexpr int kStageB = 2 * kValues;
 constexpr int kStages = 3;
+constexpr int kTaken = 256; // slots that a block takes at most
 constexpr int kRedo = 256;  // queries of a block that are not finite (at least a slot's); past that, all of its queries are redone
 static_assert(kRedo >= kTQ, "a block with one tile never runs over");
 static_assert(kQueries + kQueryB <= kStageB && kQueries % 1024 == 0 && kStageB % 1024 == 0, "stage layout");
@@ -80,12 +82,14 @@ struct Work {
 struct Shared {
     unsigned char stage[kStages][kStageB];
     unsigned char out[kWarps][16 * kRowB];  // a quad's outputs on their way
-    unsigned long long full[kStages], empty[kStages];
+    unsigned long long full[kStages], empty[kStages], asked;
+    uint4 answer;
     // The tile of a window item.  The producer is at most three items ahead of
     // a warp that is done with its tile's last item, so four places are enough.
     Work work[4];
     int holes[kStages];                    // an item has rows in bad pages
     int redo[kRedo], redos;                // token rows x heads to redo alone
+    int taken[kTaken], ntaken;             // this block's slots
     int rn[SFA_MAX_RUNGS], rc[SFA_MAX_RUNGS];
     float rt[SFA_MAX_RUNGS];
     int abort_flag;
@@ -141,6 +145,27 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// Asks for the index of a block of this grid that has not started, which then
+// never does; the answer is 16 bytes that complete on the barrier.
+__device__ __forceinline__ void ask_block(uint32_t answer, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+        "r"(bar)
+        : "memory");
+}
+// That block's index; -1: all have started.
+__device__ __forceinline__ int asked_block(uint32_t answer) {
+    int x;
+    asm volatile(
+        "{\n .reg .b128 h;\n .reg .pred p;\n ld.shared.b128 h, [%1];\n mov.s32 %0, -1;\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n}\n"
+        : "=r"(x)
+        : "r"(answer)
+        : "memory");
+    return x;
+}
+
 // Address of 16-byte chunk c of the row that starts at byte `row` of shared
 // memory (a multiple of 128) under the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(uint32_t row, int c) { return row + ((((uint32_t)c ^ (row >> 7)) & 7u) << 4); }
@@ -192,6 +217,9 @@ __device__ __forceinline__ Part rung_part(const PagedFwd& P, const Shared& S, co
     return part_of(P, x.s, x.i0 - back, from - back, x.last + 1 - back, n);
 }
 
+// kAsk: the block's slots after its own are those of blocks that have not started,
+// one asked for at a time; else those a grid apart.
+template <bool kAsk>
 __device__ void produce(const TileParams& T, Shared& S) {
     const PagedFwd& P = T.f;
     const int lane = threadIdx.x & 31, W = P.a.W;
@@ -235,13 +263,50 @@ __device__ void produce(const TileParams& T, Shared& S) {
         Part win, run[kEarly];
     };
     const int g0 = T.split ? blockIdx.x % kHkv : 0, g1 = T.split ? g0 + 1 : kHkv;
-    int slot = T.split ? blockIdx.x / kHkv : blockIdx.x;
-    const int step = T.split ? gridDim.x / kHkv : gridDim.x;
+    const int step = T.split ? T.slots : gridDim.x;
+    const uint32_t answer = smem_u32(&S.answer), asked = smem_u32(&S.asked);
+    int slot = T.split ? blockIdx.x / kHkv : blockIdx.x, asks = 0, taken = 0;
+    bool waiting = false;
+    auto ask = [&]() {
+        if (!kAsk || taken == kTaken) return;
+        if (lane == 0) {
+            fence_proxy_async();  // the answer before has been read
+            mbar_arrive_expect_tx(asked, sizeof(uint4));
+            ask_block(answer, asked);
+        }
+        waiting = true;
+    };
+    auto next_slot = [&]() {
+        if (!kAsk) return slot + step < T.slots ? slot + step : -1;
+        if (!waiting) return -1;
+        if (!warp_wait(asked, asks & 1, &S.abort_flag)) {
+            ok = false;
+            return -1;
+        }
+        ++asks;
+        waiting = false;
+        const int x = asked_block(answer);
+        __syncwarp();
+        return x;
+    };
     auto plan = [&]() {
         Plan y;
         y.x.cnt = 0;
-        for (; slot < T.slots && y.x.cnt == 0; slot += step) y.x = work_of(P, S.rc, slot);
+        while (slot >= 0 && y.x.cnt == 0) {
+            y.x = work_of(P, S.rc, slot);
+            if (y.x.cnt == 0) {
+                ask();
+                slot = next_slot();
+            }
+        }
         if (y.x.cnt == 0) return y;
+        if (kAsk) {
+            if (lane == 0) {
+                S.taken[taken] = slot;
+                S.ntaken = taken + 1;
+            }
+            ++taken;
+        }
         y.win = part_of(P, y.x.s, y.x.i0 - W, max(0, y.x.i0 - W), y.x.last, lane >> 1);
 #pragma unroll
         for (int k = 0; k < kEarly; ++k) y.run[k] = rung_part(P, S, y.x, 4 * k + p, part);
@@ -255,13 +320,17 @@ __device__ void produce(const TileParams& T, Shared& S) {
         for (int g = g0; ok && g < g1; ++g) {
             Work x = y.x;
             x.g = g;
+            if (g == g1 - 1) ask();
             if (!wait()) break;
             if (lane == 0) S.work[tile & 3] = x;
             fetch(y.win, x, tensor * kWinValues, kQueryB);
             ++tile;
             if (x.groups > 0 && wait()) fetch(y.run[0], x, block, 0u);
             // the next slot is looked up while the warps have these items to work on
-            if (g == g1 - 1) z = plan();
+            if (g == g1 - 1) {
+                slot = next_slot();
+                z = plan();
+            }
 #pragma unroll
             for (int k = 1; k < kEarly; ++k)
                 if (ok && k < x.groups && wait()) fetch(y.run[k], x, block, 0u);
@@ -285,6 +354,7 @@ __device__ void produce(const TileParams& T, Shared& S) {
         // no copy of this block may land after it is gone
         for (int i = max(0, n - kStages); i < n; ++i)
             (void)mbar_wait(full0 + 8 * (i % kStages), (i / kStages) & 1, nullptr);
+        if (kAsk && waiting) (void)mbar_wait(asked, asks & 1, nullptr);
     }
     __syncwarp();
 }
@@ -475,7 +545,9 @@ __device__ bool consume(const TileParams& T, Shared& S) {
     }
 }
 
-// Token row t alone, as the quad that it stands in computes it.
+// Token row t alone, as the quad that it stands in computes it.  (One for each
+// kernel: ptxas ends in a fault over a function that both call.)
+template <bool kAsk>
 __device__ __noinline__ void redo_query(const PagedFwd& P, const Shared& S, int t, int g) {
     const paged::Where x = paged::sequence_of(P.c, t);
     if (x.s >= P.c.S) return;
@@ -493,6 +565,7 @@ __device__ __noinline__ void redo_query(const PagedFwd& P, const Shared& S, int 
     paged::quad_pass<true, true>(P, Q, only);
 }
 
+template <bool kAsk>
 __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant__ TileParams T) {
     extern __shared__ unsigned char raw[];
     Shared& S = *reinterpret_cast<Shared*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
@@ -509,18 +582,19 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
         reinterpret_cast<uint4*>(S.stage)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async();
     if (tid == 0) {
-        S.redos = 0;
+        S.redos = S.ntaken = 0;
         S.abort_flag = 0;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&S.full[i]), 1);
             mbar_init(smem_u32(&S.empty[i]), kWarps);
         }
+        mbar_init(smem_u32(&S.asked), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kWarps) {
-        produce(T, S);
+        produce<kAsk>(T, S);
     } else if (!consume(T, S) && (tid & 31) == 0) {
         S.abort_flag = 1;
         if (T.f.c.status) atomicOr(T.f.c.status, SFA_DEVSTAT_WAIT_TIMEOUT);
@@ -529,13 +603,15 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
     const int redos = S.redos;
     if (redos == 0 || S.abort_flag) return;
     if (redos <= kRedo) {
-        for (int i = warp; i < redos; i += kWarps + 1) redo_query(T.f, S, S.redo[i] / kHkv, S.redo[i] % kHkv);
+        for (int i = warp; i < redos; i += kWarps + 1) redo_query<kAsk>(T.f, S, S.redo[i] / kHkv, S.redo[i] % kHkv);
         return;
     }
     // more than the list holds: only a block that goes through many slots, both heads of each
-    for (int v = blockIdx.x; v < T.slots; v += gridDim.x) {
-        const Work x = work_of(T.f, S.rc, v);
-        for (int i = warp; i < x.cnt * kHkv; i += kWarps + 1) redo_query(T.f, S, x.t0 + i / kHkv, i % kHkv);
+    for (int v = 0;; ++v) {
+        const int slot = kAsk ? v : blockIdx.x + v * gridDim.x;
+        if (slot >= (kAsk ? S.ntaken : T.slots)) break;
+        const Work x = work_of(T.f, S.rc, kAsk ? S.taken[slot] : slot);
+        for (int i = warp; i < x.cnt * kHkv; i += kWarps + 1) redo_query<kAsk>(T.f, S, x.t0 + i / kHkv, i % kHkv);
     }
 }
 
@@ -567,21 +643,31 @@ bool encode_queries(CUtensorMap* m, const void* base, int N, long long stride) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Blocks ask for their slots where chunks are short and rounds few: slots differ
+// in their work there (a chunk's first ones have few rungs, its last one few
+// queries or none), and a round more or less counts.  (us, a grid apart and asked
+// for: 80 chunks of up to 900 tokens after up to 900 40.9 and 36.0, 64 of 512 31.5
+// and 30.2, 50 of 700 34.3 and 32.7; 30 of up to 2000 32.7 and 31.2, but 32 of 1024
+// 30.8 and 31.5, 128 of 1024 102.5 and 105.3, 300 of up to 2000 253 and 255.)
+constexpr int kAskRounds = 6, kAskEach = 800;
+
 }  // namespace
 
 cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
-    static CtxSetting done[64];  // per device: dynamic shared memory allowed
+    const long long slots = (long long)P.c.N / kTQ + P.c.S, most = 152 * 2;
+    const bool ask = slots > most && slots <= kAskRounds * most && P.c.N <= kAskEach * (long long)P.c.S;
+    void (*const kernel)(TileParams) = ask ? tile_kernel<true> : tile_kernel<false>;
+    static CtxSetting done[2][64];  // per kernel and device: dynamic shared memory allowed
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     constexpr size_t smem = sizeof(Shared) + 1024;
-    if (!ctx_setting_holds(done[dev & 63], smem)) {
-        e = cudaFuncSetAttribute(tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(tile_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (!ctx_setting_holds(done[ask][dev & 63], smem)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return e;
-        ctx_setting_done(done[dev & 63], smem);
+        ctx_setting_done(done[ask][dev & 63], smem);
     }
-    const long long slots = (long long)P.c.N / kTQ + P.c.S, most = 152 * 2;
     TileParams T;
     std::memset(&T, 0, sizeof(T));
     T.f = P;
@@ -593,7 +679,7 @@ cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
             return cudaErrorInvalidValue;
     if (!encode_queries(&T.q, P.q, P.c.N, P.qs)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(T.split ? slots * kHkv : slots < most ? slots : most));
+    cfg.gridDim = dim3((unsigned)(T.split ? slots * kHkv : ask || slots < most ? slots : most));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -602,7 +688,7 @@ cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tile_kernel, T);
+    e = cudaLaunchKernelEx(&cfg, kernel, T);
     if (e == cudaSuccess) count_launch();
     return e;
 }

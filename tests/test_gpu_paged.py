@@ -592,3 +592,38 @@ def test_where_the_kernels_change(lens, behind):
     cache = Cache(lens, 16, "bf16", seed=70 + len(lens) + behind, behind=behind)
     kw = dict(alpha=0.87, W=12, rungs=FIB)
     _check(cache, _forward(cache, **kw), attention64(cache, tensor_cores=True, **kw))
+
+
+def test_more_bad_values_than_a_block_lists_in_short_chunks():
+    """The same in many short chunks, whose blocks ask for their slots."""
+    S, n, page = 75, 600, 64
+    each = -(-n // page)
+    g = torch.Generator("cuda").manual_seed(5)
+    kp, vp = (torch.randn((S * each, page, HKV, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    vp.view(-1, HKV, D)[::4, :, 11] = float("nan")
+    q = torch.randn((S * n, HQ, D), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.arange(S * each, dtype=torch.int32, device="cuda").view(S, each)
+    cu = torch.arange(0, S * n + 1, n, dtype=torch.int32, device="cuda")
+    seq = torch.full((S,), n, dtype=torch.int32, device="cuda")
+    o, lse = api.sfa_paged_forward(q, kp, vp, table, cu, seq, alpha=1.0, W=0, rungs=())
+    own = vp.view(S, each * page, HKV, D)[:, :n].reshape(S * n, HKV, D).repeat_interleave(HQ // HKV, 1)
+    assert torch.equal(o.isnan(), own.isnan()) and torch.equal(o.nan_to_num(9.0), own.nan_to_num(9.0))
+    assert bool(lse.isfinite().all())
+
+
+def test_short_chunks_of_one_call():
+    """Ragged chunks over several rounds of blocks, three of them against the
+    definition."""
+    rng = np.random.default_rng(9)
+    lens = [(int(rng.integers(1, 900)), int(rng.integers(0, 900))) for _ in range(60)]
+    cache = Cache(lens, 64, "bf16", seed=90)
+    kw = dict(alpha=0.87, W=12, rungs=FIB)
+    o, lse, status = _forward(cache, **kw)
+    assert status == 0
+    for s in (0, 17, 59):
+        a, b = int(cache.cu[s]), int(cache.cu[s + 1])
+        one = Cache([lens[s]], 64, "bf16", behind=0)
+        one.k, one.v, one.q = [cache.k[s]], [cache.v[s]], cache.q[a:b]
+        ref = attention64(one, tensor_cores=True, **kw)
+        within(o[a:b], ref[0], ref[2], f"o of sequence {s}")
+        within(lse[a:b], ref[1], ref[3], f"lse of sequence {s}")
