@@ -515,7 +515,7 @@ def test_windows_wider_than_any_sequence(W):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and a[2] == 0
 
 
-@pytest.mark.parametrize("lens", [MANY, [(120, 9), (500, 0)], LONG])
+@pytest.mark.parametrize("lens", [MANY, [(120, 9), (500, 0)], LONG, [(300 + s, 40) for s in range(60)]])
 def test_two_calls_at_once(lens):
     """The same entry points on two streams at the same time, each on its own
     cache: the results of one call after the other, bit for bit."""
@@ -627,3 +627,41 @@ def test_short_chunks_of_one_call():
         ref = attention64(one, tensor_cores=True, **kw)
         within(o[a:b], ref[0], ref[2], f"o of sequence {s}")
         within(lse[a:b], ref[1], ref[3], f"lse of sequence {s}")
+
+
+@pytest.mark.parametrize("lens", [MANY, [(120, 9), (500, 0)], [(4, 30)] * 500, LONG, [(300 + s, 40) for s in range(60)]])
+def test_launches_in_a_row_wait_for_one_another(lens):
+    """Append and attention in turn on one buffer of queries, nothing between them:
+    an append that ran into the attention before it would change what that reads."""
+    cache = Cache(lens, 16, "bf16", seed=95)
+    kp, vp = cache.pages()
+    meta = cache.meta()
+    new = [torch.cat([x[s][c:] for s, (_, c) in enumerate(lens)] + [torch.zeros((7, HKV, D), dtype=DT["bf16"])]).cuda()
+           for x in (cache.k, cache.v)]
+    qs = [cache.q.cuda(), cache.q.flip(0).contiguous().cuda()]
+    rope = api.rope_table(4096, "cuda")
+    qo = torch.zeros_like(qs[0])
+    outs = [torch.zeros_like(qo) for _ in range(12)]
+    kw = dict(alpha=0.87, W=12, rungs=FIB, need_lse=False)
+
+    def step(q, o):
+        api.sfa_paged_append(*new, kp, vp, *meta, q=q, q_out=qo, rope=rope)
+        api.sfa_paged_forward(qo, kp, vp, *meta, out=o, **kw)
+
+    want = []
+    for q in qs:
+        o = torch.zeros_like(qo)
+        step(q, o)
+        torch.cuda.synchronize()
+        want.append(o)
+    assert not torch.equal(*want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i, o in enumerate(outs):
+            step(qs[i % 2], o)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want[i % 2]) for i, o in enumerate(outs))
