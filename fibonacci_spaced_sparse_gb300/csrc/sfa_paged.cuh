@@ -15,9 +15,12 @@ struct Where {
 };
 
 // Those of sequence s, loaded together, used or not: a chain of dependent
-// lookups is what a short step's time consists of.
+// lookups is what a short step's time consists of.  A length below 0 counts as
+// 0 (no token's position is then in range, as with the length itself): len -
+// (end - t) and the sums that the kernels form with it cannot pass the lowest
+// int that way and come out as a position that exists.
 __device__ __forceinline__ Where look(const PagedArgs& c, int s) {
-    const Where x = {s, fresh(c.cu + s), fresh(c.cu + s + 1), fresh(c.lens + s)};
+    const Where x = {s, fresh(c.cu + s), fresh(c.cu + s + 1), max(fresh(c.lens + s), 0)};
     asm volatile("" ::"r"(x.start), "r"(x.end), "r"(x.len));  // none of the loads moves behind a branch
     return x;
 }
