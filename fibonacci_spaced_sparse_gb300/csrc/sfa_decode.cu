@@ -57,16 +57,15 @@ __device__ __forceinline__ Entry entry_of(const LayerArgs& a, int i, int e, int 
 
 template <typename T>
 __global__ void __launch_bounds__(kSplit * 32)
-decode_kernel(const LayerArgs a, int Tc, const T* __restrict__ q, const T* __restrict__ kc,
-              const T* __restrict__ vc, const int* __restrict__ pos, const float2* __restrict__ rope,
-              T* __restrict__ o, float* __restrict__ lse, unsigned* __restrict__ status) {
+decode_kernel(const LayerArgs a, int Tc, const T* q, const T* kc, const T* vc, const int* pos,
+              const float2* __restrict__ rope, T* o, float* lse, unsigned* status) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = blockIdx.x % kHkv, b = blockIdx.x / kHkv;
     // the next launch may be scheduled now; this one reads its inputs only
     // once the launch before it has completed
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int i = __ldg(pos + b);
+    const int i = fresh(pos + b);
     const size_t qbase = ((size_t)b * kHq + g * kG) * kD + lane;
     if (i < 0 || i >= Tc) {
         // a position outside the cache: report it, read nothing, output zeros
@@ -99,7 +98,7 @@ decode_kernel(const LayerArgs a, int Tc, const T* __restrict__ q, const T* __res
     float qh0[kG], qh1[kG], m[kG], l[kG], acc0[kG], acc1[kG];
 #pragma unroll
     for (int h = 0; h < kG; ++h) {
-        const float x0 = to_f32(q[qbase + h * kD]), x1 = to_f32(q[qbase + h * kD + kPairs]);
+        const float x0 = to_f32(fresh(q + qbase + h * kD)), x1 = to_f32(fresh(q + qbase + h * kD + kPairs));
         qh0[h] = x0 * csi.x - x1 * csi.y;
         qh1[h] = x1 * csi.x + x0 * csi.y;
         m[h] = -INFINITY;
@@ -111,12 +110,12 @@ decode_kernel(const LayerArgs a, int Tc, const T* __restrict__ q, const T* __res
     // rotated key pair and value pair of cache row j
     auto load = [&](int j, float& k0, float& k1, float& v0, float& v1) {
         const size_t off = row_off(j);
-        const float x0 = to_f32(kc[off]), x1 = to_f32(kc[off + kPairs]);
+        const float x0 = to_f32(fresh(kc + off)), x1 = to_f32(fresh(kc + off + kPairs));
         const float2 cs = rope_cs(rope, j, lane);
         k0 = x0 * cs.x - x1 * cs.y;
         k1 = x1 * cs.x + x0 * cs.y;
-        v0 = to_f32(vc[off]);
-        v1 = to_f32(vc[off + kPairs]);
+        v0 = to_f32(fresh(vc + off));
+        v1 = to_f32(fresh(vc + off + kPairs));
     };
 
     for (int e0 = warp * kBatch; e0 < nent; e0 += kSplit * kBatch) {
@@ -225,13 +224,12 @@ struct RawRow {
     float4 cs[4];
 };
 
-__device__ __forceinline__ void fetch_row(const __nv_bfloat16* __restrict__ base,
-                                          const __nv_bfloat16* __restrict__ vbase,
+__device__ __forceinline__ void fetch_row(const __nv_bfloat16* base, const __nv_bfloat16* vbase,
                                           const float2* __restrict__ rope, int pos, int c, RawRow& R) {
-    R.kx = __ldg(reinterpret_cast<const uint4*>(base) + c);
-    R.ky = __ldg(reinterpret_cast<const uint4*>(base) + 4 + c);
-    R.vx = __ldg(reinterpret_cast<const uint4*>(vbase) + c);
-    R.vy = __ldg(reinterpret_cast<const uint4*>(vbase) + 4 + c);
+    R.kx = fresh(reinterpret_cast<const uint4*>(base) + c);
+    R.ky = fresh(reinterpret_cast<const uint4*>(base) + 4 + c);
+    R.vx = fresh(reinterpret_cast<const uint4*>(vbase) + c);
+    R.vy = fresh(reinterpret_cast<const uint4*>(vbase) + 4 + c);
     if (rope) {
         const float4* t = reinterpret_cast<const float4*>(rope + (size_t)pos * kPairs + 8 * c);
 #pragma unroll
@@ -289,9 +287,8 @@ __device__ __forceinline__ void prefetch_row(const __nv_bfloat16* kc, const __nv
 }
 
 __global__ void __launch_bounds__(kFastThreads) decode_fast_kernel(
-    const LayerArgs a, int Tc, const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kc,
-    const __nv_bfloat16* __restrict__ vc, const int* __restrict__ pos, const float2* __restrict__ rope,
-    __nv_bfloat16* __restrict__ o, float* __restrict__ lse, unsigned* __restrict__ status) {
+    const LayerArgs a, int Tc, const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, const int* pos,
+    const float2* __restrict__ rope, __nv_bfloat16* o, float* lse, unsigned* status) {
     __shared__ __align__(16) float red[kFastEntries * kRedStride];  // p v per entry
     __shared__ float mw[4][kG], lw[4][kG];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -302,7 +299,9 @@ __global__ void __launch_bounds__(kFastThreads) decode_fast_kernel(
     // once the launch before it has completed.  While it waits, it asks L2 for
     // the cache rows of its entry at the position it reads now (clamped into
     // the cache): if the launch before rewrites the position, only these
-    // prefetches go to other rows, and every value used is read after the wait
+    // prefetches go to other rows, and every value used is read after the wait,
+    // by plain loads (fresh): with read-only ones a chain of sfa_qk_norm_rope and
+    // this call, whose launches all start early, got the queries of the step before
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (c == 0) {
         const int ip = min(max(*reinterpret_cast<const volatile int*>(pos + b), 0), Tc - 1);
@@ -319,10 +318,10 @@ __global__ void __launch_bounds__(kFastThreads) decode_fast_kernel(
     uint4 qxw[kG], qyw[kG];
 #pragma unroll
     for (int h = 0; h < kG; ++h) {
-        qxw[h] = __ldg(reinterpret_cast<const uint4*>(q + qbase + h * kD) + c);
-        qyw[h] = __ldg(reinterpret_cast<const uint4*>(q + qbase + h * kD) + 4 + c);
+        qxw[h] = fresh(reinterpret_cast<const uint4*>(q + qbase + h * kD) + c);
+        qyw[h] = fresh(reinterpret_cast<const uint4*>(q + qbase + h * kD) + 4 + c);
     }
-    const int i = __ldg(pos + b);
+    const int i = fresh(pos + b);
     if (i < 0 || i >= Tc) {
         // a position outside the cache: report it, read nothing, output zeros
         if (tid == 0 && status) atomicOr(status, SFA_DEVSTAT_BAD_INDEX);

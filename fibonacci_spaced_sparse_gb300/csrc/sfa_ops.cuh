@@ -6,15 +6,6 @@
 
 namespace sfa {
 
-// A load of memory that the launch before this one may have written.  It is
-// plain on purpose: a read-only (non-coherent) load, and so __ldg or a const
-// __restrict__ argument, promises that nothing writes the memory while this
-// grid is in flight, and may be moved ahead of griddepcontrol.wait.
-template <typename V>
-__device__ __forceinline__ V fresh(const V* p) {
-    return *p;
-}
-
 // Norm with rotation (sfa_norm.cu).  Token strides in elements.
 struct NormArgs {
     int N, T;              // tokens; tokens per sequence (position = index % T)
