@@ -81,7 +81,10 @@ __device__ __forceinline__ void report(unsigned* status) {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;     // raise a running maximum (log2 units) past this margin
-constexpr float kFloor = -1e30f;  // running maximum before the first entry
+// Running maximum before the first entry: the lowest finite value, so that any
+// score raises it or lies within the margin of it, and -infinity, which marks
+// what is no entry, stays below it.
+constexpr float kFloor = -3.402823466e38f;
 
 // Arguments of the attention kernels.
 struct PagedFwd {
