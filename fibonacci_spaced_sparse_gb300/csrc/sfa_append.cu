@@ -5,7 +5,8 @@
 // A copy with arithmetic, bound by memory when there are many tokens and by
 // the latency of its lookups (cu_q and seq_lens -> block_table and the rotation's
 // angles) in a decode step: what does not depend on a lookup is loaded before it
-// (256 tokens 2.4 us; with the weights and angles loaded last 2.6).  Blocks that
+// (256 tokens 2.4 us; with the weights and angles loaded last 2.6), and each lane
+// looks its own token up first (2.2).  Blocks that
 // go through consecutive tokens and copy the next step's rows ahead, as the norm
 // does for many tokens, are slower here (14.9 against 13.0 us for 16 prompts of
 // up to 2048 tokens, 26.5 against 22.5 us for 32768 tokens, before the order of
@@ -50,11 +51,30 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     const float* wp = role == kKey ? a.wk : a.wq;
     Row w{};
     if (wp && role != kValue) w = weights(wp, c);
-    // the sequence of the warp's first token, then forward to this lane's
-    paged::Where x = paged::sequence_of(a.c, warp_t);
-    if (x.s >= a.c.S) return;  // it lies behind the last sequence, and so do the others
-    while (x.end <= tt && x.s + 1 < a.c.S) x = paged::look(a.c, x.s + 1);
-    if (!in_n || tt >= x.end) return;
+    // a step in which every sequence brings one token: each lane's look-up finds its own
+    paged::Where x{};
+    bool live = in_n, found = false;
+    if (warp_t < a.c.S) {
+        x = paged::look(a.c, min(tt, a.c.S - 1));
+        found = x.start == tt && x.end == tt + 1;
+    }
+    if (!__all_sync(kFull, found || !in_n)) {
+        // the sequence of the warp's first token, then the next one, and a search for
+        // tokens that lie further on (there may be any number of sequences without
+        // a token between two of a warp's two to four tokens)
+        live = live && tt < fresh(a.c.cu + a.c.S);
+        x = paged::search(a.c, warp_t);
+        if (x.s >= a.c.S) return;  // it lies behind the last sequence, and so do the others
+        if (live && x.end <= tt && x.s + 1 < a.c.S) x = paged::look(a.c, x.s + 1);
+        for (unsigned behind; (behind = __ballot_sync(kFull, live && x.end <= tt)) != 0u;) {
+            const paged::Where y = paged::search(a.c, __shfl_sync(kFull, tt, __ffs(behind) - 1));
+            if (live && x.end <= tt) {
+                x = y;
+                live = y.s < a.c.S;  // with offsets that decrease a token may be in none
+            }
+        }
+    }
+    if (!live) return;
     const int pos = x.len - (x.end - tt);
     const bool good = pos >= 0 && pos < a.c.cap;
     Angles rot;

@@ -46,16 +46,20 @@ __device__ __forceinline__ Where last_at_most(const PagedArgs& c, int x, F first
 }
 
 // The sequence that token row t belongs to, or S when it belongs to none (the
-// whole warp asks for the same t).  A step in which every sequence brings one
-// token is found at once.
+// whole warp asks for the same t).
+__device__ __forceinline__ Where search(const PagedArgs& c, int t) {
+    Where x = last_at_most(c, t, [](int start, int) { return start; });
+    if (t < x.start || t >= x.end) x.s = c.S;
+    return x;
+}
+
+// The same; a step in which every sequence brings one token is found at once.
 __device__ __forceinline__ Where sequence_of(const PagedArgs& c, int t) {
     if (t < c.S) {
         const Where x = look(c, t);
         if (x.start == t && x.end == t + 1) return x;
     }
-    Where x = last_at_most(c, t, [](int start, int) { return start; });
-    if (t < x.start || t >= x.end) x.s = c.S;
-    return x;
+    return search(c, t);
 }
 
 // Row of the pages that holds position pos >= 0 of sequence s; -1 for a page
