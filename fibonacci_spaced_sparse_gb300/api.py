@@ -106,7 +106,8 @@ def launch_count() -> int:
 # ------------------------------------------------------------- RoPE table --
 
 _rope_cache: dict = {}
-_rope_outgrown: list = []  # captured graphs may still read them; at most as large together as the last one
+_rope_outgrown: list = []  # captured graphs may still read them; at most twice as large together as the last one
+_ROPE_ROWS = 1 << 24  # of the longest table that sfa_rope_table makes
 
 
 def rope_table(T: int, device, D: int = 64, rope_theta: float = 1e4, stream=None) -> torch.Tensor:
@@ -117,7 +118,7 @@ def rope_table(T: int, device, D: int = 64, rope_theta: float = 1e4, stream=None
            float(rope_theta))
     tab = _rope_cache.get(key)
     if tab is None or tab.shape[0] < T:
-        rows = max(T, 1024 if tab is None else 2 * tab.shape[0])
+        rows = max(T, 1024 if tab is None else min(2 * tab.shape[0], _ROPE_ROWS))
         lib = _lib.load()
         n = lib.sfa_rope_table_floats(int(rows), int(D))
         tab = torch.empty(n, dtype=torch.float32, device=device).view(rows, D // 2, 2)
@@ -428,7 +429,7 @@ def sfa_paged_append(k, v, k_pages, v_pages, block_table, cu_q, seq_lens, *, q=N
     if rope_theta <= 0:
         rope = None
     elif rope is None and k_pages.is_cuda and k_pages.dim() == 4 and block_table.numel():
-        rope = rope_table(min(block_table.shape[-1] * k_pages.shape[1], 1 << 24), k_pages.device,
+        rope = rope_table(min(block_table.shape[-1] * k_pages.shape[1], _ROPE_ROWS), k_pages.device,
                           rope_theta=rope_theta)
     return _native().paged_append(k, v, k_pages, v_pages, block_table, cu_q, seq_lens, q, wq, wk, eps, rope_theta,
                                   rope, q_out, status)
