@@ -122,7 +122,8 @@ def rope_table(T: int, device, D: int = 64, rope_theta: float = 1e4, stream=None
         lib = _lib.load()
         n = lib.sfa_rope_table_floats(int(rows), int(D))
         tab = torch.empty(n, dtype=torch.float32, device=device).view(rows, D // 2, 2)
-        st = lib.sfa_rope_table(_vp(tab), int(rows), int(D), float(rope_theta), _stream(device, stream))
+        with torch.cuda.device(device):  # a launch goes to the current device
+            st = lib.sfa_rope_table(_vp(tab), int(rows), int(D), float(rope_theta), _stream(device, stream))
         _lib.check(st, "sfa_rope_table")
         # the table is shared by later calls on any stream: finish building it
         (stream if stream is not None else torch.cuda.current_stream(device)).synchronize()

@@ -58,3 +58,10 @@ def test_growth_stops_at_the_longest_table(lib):
     with pytest.raises(RuntimeError):
         _table(LIMIT + 1)
     assert _table(LIMIT).shape[0] == LIMIT
+
+
+def test_tables_are_made_on_their_own_device(lib):
+    """The launch goes to the table's device, whichever one is current."""
+    for index in (0, 1, 1, 0):
+        _table(10, index, rope_theta=500.0)
+    assert lib.devices == [torch.device("meta", 0), torch.device("meta", 1)] and lib.current is None
