@@ -416,8 +416,9 @@ SFA_API sfa_status sfa_qk_norm_rope_backward(const sfa_params *p, const void *Q,
  *   i = seq_lens[s] - (cu_q[s + 1] - t),
  * so seq_lens counts a sequence's rows with the new ones, and a sequence's
  * new tokens are its last rows.  A sequence may bring no token, one or many.
- * Rows t >= cu_q[B] belong to no sequence: they are not read, and their
- * outputs are left as they were.  Position i of sequence s lives in row
+ * Rows t >= cu_q[B] belong to no sequence: what they hold does not matter, and
+ * their outputs are left as they were.  They are loaded all the same, so all N
+ * rows of Q, K and V have to be memory that can be read.  Position i of sequence s lives in row
  * i % page_size of page block_table[s][i / page_size]; only the entries of
  * block_table that a call needs are read, so entries of pages that are not
  * yet or no longer there may hold anything.  Cached keys are rotated (and
