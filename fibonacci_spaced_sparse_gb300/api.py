@@ -443,7 +443,8 @@ def sfa_paged_forward(q, k_pages, v_pages, block_table, cu_q, seq_lens, *, alpha
     include/sfa.h): q [N, 8, 64], already rotated; the cache and its metadata
     as in sfa_paged_append, after it.  Sequences may bring one token or many.
     Returns (o [N, 8, 64], lse [N, 8]); rows at and behind cu_q[S] are left as
-    they are (uninitialised without ``out`` and ``lse``)."""
+    they are (uninitialised without ``out`` and ``lse``).  A token's last bits
+    may change with what else is in the call, padding rows included."""
     if stream is not None:
         with _on(stream):
             return sfa_paged_forward(q, k_pages, v_pages, block_table, cu_q, seq_lens, alpha=alpha, W=W, rungs=rungs,

@@ -32,6 +32,14 @@
 // Neighbouring queries read neighbouring rows, so a row comes from L2 once a
 // block and from L1 after that.
 //
+// Probabilities are rounded to bf16, the type of the value product's operands;
+// the sum that divides the result keeps them in fp32, as lse needs it.  A rounding
+// is off by 2^-8 of its probability at most, and the errors of some 25 entries
+// add up to 1.2e-3 of O's norm, beside the 1.7e-3 of rounding O itself (2.1e-3
+// together).  A second product with what the first rounding left would bring that
+// back for 8 more MMAs and a second turned operand beside the 16 MMAs of a pair
+// of tiles, in a kernel that its instructions bound.
+//
 // Masked entries get probability 0.  A row that some queries of the quad read
 // is multiplied with the others' zeros, and a tile row that none reads is
 // filled with the first query's own row; infinity or NaN there would reach

@@ -473,7 +473,14 @@ SFA_API sfa_status sfa_paged_append(const sfa_params *p, const sfa_paged *c, con
  * token's key list never reach its output, whatever they hold.
  * One launch (bf16 with many tokens, W <= 28 and pages aligned to 32 bytes:
  * tensor cores, fp32 accumulation, probabilities rounded to bf16 for the value
- * product; else fp32 arithmetic); allocates nothing.  Asynchronous on stream. */
+ * product; else fp32 arithmetic); allocates nothing.  Asynchronous on stream.
+ * The kernel and the order of its sums go by N (rows behind cu_q[B] count), B,
+ * W and the pages, so a token's bits can differ between two calls that hold
+ * other tokens or other padding beside it; they do not between two calls alike.
+ * fp32 results and lse move by the rounding of fp32 sums, bf16 ones by that
+ * and by the rounding of the probabilities: for values of unit scale the error
+ * of O is 2.1e-3 of its norm on the tensor cores and 1.7e-3 in fp32 arithmetic,
+ * which is that of rounding O itself. */
 SFA_API sfa_status sfa_paged_forward(const sfa_params *p, const sfa_paged *c, const void *Q,
                                      long long q_stride, void *O, float *lse,
                                      unsigned int *status, cudaStream_t stream);
