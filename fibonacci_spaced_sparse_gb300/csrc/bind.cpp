@@ -127,9 +127,19 @@ const float* table(PyObject* o, const Tensor& ref, int64_t* rows) {
     return static_cast<const float*>(t.data_ptr());
 }
 
+// Without the interpreter's lock: other threads run while this one allocates or
+// waits for room in the launch queue.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // A new tensor on ref's device (the allocator's own entry: a dispatched
 // at::empty costs a microsecond on a Grace core).
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& ref) {
+    const Unlocked here;
     return Tensor(at::detail::empty_cuda(shape, type, ref.device(), std::nullopt));
 }
 
@@ -191,8 +201,15 @@ sfa_params params(int64_t B, int64_t T, sfa_dtype dt, double theta) {
     return p;
 }
 
-// Raises SfaError for a status other than SFA_OK.
-void check(sfa_status st, const char* where) {
+// Makes a call of the library without the interpreter's lock; raises SfaError for
+// a status other than SFA_OK.
+template <typename F>
+void call(const char* where, F f) {
+    sfa_status st;
+    {
+        const Unlocked here;
+        st = f();
+    }
     if (st == SFA_OK) return;
     PyObject* lib = PyImport_ImportModule("fibonacci_spaced_sparse_gb300._lib");
     if (lib) Py_XDECREF(PyObject_CallMethod(lib, "check", "is", (int)st, where));
@@ -260,10 +277,12 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const NormIn x(a);
         c10::cuda::OptionalCUDAGuard guard(x.q.device());
         Out qh(a[8], "out[0]", x.q.sizes(), x.q.scalar_type(), x.q), kh(a[9], "out[1]", x.k.sizes(), x.q.scalar_type(), x.q);
-        check(sfa_qk_norm_rope(&x.p, x.q.data_ptr(), x.qs, x.k.data_ptr(), x.ks, x.wq, x.wk, (float)x.eps, x.positions,
-                               x.rope, small(x.rows), qh.ptr, kh.ptr, status_word(a[10], x.q),
-                               c10::cuda::getCurrentCUDAStream(x.q.device().index()).stream()),
-              "sfa_qk_norm_rope");
+        unsigned* status = status_word(a[10], x.q);
+        const auto stream = c10::cuda::getCurrentCUDAStream(x.q.device().index()).stream();
+        call("sfa_qk_norm_rope", [&] {
+            return sfa_qk_norm_rope(&x.p, x.q.data_ptr(), x.qs, x.k.data_ptr(), x.ks, x.wq, x.wk, (float)x.eps, x.positions,
+                                    x.rope, small(x.rows), qh.ptr, kh.ptr, status, stream);
+        });
         return tuple_of({qh.object(), kh.object()});
     });
 }
@@ -299,12 +318,14 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             for (int i = 0; i < 2; ++i) dw[i] = part(whole, i, kD);
         }
         Out dwq(a[13], "out[2]", {kD}, at::kFloat, x.q, dw[0]), dwk(a[14], "out[3]", {kD}, at::kFloat, x.q, dw[1]);
-        check(sfa_qk_norm_rope_backward(&x.p, x.q.data_ptr(), x.qs, x.k.data_ptr(), x.ks, x.wq, x.wk, (float)x.eps,
-                                        x.positions, x.rope, small(x.rows), dqhat, dkhat, dq.ptr, dk.ptr,
-                                        static_cast<float*>(dwq.ptr), static_cast<float*>(dwk.ptr), ws, bytes,
-                                        status_word(a[15], x.q),
-                                        c10::cuda::getCurrentCUDAStream(x.q.device().index()).stream()),
-              "sfa_qk_norm_rope_backward");
+        unsigned* status = status_word(a[15], x.q);
+        const auto stream = c10::cuda::getCurrentCUDAStream(x.q.device().index()).stream();
+        call("sfa_qk_norm_rope_backward", [&] {
+            return sfa_qk_norm_rope_backward(&x.p, x.q.data_ptr(), x.qs, x.k.data_ptr(), x.ks, x.wq, x.wk, (float)x.eps,
+                                             x.positions, x.rope, small(x.rows), dqhat, dkhat, dq.ptr, dk.ptr,
+                                             static_cast<float*>(dwq.ptr), static_cast<float*>(dwk.ptr), ws, bytes, status,
+                                             stream);
+        });
         return tuple_of({dq.object(), dk.object(), dwq.object(), dwk.object()});
     });
 }
@@ -365,18 +386,20 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         c10::cuda::OptionalCUDAGuard guard(x.k.device());
         const auto stream = c10::cuda::getCurrentCUDAStream(x.k.device().index()).stream();
         if (!with_q) {
-            check(sfa_paged_append(&p, &x.c, nullptr, 0, k.data_ptr(), ks, v.data_ptr(), vs, nullptr, wk, (float)eps,
-                                   rope, nullptr, status, stream),
-                  "sfa_paged_append");
+            call("sfa_paged_append", [&] {
+                return sfa_paged_append(&p, &x.c, nullptr, 0, k.data_ptr(), ks, v.data_ptr(), vs, nullptr, wk, (float)eps,
+                                        rope, nullptr, status, stream);
+            });
             Py_RETURN_NONE;
         }
         const Tensor& q = tensor(a[7], "q");
         like(q, "q", x.k);
         const int64_t qs = token_stride(q, "q", lead, kHq);
         Out out(a[13], "q_out", q.sizes(), q.scalar_type(), x.k);
-        check(sfa_paged_append(&p, &x.c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, wq, wk, (float)eps, rope,
-                               out.ptr, status, stream),
-              "sfa_paged_append");
+        call("sfa_paged_append", [&] {
+            return sfa_paged_append(&p, &x.c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, wq, wk, (float)eps,
+                                    rope, out.ptr, status, stream);
+        });
         return out.object();
     });
 }
@@ -409,10 +432,10 @@ PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Out out(a[11], "out", q.sizes(), q.scalar_type(), x.k);
         const int64_t lse_shape[2] = {lead[0], kHq};
         const bool need_lse = PyObject_IsTrue(a[10]);
+        const auto stream = c10::cuda::getCurrentCUDAStream(x.k.device().index()).stream();
         auto run = [&](float* lse) {
-            check(sfa_paged_forward(&p, &x.c, q.data_ptr(), qs, out.ptr, lse, status,
-                                    c10::cuda::getCurrentCUDAStream(x.k.device().index()).stream()),
-                  "sfa_paged_forward");
+            call("sfa_paged_forward",
+                 [&] { return sfa_paged_forward(&p, &x.c, q.data_ptr(), qs, out.ptr, lse, status, stream); });
         };
         if (!need_lse) {
             run(nullptr);
