@@ -139,34 +139,28 @@ struct Unlocked {
 // A new tensor on ref's device (the allocator's own entry: a dispatched
 // at::empty costs a microsecond on a Grace core).
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& ref) {
-    const Unlocked here;
     return Tensor(at::detail::empty_cuda(shape, type, ref.device(), std::nullopt));
 }
 
-// Part `i` of `whole`, n values, as a tensor of its own on the same storage (half
-// the price of another allocation).
-Tensor part(const Tensor& whole, int64_t i, int64_t n) {
-    auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
-                                                  whole.dtype());
-    t->set_sizes_contiguous({n});
-    t->set_storage_offset(i * n);
-    return Tensor(std::move(t));
-}
-
-// An output: the given one, checked, or a new one.
+// An output: the given one, checked, or a new one, which make() allocates (without
+// the interpreter's lock, beside the library's call).
 struct Out {
     Tensor made;
     PyObject* given;
-    void* ptr;
-    // fresh: the new one, if there is one already
-    Out(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const Tensor& ref, Tensor fresh = {})
-        : given(o) {
-        if (o == Py_None) {
-            made = fresh.defined() ? std::move(fresh) : empty(shape, type, ref);
+    at::DimVector shape;
+    at::ScalarType type;
+    const Tensor& ref;
+    void* ptr = nullptr;
+    Out(PyObject* o, const char* name, at::IntArrayRef sizes, at::ScalarType t, const Tensor& r)
+        : given(o), shape(sizes), type(t), ref(r) {
+        if (o != Py_None) ptr = dense(tensor(o, name), name, sizes, t, r);
+    }
+    void* make() {
+        if (given == Py_None) {
+            made = empty(shape, type, ref);
             ptr = made.data_ptr();
-        } else {
-            ptr = dense(tensor(o, name), name, shape, type, ref);
         }
+        return ptr;
     }
     PyObject* object() {
         if (given != Py_None) return Py_NewRef(given);
@@ -201,8 +195,8 @@ sfa_params params(int64_t B, int64_t T, sfa_dtype dt, double theta) {
     return p;
 }
 
-// Makes a call of the library without the interpreter's lock; raises SfaError for
-// a status other than SFA_OK.
+// Makes a call of the library, and its allocations, without the interpreter's lock;
+// raises SfaError for a status other than SFA_OK.
 template <typename F>
 void call(const char* where, F f) {
     sfa_status st;
@@ -281,7 +275,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const auto stream = c10::cuda::getCurrentCUDAStream(x.q.device().index()).stream();
         call("sfa_qk_norm_rope", [&] {
             return sfa_qk_norm_rope(&x.p, x.q.data_ptr(), x.qs, x.k.data_ptr(), x.ks, x.wq, x.wk, (float)x.eps, x.positions,
-                                    x.rope, small(x.rows), qh.ptr, kh.ptr, status, stream);
+                                    x.rope, small(x.rows), qh.make(), kh.make(), status, stream);
         });
         return tuple_of({qh.object(), kh.object()});
     });
@@ -297,14 +291,9 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const void* dkhat = dense(tensor(a[9], "dkhat"), "dkhat", x.k.sizes(), type, x.q);
         Tensor scratch;
         void* ws = nullptr;
-        size_t bytes;
-        if (a[10] == Py_None) {
-            bytes = sfa_qk_norm_rope_backward_workspace_size(&x.p);
-            if (bytes) {
-                scratch = empty({(int64_t)bytes}, at::kByte, x.q);
-                ws = scratch.data_ptr();
-            }
-        } else {
+        size_t bytes = 0;
+        const bool own_scratch = a[10] == Py_None;
+        if (!own_scratch) {
             const Tensor& t = tensor(a[10], "workspace");
             if (t.device() != x.q.device() || !t.is_contiguous())
                 refuse("workspace must be a contiguous tensor on " + x.q.device().str());
@@ -312,19 +301,18 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             bytes = (size_t)t.nbytes();
         }
         Out dq(a[11], "out[0]", x.q.sizes(), type, x.q), dk(a[12], "out[1]", x.k.sizes(), type, x.q);
-        Tensor dw[2];
-        if (a[13] == Py_None && a[14] == Py_None) {
-            const Tensor whole = empty({2 * kD}, at::kFloat, x.q);
-            for (int i = 0; i < 2; ++i) dw[i] = part(whole, i, kD);
-        }
-        Out dwq(a[13], "out[2]", {kD}, at::kFloat, x.q, dw[0]), dwk(a[14], "out[3]", {kD}, at::kFloat, x.q, dw[1]);
+        Out dwq(a[13], "out[2]", {kD}, at::kFloat, x.q), dwk(a[14], "out[3]", {kD}, at::kFloat, x.q);
         unsigned* status = status_word(a[15], x.q);
         const auto stream = c10::cuda::getCurrentCUDAStream(x.q.device().index()).stream();
         call("sfa_qk_norm_rope_backward", [&] {
+            if (own_scratch && (bytes = sfa_qk_norm_rope_backward_workspace_size(&x.p)) != 0) {
+                scratch = empty({(int64_t)bytes}, at::kByte, x.q);
+                ws = scratch.data_ptr();
+            }
             return sfa_qk_norm_rope_backward(&x.p, x.q.data_ptr(), x.qs, x.k.data_ptr(), x.ks, x.wq, x.wk, (float)x.eps,
-                                             x.positions, x.rope, small(x.rows), dqhat, dkhat, dq.ptr, dk.ptr,
-                                             static_cast<float*>(dwq.ptr), static_cast<float*>(dwk.ptr), ws, bytes, status,
-                                             stream);
+                                             x.positions, x.rope, small(x.rows), dqhat, dkhat, dq.make(), dk.make(),
+                                             static_cast<float*>(dwq.make()), static_cast<float*>(dwk.make()), ws, bytes,
+                                             status, stream);
         });
         return tuple_of({dq.object(), dk.object(), dwq.object(), dwk.object()});
     });
@@ -398,7 +386,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Out out(a[13], "q_out", q.sizes(), q.scalar_type(), x.k);
         call("sfa_paged_append", [&] {
             return sfa_paged_append(&p, &x.c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, wq, wk, (float)eps,
-                                    rope, out.ptr, status, stream);
+                                    rope, out.make(), status, stream);
         });
         return out.object();
     });
@@ -432,17 +420,13 @@ PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Out out(a[11], "out", q.sizes(), q.scalar_type(), x.k);
         const int64_t lse_shape[2] = {lead[0], kHq};
         const bool need_lse = PyObject_IsTrue(a[10]);
+        Out lse(need_lse ? a[12] : Py_None, "lse", lse_shape, at::kFloat, x.k);
         const auto stream = c10::cuda::getCurrentCUDAStream(x.k.device().index()).stream();
-        auto run = [&](float* lse) {
-            call("sfa_paged_forward",
-                 [&] { return sfa_paged_forward(&p, &x.c, q.data_ptr(), qs, out.ptr, lse, status, stream); });
-        };
-        if (!need_lse) {
-            run(nullptr);
-            return tuple_of({out.object(), Py_NewRef(Py_None)});
-        }
-        Out lse(a[12], "lse", lse_shape, at::kFloat, x.k);
-        run(static_cast<float*>(lse.ptr));
+        call("sfa_paged_forward", [&] {
+            return sfa_paged_forward(&p, &x.c, q.data_ptr(), qs, out.make(),
+                                     need_lse ? static_cast<float*>(lse.make()) : nullptr, status, stream);
+        });
+        if (!need_lse) return tuple_of({out.object(), Py_NewRef(Py_None)});
         return tuple_of({out.object(), lse.object()});
     });
 }
