@@ -180,6 +180,12 @@ int64_t integer(PyObject* o) {
     return x;
 }
 
+bool truth(PyObject* o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) throw python_error();
+    return x != 0;
+}
+
 int small(int64_t x) { return (int)std::clamp<int64_t>(x, -1, 0x7fffffff); }  // the library refuses both
 
 sfa_params params(int64_t B, int64_t T, sfa_dtype dt, double theta) {
@@ -414,12 +420,12 @@ PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (PyErr_Occurred()) throw python_error();
         p.rungs = rungs;
         p.scale = (float)number(a[9]);
-        p.round_offsets = PyObject_IsTrue(a[14]);
+        p.round_offsets = truth(a[14]);
         unsigned* status = status_word(a[13], x.k);
         c10::cuda::OptionalCUDAGuard guard(x.k.device());
         Out out(a[11], "out", q.sizes(), q.scalar_type(), x.k);
         const int64_t lse_shape[2] = {lead[0], kHq};
-        const bool need_lse = PyObject_IsTrue(a[10]);
+        const bool need_lse = truth(a[10]);
         Out lse(need_lse ? a[12] : Py_None, "lse", lse_shape, at::kFloat, x.k);
         const auto stream = c10::cuda::getCurrentCUDAStream(x.k.device().index()).stream();
         call("sfa_paged_forward", [&] {
