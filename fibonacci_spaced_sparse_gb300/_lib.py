@@ -117,7 +117,8 @@ _bind = None
 
 
 def bind():
-    """The native half of the binding (csrc/bind.cpp); raises if it is missing."""
+    """The native half of the binding (csrc/bind.cpp); raises if it is missing or
+    was built for another torch or Python."""
     global _bind
     if _bind is None:
         load()
@@ -126,6 +127,11 @@ def bind():
                 f"_sfa_bind.so is not built ({BIND_PATH}); run "
                 "`python -c 'import __graft_entry__ as g; g.build()'` first")
         import torch  # noqa: F401  (its libraries)
+        from . import build
+        if build.built_for(BIND_PATH) != build.binding_key():
+            raise RuntimeError(
+                f"_sfa_bind.so was built for {build.built_for(BIND_PATH) or 'another torch or Python'}, here is "
+                f"{build.binding_key()}; run `python -c 'import __graft_entry__ as g; g.build()'` first")
         spec = importlib.util.spec_from_file_location("_sfa_bind", BIND_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
