@@ -106,11 +106,11 @@ __device__ __forceinline__ void close(const Row& a, Raw<float>& r) {
     r.y1 = make_float4(a.y[2].x, a.y[2].y, a.y[3].x, a.y[3].y);
 }
 
-// The same words through shared memory: each lane copies its own 16-byte pieces
-// there ahead of time and reads them back itself, so that loads in flight take
-// no registers and no barrier.  Slot p of thread i is slot[p * blockDim.x + i].
-template <typename T>
-constexpr int kPieces = sizeof(Raw<T>) / 16;
+// The same words of a bf16 row through shared memory: each lane copies its own
+// 16-byte pieces there ahead of time and reads them back itself, so that loads in
+// flight take no registers and no barrier.  Slot p of thread i is
+// slot[p * blockDim.x + i].
+constexpr int kPieces = sizeof(Raw<__nv_bfloat16>) / 16;
 
 __device__ __forceinline__ void copy16(uint4* slot, const void* src, bool keep = false) {
     const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
@@ -119,25 +119,12 @@ __device__ __forceinline__ void copy16(uint4* slot, const void* src, bool keep =
     else
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <typename T>
-__device__ __forceinline__ void copy_row(uint4* slot, const T* row, int c) {
+__device__ __forceinline__ void copy_row(uint4* slot, const __nv_bfloat16* row, int c) {
     const uint4* p = reinterpret_cast<const uint4*>(row);
-    if (kPieces<T> == 2) {
-        copy16(slot, p + c);
-        copy16(slot + blockDim.x, p + 4 + c);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) copy16(slot + i * blockDim.x, p + 2 * c + (i & 1) + 8 * (i >> 1));
-    }
+    copy16(slot, p + c);
+    copy16(slot + blockDim.x, p + 4 + c);
 }
-template <typename T>
-__device__ __forceinline__ Raw<T> take_row(const uint4* slot) {
-    Raw<T> r;
-    uint4* w = reinterpret_cast<uint4*>(&r);
-#pragma unroll
-    for (int i = 0; i < kPieces<T>; ++i) w[i] = slot[i * blockDim.x];
-    return r;
-}
+__device__ __forceinline__ Raw<__nv_bfloat16> take_row(const uint4* slot) { return {slot[0], slot[blockDim.x]}; }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until all but the n latest groups of this thread's copies are there.
 template <int n>

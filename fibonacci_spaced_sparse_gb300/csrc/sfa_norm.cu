@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_fwd_kernel(const NormArgs a,
 // a grid apart and copies the next step's rows and angles to shared memory
 // meanwhile, each lane its own pieces (sfa_heads.cuh): no registers, no
 // barrier.
-constexpr int kFwdPieces = 2 * kPieces<__nv_bfloat16>, kSlots = kFwdPieces + 4;  // pieces of a step: rows, angles
+constexpr int kFwdPieces = 2 * kPieces, kSlots = kFwdPieces + 4;  // pieces of a step: rows, angles
 constexpr int kAhead = 2;  // steps whose rows are on their way or in use
 constexpr int kPipedBlocks = 152 * 3;
 constexpr size_t kPipedSmem = (size_t)kAhead * kSlots * kThreads * sizeof(uint4);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 3)
             uint4* slot = slots + i * kSlots * kThreads + threadIdx.x;
             pos[i] = position(a, next);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) copy_row(slot + h * kPieces<T> * kThreads, in.of(next) + h * kD, c);
+            for (int h = 0; h < 2; ++h) copy_row(slot + h * kPieces * kThreads, in.of(next) + h * kD, c);
             if (a.rope) copy_angles(slot + kFwdPieces * kThreads, a.rope, max(pos[i], 0), c);
             next += step;
         }
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 3)
             if (a.rope) rot = take_angles(slot + kFwdPieces * kThreads);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                Row x = open(take_row<T>(slot + h * kPieces<T> * kThreads));
+                Row x = open(take_row(slot + h * kPieces * kThreads));
                 if (h == 1) start(i);  // the slots have been read
                 norm_row(a, x, w, rot, p, mask);
                 store(dst + h * kD, c, x);

@@ -52,7 +52,6 @@ using namespace mma;
 using paged::Pair;
 using paged::PagedFwd;
 using paged::Quad;
-using paged::kFloor;
 using paged::kLn2;
 using paged::kLog2e;
 using ring::warp_wait;
