@@ -111,18 +111,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
 template <typename T, bool kQ>
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
     const int roles = kQ ? kHq / 2 + 2 : 2, tokens = kThreads / 4 / roles;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.c.N + tokens - 1) / tokens));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, append_kernel<T, kQ>, a);
-    if (e == cudaSuccess) count_launch();
-    return e;
+    return launch_early(append_kernel<T, kQ>, (unsigned)((a.c.N + tokens - 1) / tokens), kThreads, 0, s, a);
 }
 
 }  // namespace

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_fwd_kernel(const NormArgs a,
 // barrier.
 constexpr int kFwdPieces = 2 * kPieces, kSlots = kFwdPieces + 4;  // pieces of a step: rows, angles
 constexpr int kAhead = 2;  // steps whose rows are on their way or in use
-constexpr int kPipedBlocks = 152 * 3;
+constexpr int kPipedBlocks = kSms * 3;
 constexpr size_t kPipedSmem = (size_t)kAhead * kSlots * kThreads * sizeof(uint4);
 
 __global__ void __launch_bounds__(kThreads, 3)
@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 // Resident blocks (of 8 tokens a step): 3 a SM at the 128 registers of bf16, 2
 // at the 165 of fp32.
 template <typename T>
-constexpr int kBwdBlocks = 152 * (sizeof(T) == 2 ? 3 : 2);
-constexpr int kMaxBlocks = 152 * 3;  // partial sums of dw
+constexpr int kBwdBlocks = kSms * (sizeof(T) == 2 ? 3 : 2);
+constexpr int kMaxBlocks = kSms * 3;  // partial sums of dw
 constexpr int kPartial = 2 * kD;     // floats of one: dwq, dwk
 
 __device__ __forceinline__ void cluster_sync() {
@@ -177,7 +177,7 @@ __device__ __forceinline__ float cluster_load(const float* p, unsigned rank) {
 // kCluster: the grid is one cluster of blocks, whose parts are summed through
 // distributed shared memory by its first block, dw = partial: one launch.
 template <typename T, bool kCluster>
-__global__ void __launch_bounds__(kThreads, kBwdBlocks<T> / 152)
+__global__ void __launch_bounds__(kThreads, kBwdBlocks<T> / kSms)
     norm_bwd_kernel(const NormArgs a, const T* dqhat, const T* dkhat, T* dq, T* dk, float* partial, float* dwk) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -295,26 +295,6 @@ __global__ void __launch_bounds__(kFinCols* kFinRows) norm_dw_kernel(const float
     }
 }
 
-// cluster: the grid is one cluster.
-template <bool kCluster = false, typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {grid, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = kCluster ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    if (e == cudaSuccess) count_launch();
-    return e;
-}
-
 unsigned steps_of(int N) { return (unsigned)((N + kTok - 1) / kTok); }
 
 cudaError_t launch_piped(const NormArgs& a, __nv_bfloat16* qhat, __nv_bfloat16* khat, cudaStream_t s) {
@@ -329,7 +309,7 @@ cudaError_t launch_piped(const NormArgs& a, __nv_bfloat16* qhat, __nv_bfloat16* 
         if (e != cudaSuccess) return e;
         ctx_setting_done(done[dev & 63], kPipedSmem);
     }
-    return launch(norm_fwd_piped_kernel, kPipedBlocks, kThreads, kPipedSmem, s, a, qhat, khat);
+    return launch_early(norm_fwd_piped_kernel, kPipedBlocks, kThreads, kPipedSmem, s, a, qhat, khat);
 }
 
 // bf16 tokens from which the piped kernel is the faster one (us, direct and
@@ -341,9 +321,9 @@ constexpr int kPipedFrom = 10240;
 
 cudaError_t launch_norm_fwd(const NormArgs& a, sfa_dtype dt, void* qhat, void* khat, cudaStream_t s) {
     if (dt == SFA_F32)
-        return launch(norm_fwd_kernel<float>, steps_of(a.N), kThreads, 0, s, a, (float*)qhat, (float*)khat);
+        return launch_early(norm_fwd_kernel<float>, steps_of(a.N), kThreads, 0, s, a, (float*)qhat, (float*)khat);
     if (a.N >= kPipedFrom) return launch_piped(a, (__nv_bfloat16*)qhat, (__nv_bfloat16*)khat, s);
-    return launch(norm_fwd_kernel<__nv_bfloat16>, steps_of(a.N), kThreads, 0, s, a, (__nv_bfloat16*)qhat,
+    return launch_early(norm_fwd_kernel<__nv_bfloat16>, steps_of(a.N), kThreads, 0, s, a, (__nv_bfloat16*)qhat,
                   (__nv_bfloat16*)khat);
 }
 
@@ -366,13 +346,13 @@ cudaError_t launch_bwd(const NormArgs& a, const void* dqhat, const void* dkhat, 
     T *oq = static_cast<T*>(dq), *ok = static_cast<T*>(dk);
     const unsigned steps = steps_of(a.N);
     if (a.N <= kClusterTo)
-        return launch<true>(norm_bwd_kernel<T, true>, steps, kThreads, 0, s, a, gq, gk, oq, ok, dwq, dwk);
+        return launch_early<true>(norm_bwd_kernel<T, true>, steps, kThreads, 0, s, a, gq, gk, oq, ok, dwq, dwk);
     const unsigned blocks = steps < (unsigned)kBwdBlocks<T> ? steps : (unsigned)kBwdBlocks<T>;
     float* partial = static_cast<float*>(ws);
     const cudaError_t e =
-        launch(norm_bwd_kernel<T, false>, blocks, kThreads, 0, s, a, gq, gk, oq, ok, partial, (float*)nullptr);
+        launch_early(norm_bwd_kernel<T, false>, blocks, kThreads, 0, s, a, gq, gk, oq, ok, partial, (float*)nullptr);
     if (e != cudaSuccess) return e;
-    return launch(norm_dw_kernel, (unsigned)(kPartial / kFinCols), (unsigned)(kFinCols * kFinRows), 0, s,
+    return launch_early(norm_dw_kernel, (unsigned)(kPartial / kFinCols), (unsigned)(kFinCols * kFinRows), 0, s,
                   (const float*)partial, (int)blocks, dwq, dwk);
 }
 

@@ -6,6 +6,31 @@
 
 namespace sfa {
 
+constexpr int kSms = 152;  // of a GB300; grids and the rules between kernels go by it
+
+// Launches a kernel that waits for the launch before it by itself
+// (griddepcontrol.wait), so its blocks may start while that one drains.  kCluster:
+// the grid is one cluster.
+template <bool kCluster = false, typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                         const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {grid, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = kCluster ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
 // Norm with rotation (sfa_norm.cu).  Token strides in elements.
 struct NormArgs {
     int N, T;              // tokens; tokens per sequence (position = index % T)

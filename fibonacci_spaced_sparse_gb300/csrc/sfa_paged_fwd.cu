@@ -327,18 +327,7 @@ template <typename T, int kNW>
 cudaError_t launch_rows_nw(const PagedFwd& P, cudaStream_t s) {
     constexpr int kUnits = kNW > 1 ? 1 : 2;
     const long long units = (long long)P.c.N * kHkv;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((units + kUnits - 1) / kUnits));
-    cfg.blockDim = dim3(kRowThreads<kNW>);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, rows_kernel<T, kNW>, P);
-    if (e == cudaSuccess) count_launch();
-    return e;
+    return launch_early(rows_kernel<T, kNW>, (unsigned)((units + kUnits - 1) / kUnits), kRowThreads<kNW>, 0, s, P);
 }
 
 // As many warps a (token, head) as keep all of them resident at once (16 a SM
@@ -348,7 +337,7 @@ cudaError_t launch_rows_nw(const PagedFwd& P, cudaStream_t s) {
 // 5.8, 6.5; 1024 19.8, 14.0, 10.7, 6.9.
 template <typename T>
 cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
-    const long long most = 152 * 16 / ((long long)P.c.N * kHkv);
+    const long long most = kSms * 16 / ((long long)P.c.N * kHkv);
     return most >= 8   ? launch_rows_nw<T, 8>(P, s)
            : most >= 4 ? launch_rows_nw<T, 4>(P, s)
            : most >= 2 ? launch_rows_nw<T, 2>(P, s)
@@ -361,7 +350,7 @@ cudaError_t launch_rows(const PagedFwd& P, cudaStream_t s) {
 // four (kDeep) at 242 (8 warps), where that keeps every warp resident (us, two and
 // four: one chunk of 512 tokens 4.4 and 4.2, of 2048 7.0 and 5.6; of 3100 6.8 and
 // 9.3, 512 chunks of 2 5.7 and 8.2, 1000 of 16 43 and 49).
-constexpr int kQuadWarps = 4, kDeepSlots = 152 * 2 * kQuadWarps / kHkv;
+constexpr int kQuadWarps = 4, kDeepSlots = kSms * 2 * kQuadWarps / kHkv;
 
 // A call of its own, so that the rare pass takes no registers of the common one
 // (and one for each kernel: they differ in their registers).
@@ -411,19 +400,8 @@ long long quad_slots(const PagedArgs& c) { return (long long)c.N / 4 + c.S; }
 
 cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
     const long long slots = quad_slots(P.c);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((slots + kQuadWarps - 1) / kQuadWarps * kHkv));
-    cfg.blockDim = dim3(kQuadWarps * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     void (*const kernel)(PagedFwd) = slots <= kDeepSlots ? quad_kernel<true> : quad_kernel<false>;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
-    if (e == cudaSuccess) count_launch();
-    return e;
+    return launch_early(kernel, (unsigned)((slots + kQuadWarps - 1) / kQuadWarps * kHkv), kQuadWarps * 32, 0, s, P);
 }
 
 // Token rows from which the quad kernel is taken, if there are two a sequence at
@@ -441,7 +419,7 @@ constexpr int kQuadsFrom = 305;
 // of 28 14.6 and 16.5, 256 of 16 12.2 and 13.1; 8 chunks of 512 beside 56 single
 // tokens 8.7 and 8.9, beside 192 9.1 and 13.3).  A smaller call would wait for
 // the host besides, which makes the tiles' maps in 3 us.
-constexpr int kQuadsWave = 152 * 3 * kQuadWarps / kHkv, kTilesEach = 32;
+constexpr int kQuadsWave = kSms * 3 * kQuadWarps / kHkv, kTilesEach = 32;
 
 }  // namespace
 

@@ -653,7 +653,7 @@ constexpr int kAskRounds = 6, kAskEach = 800;
 }  // namespace
 
 cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
-    const long long slots = (long long)P.c.N / kTQ + P.c.S, most = 152 * 2;
+    const long long slots = (long long)P.c.N / kTQ + P.c.S, most = kSms * 2;
     const bool ask = slots > most && slots <= kAskRounds * most && P.c.N <= kAskEach * (long long)P.c.S;
     void (*const kernel)(TileParams) = ask ? tile_kernel<true> : tile_kernel<false>;
     static CtxSetting done[2][64];  // per kernel and device: dynamic shared memory allowed
@@ -677,19 +677,7 @@ cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
         if (!encode_pages(&T.kv[0][h], P.c.k, rows, h + 1) || !encode_pages(&T.kv[1][h], P.c.v, rows, h + 1))
             return cudaErrorInvalidValue;
     if (!encode_queries(&T.q, P.q, P.c.N, P.qs)) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(T.split ? slots * kHkv : ask || slots < most ? slots : most));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, T);
-    if (e == cudaSuccess) count_launch();
-    return e;
+    return launch_early(kernel, (unsigned)(T.split ? slots * kHkv : ask || slots < most ? slots : most), kThreads, smem, s, T);
 }
 
 }  // namespace sfa
