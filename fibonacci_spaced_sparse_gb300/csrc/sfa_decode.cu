@@ -19,7 +19,7 @@
 // (base 2).  The kSplit partial states are then merged in shared memory in a
 // fixed order (the split of the flash-decoding kind).  Rows past pos[b] are
 // never read.
-#include "sfa_internal.cuh"
+#include "sfa_ops.cuh"
 
 namespace sfa {
 

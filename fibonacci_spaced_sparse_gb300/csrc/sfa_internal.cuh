@@ -132,15 +132,6 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// A load of memory that the launch before this one may have written.  It is
-// plain on purpose: a read-only (non-coherent) load, and so __ldg or a const
-// __restrict__ argument, promises that nothing writes the memory while this
-// grid is in flight, and may be moved ahead of griddepcontrol.wait.
-template <typename V>
-__device__ __forceinline__ V fresh(const V* p) {
-    return *p;
-}
-
 constexpr unsigned kFull = 0xffffffffu;
 
 // Sum over the 32 lanes of four per-lane values (one per query head of a

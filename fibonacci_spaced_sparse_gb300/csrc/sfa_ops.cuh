@@ -1,10 +1,20 @@
-// sfa_ops.cuh -- launch arguments of the norm and paged-cache kernels.  Private
-// to the CUDA library.
+// sfa_ops.cuh -- launch arguments of the norm and paged-cache kernels, and what
+// they and the decode share to start before the launch ahead of them has ended.
+// Private to the CUDA library.
 #pragma once
 
 #include "sfa_internal.cuh"
 
 namespace sfa {
+
+// A load of memory that the launch before this one may have written.  It is
+// plain on purpose: a read-only (non-coherent) load, and so __ldg or a const
+// __restrict__ argument, promises that nothing writes the memory while this
+// grid is in flight, and may be moved ahead of griddepcontrol.wait.
+template <typename V>
+__device__ __forceinline__ V fresh(const V* p) {
+    return *p;
+}
 
 constexpr int kSms = 152;  // of a GB300; grids and the rules between kernels go by it
 
