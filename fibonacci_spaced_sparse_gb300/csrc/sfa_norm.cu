@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 // -------------------------------------------------------------- backward
 
 // Resident blocks (of 8 tokens a step): 3 a SM at the 128 registers of bf16, 2
-// at the 165 of fp32.
+// at the 167 of fp32.
 template <typename T>
 constexpr int kBwdBlocks = kSms * (sizeof(T) == 2 ? 3 : 2);
 constexpr int kMaxBlocks = kSms * 3;  // partial sums of dw

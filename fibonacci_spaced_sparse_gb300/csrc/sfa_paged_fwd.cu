@@ -251,7 +251,7 @@ __device__ __forceinline__ void write_part(const PagedFwd& P, int t, int g, int 
 }
 
 template <int kNW>
-constexpr int kRowThreads = kNW > 1 ? 32 * kNW : 64;  // one unit a block, or two of one warp each (of eight: 2048 single tokens 15.9 and 15.5 us, 16 x 1024 in fp32 50.1 and 45.8)
+constexpr int kRowThreads = kNW > 1 ? 32 * kNW : 64;  // one unit a block, or two of one warp each (of eight: 2048 single tokens 15.9 and 15.5 us, 16 ragged fp32 prompts of up to 1024 50.1 and 45.8)
 
 template <typename T, int kNW>
 __global__ void __launch_bounds__(kRowThreads<kNW>, 512 / kRowThreads<kNW>) rows_kernel(const __grid_constant__ PagedFwd P) {

@@ -647,7 +647,9 @@ bool encode_queries(CUtensorMap* m, const void* base, int N, long long stride) {
 // queries or none), and a round more or less counts.  (us, a grid apart and asked
 // for: 80 chunks of up to 900 tokens after up to 900 40.9 and 36.0, 64 of 512 31.5
 // and 30.2, 50 of 700 34.3 and 32.7; 30 of up to 2000 32.7 and 31.2, but 32 of 1024
-// 30.8 and 31.5, 128 of 1024 102.5 and 105.3, 300 of up to 2000 253 and 255.)
+// 30.8 and 31.5, 128 of 1024 102.5 and 105.3, 300 of up to 2000 253 and 255.)  What
+// decides is how unequal the slots are, which the host does not know; it goes by the
+// average length, and so leaves out the 30 ragged chunks for the 32 equal ones.
 constexpr int kAskRounds = 6, kAskEach = 800;
 
 }  // namespace
