@@ -420,9 +420,9 @@ def sfa_paged_append(k, v, k_pages, v_pages, block_table, cu_q, seq_lens, *, q=N
     int32 [S] (rows with the new ones) on the device.  With ``q`` [N, 8, 64]
     the step's queries are normed (with wq) and rotated too and returned,
     ready for sfa_paged_forward; else returns None.  Rows at and behind
-    cu_q[S] may hold anything and are left as they are, in q_out too.  ``rope`` (rope_table(rows,
-    device)) bounds the positions; without it the shared table is grown to
-    max_pages * page_size rows."""
+    cu_q[S] may hold anything and are left as they are, in q_out too.
+    ``rope`` (rope_table(rows, device)) bounds the positions; without it the
+    shared table is grown to max_pages * page_size rows."""
     if stream is not None:
         with _on(stream):
             return sfa_paged_append(k, v, k_pages, v_pages, block_table, cu_q, seq_lens, q=q, wq=wq, wk=wk, eps=eps,
