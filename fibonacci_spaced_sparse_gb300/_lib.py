@@ -46,6 +46,10 @@ class SfaPaged(ctypes.Structure):
     ]
 
 
+class SfaPagedFp8(ctypes.Structure):
+    _fields_ = [("pages", SfaPaged), ("scales", ctypes.c_void_p), ("block_size", ctypes.c_int)]
+
+
 class SfaError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -59,6 +63,7 @@ _FP = ctypes.POINTER(ctypes.c_float)
 _IP = ctypes.POINTER(ctypes.c_int)
 _PP = ctypes.POINTER(SfaParams)
 _CP = ctypes.POINTER(SfaPaged)
+_C8 = ctypes.POINTER(SfaPagedFp8)
 _LL = ctypes.c_longlong
 
 _SIGS = {
@@ -90,6 +95,16 @@ _SIGS = {
     "sfa_paged_append": ([_PP, _CP, _VP, _LL, _VP, _LL, _VP, _LL, _VP, _VP, ctypes.c_float, _VP, _VP,
                           _VP, _VP], ctypes.c_int),
     "sfa_paged_forward": ([_PP, _CP, _VP, _LL, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "sfa_add_rms_norm": ([ctypes.c_int, ctypes.c_int, ctypes.c_int, _VP, _LL, _VP, _LL, _VP, ctypes.c_float, _VP, _VP, _VP,
+                          _VP, _VP], ctypes.c_int),
+    "sfa_add_rms_norm_backward_workspace_size": ([ctypes.c_int, ctypes.c_int, ctypes.c_int], ctypes.c_size_t),
+    "sfa_add_rms_norm_backward": ([ctypes.c_int, ctypes.c_int, ctypes.c_int, _VP, _VP, ctypes.c_float] + [_VP] * 5
+                                  + [ctypes.c_size_t, _VP], ctypes.c_int),
+    "sfa_quantize_rows_fp8": ([ctypes.c_int, ctypes.c_int, ctypes.c_int, _VP, _LL, _VP, _VP, _VP], ctypes.c_int),
+    "sfa_qkv_rope_fp8": ([_PP, ctypes.c_int] + [_VP] * 10, ctypes.c_int),
+    "sfa_paged_append_fp8": ([_PP, _C8, _VP, _LL, _VP, _LL, _VP, _LL, _VP, _VP, ctypes.c_float, _VP, _VP, _VP, _VP],
+                             ctypes.c_int),
+    "sfa_paged_forward_fp8": ([_PP, _C8, _VP, _LL, _VP, _VP, _VP, _VP], ctypes.c_int),
     "sfa_backward_workspace_size": ([_PP], ctypes.c_size_t),
     "sfa_backward": ([_PP] + [_VP] * 13 + [ctypes.c_size_t, _VP, _VP], ctypes.c_int),
     "sfa_read_status": ([_VP, ctypes.POINTER(ctypes.c_uint), _VP], ctypes.c_int),

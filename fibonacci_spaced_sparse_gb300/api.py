@@ -347,8 +347,8 @@ def sfa_backward(q, k, v, o, dO, lse, *, alpha: float, W: int, rungs=FIBONACCI_B
 
 # ------------------------------------------------------- norm with rotation --
 #
-# The norm and paged-cache calls run once per layer and step of a serving loop
-# on kernels of a few microseconds, so their checks, allocations and launches
+# The norm, paged-cache and 8-bit calls run once per layer and step of a serving
+# loop on kernels of a few microseconds, so their checks, allocations and launches
 # are native (csrc/bind.cpp).
 
 
@@ -454,6 +454,103 @@ def sfa_paged_forward(q, k_pages, v_pages, block_table, cu_q, seq_lens, *, alpha
                                    out, lse, status, round_offsets)
 
 
+# ------------------------------------ residual addition, norm, 8-bit serving --
+#
+# 8-bit values are torch.float8_e4m3fn, kept with a scale: x = scale * x8.float().
+
+
+def sfa_add_rms_norm(x, residual, w, *, eps: float = 1e-6, fp8: bool = False, out=None, stream=None):
+    """The residual's addition and the RMS norm of every row (sfa_add_rms_norm
+    in include/sfa.h): x and residual [..., dim], bf16 or fp32, rows at one
+    stride each; w fp32 [dim]; dim a multiple of 8, up to 16384.  Returns (h, y)
+    with h = x + residual (x itself where residual is None) and y its norm, or,
+    with ``fp8``, (h, y8, scale): y in 8 bits with a scale a row, as
+    sfa_qkv_rope_fp8 takes it.  ``out`` may supply the results; its h may be x or
+    residual."""
+    if stream is not None:
+        with _on(stream):
+            return sfa_add_rms_norm(x, residual, w, eps=eps, fp8=fp8, out=out)
+    h, y, s = (*out, None)[:3] if out is not None else (None, None, None)
+    return _native().add_rms_norm(x, residual, w, eps, fp8, h, y, s)
+
+
+def sfa_add_rms_norm_backward(h, w, dy, dh=None, *, eps: float = 1e-6, workspace=None, out=None, stream=None):
+    """(dx, dw) of sfa_add_rms_norm for the gradients dy of its norm and dh of the
+    sum (None: nothing else reads it): dx is the gradient of x and of the residual
+    alike, dw (fp32) that of w.  h: the sum that the forward returned.  All
+    contiguous.  ``out`` may supply the outputs (dx may be dh) and ``workspace``
+    (uint8) the scratch; calls that may overlap need one each."""
+    if stream is not None:
+        with _on(stream):
+            return sfa_add_rms_norm_backward(h, w, dy, dh, eps=eps, workspace=workspace, out=out)
+    dx, dw = out if out is not None else (None, None)
+    return _native().add_rms_norm_backward(h, w, dy, dh, eps, workspace, dx, dw)
+
+
+def sfa_quantize_rows_fp8(x, *, out=None, stream=None):
+    """(x8, scale): the rows of x [..., dim] (bf16 or fp32) in 8 bits with a scale
+    each (sfa_quantize_rows_fp8 in include/sfa.h); for the weights of
+    sfa_qkv_rope_fp8, once, and for rows that come from no norm."""
+    if stream is not None:
+        with _on(stream):
+            return sfa_quantize_rows_fp8(x, out=out)
+    x8, s = out if out is not None else (None, None)
+    return _native().quantize_rows_fp8(x, x8, s)
+
+
+def sfa_qkv_rope_fp8(x8, x_scale, w8, w_scale, *, rope_theta: float = 1e4, rope=None, out=None, status=None, stream=None):
+    """The fused front end on 8-bit rows and weights (sfa_qkv_rope_fp8 in
+    include/sfa.h): x8 [B, T, d_model] with x_scale fp32 [B, T], w8 [768,
+    d_model] with w_scale fp32 [768]; returns (qhat [B, T, 8, 64], khat [B, T, 2,
+    64], v [B, T, 2, 64]) in bf16, qhat and khat rotated at the positions 0 .. T -
+    1 (rope_theta=0: not rotated, as sfa_paged_append_fp8 takes them).  ``rope``:
+    a table of T rows at least instead of the shared one."""
+    if stream is not None:
+        with _on(stream):
+            return sfa_qkv_rope_fp8(x8, x_scale, w8, w_scale, rope_theta=rope_theta, rope=rope, out=out, status=status)
+    if rope_theta <= 0:
+        rope = None
+    elif rope is None and x8.is_cuda and x8.dim() == 3 and x8.numel():
+        rope = rope_table(x8.shape[1], x8.device, rope_theta=rope_theta)
+    q, k, v = out if out is not None else (None, None, None)
+    return _native().qkv_rope_fp8(x8, x_scale, w8, w_scale, rope_theta, rope, q, k, v, status)
+
+
+def sfa_paged_append_fp8(k, v, k_pages, v_pages, page_scales, block_table, cu_q, seq_lens, *, q=None, wq=None, wk=None,
+                         eps: float = 1e-6, rope_theta: float = 1e4, rope=None, q_out=None, status=None, stream=None):
+    """sfa_paged_append to a cache of 8-bit rows (sfa_paged_fp8 and
+    sfa_paged_append_fp8 in include/sfa.h): k_pages, v_pages [num_pages,
+    page_size, 2, 64] float8_e4m3fn, page_scales fp32 [num_pages, page_size /
+    block_size, 2, 2] (a block of block_size rows, keys and values, heads;
+    block_size a power of two from 8 on), all updated in place: an older row of a
+    block whose scale grows is written again.  Everything else as there."""
+    if stream is not None:
+        with _on(stream):
+            return sfa_paged_append_fp8(k, v, k_pages, v_pages, page_scales, block_table, cu_q, seq_lens, q=q, wq=wq, wk=wk,
+                                        eps=eps, rope_theta=rope_theta, rope=rope, q_out=q_out, status=status)
+    if rope_theta <= 0:
+        rope = None
+    elif rope is None and k_pages.is_cuda and k_pages.dim() == 4 and block_table.numel():
+        rope = rope_table(min(block_table.shape[-1] * k_pages.shape[1], _ROPE_ROWS), k_pages.device,
+                          rope_theta=rope_theta)
+    return _native().paged_append_fp8(k, v, k_pages, v_pages, page_scales, block_table, cu_q, seq_lens, q, wq, wk, eps,
+                                      rope_theta, rope, q_out, status)
+
+
+def sfa_paged_forward_fp8(q, k_pages, v_pages, page_scales, block_table, cu_q, seq_lens, *, alpha: float, W: int,
+                          rungs=FIBONACCI_BASE, scale: float = 0.0, need_lse: bool = True, out=None, lse=None, status=None,
+                          stream=None, round_offsets: bool = False):
+    """sfa_paged_forward over a cache of 8-bit rows, as sfa_paged_append_fp8 fills
+    it; q and the results in bf16 or fp32.  Everything else as there."""
+    if stream is not None:
+        with _on(stream):
+            return sfa_paged_forward_fp8(q, k_pages, v_pages, page_scales, block_table, cu_q, seq_lens, alpha=alpha, W=W,
+                                         rungs=rungs, scale=scale, need_lse=need_lse, out=out, lse=lse, status=status,
+                                         round_offsets=round_offsets)
+    return _native().paged_forward_fp8(q, k_pages, v_pages, page_scales, block_table, cu_q, seq_lens, alpha, W, rungs, scale,
+                                       need_lse, out, lse, status, round_offsets)
+
+
 def sfa_read_status(status: torch.Tensor, stream=None) -> int:
     """Synchronises and returns the device status word (0 = no error)."""
     w = ctypes.c_uint(0)
@@ -507,3 +604,28 @@ class QKNormRope(torch.autograd.Function):
         grads = sfa_qk_norm_rope_backward(q, k, wq, wk, dqhat.contiguous(), dkhat.contiguous(), eps=eps,
                                           rope_theta=rope_theta, positions=positions, rope=rope)
         return *grads, None, None, None, None
+
+
+class AddRMSNorm(torch.autograd.Function):
+    """Autograd wrapper of sfa_add_rms_norm: (h, y) with h = x + residual and y
+    the norm of h with the weights w (fp32 [dim]); y alone where residual is None.
+    Forward and backward can be captured into a CUDA graph as those of QKNormRope."""
+
+    @staticmethod
+    def forward(ctx, x, residual, w, eps=1e-6):
+        h, y = sfa_add_rms_norm(x, residual, w, eps=eps)
+        ctx.save_for_backward(h, w)
+        ctx.eps, ctx.sum = eps, residual is not None
+        ctx.set_materialize_grads(False)
+        return (h, y) if ctx.sum else y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        h, w = ctx.saved_tensors
+        dh, dy = grads if ctx.sum else (None, grads[0])
+        if dy is None:  # nothing reads the norm
+            return dh, dh if ctx.sum else None, None, None
+        dx, dw = sfa_add_rms_norm_backward(h.contiguous(), w, dy.contiguous(), None if dh is None else dh.contiguous(),
+                                           eps=ctx.eps)
+        return dx, dx if ctx.sum else None, dw, None

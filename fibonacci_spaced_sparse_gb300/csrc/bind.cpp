@@ -1,5 +1,5 @@
-// bind.cpp -- the native half of the Python binding of the norm and
-// paged-cache calls (api.py): looks at the tensors, allocates outputs and
+// bind.cpp -- the native half of the Python binding of the norm, paged-cache and
+// 8-bit calls (api.py): looks at the tensors, allocates outputs and
 // calls the C ABI.  These calls run once per layer and step of a serving loop
 // on kernels of a few microseconds, where marshalling in Python (ctypes and
 // tensor attributes, 19 to 27 us a call on the Grace cores of a GB300) would
@@ -330,23 +330,30 @@ struct CacheIn {
     const Tensor& k;
     sfa_dtype dt;
     int64_t S, cap;
-    sfa_paged c;
+    sfa_paged_fp8 f = {};       // scales and block_size of 8-bit pages
+    sfa_paged& c = f.pages;
 
-    // a: k_pages, v_pages, block_table, cu_q, seq_lens
-    CacheIn(PyObject* const* a, int64_t N) : k(tensor(a[0], "k_pages")) {
-        dt = dtype_of(k);
+    // a: k_pages, v_pages, (scales of 8-bit pages,) block_table, cu_q, seq_lens; token:
+    // the step's queries or keys
+    CacheIn(PyObject* const* a, const Tensor& token, bool fp8) : k(tensor(a[0], "k_pages")) {
+        dt = dtype_of(fp8 ? token : k);
+        if (fp8 && k.scalar_type() != at::kFloat8_e4m3fn)
+            throw Refused{PyExc_TypeError, std::string("k_pages must be float8_e4m3fn, got ") + at::toString(k.scalar_type())};
+        const int64_t N = token.size(0);
         if (!k.is_cuda()) refuse("k_pages must be a CUDA tensor");
         if (k.dim() != 4 || k.size(2) != kHkv || k.size(3) != kD || !k.is_contiguous())
             refuse("k_pages must be a contiguous [num_pages, page_size, 2, 64] tensor, got " + shape_text(k.sizes()));
         const int64_t page = k.size(1);
+        PyObject* const v_pages = a[1];
         if (k.size(0) < 1 || page < 1 || (page & (page - 1)))
             refuse("page_size must be a power of two and num_pages at least 1, got " + shape_text(k.sizes()));
+        if (fp8) blocks(tensor(a[2], "page_scales"), page);
+        a += fp8 ? 1 : 0;
         const Tensor& t = tensor(a[2], "block_table");
         if (t.dim() != 2 || t.size(1) < 1) refuse("block_table must be [S, max_pages], got " + shape_text(t.sizes()));
         S = t.size(0);
-        c = {};
         c.k_pages = k.data_ptr();
-        c.v_pages = dense(tensor(a[1], "v_pages"), "v_pages", k.sizes(), k.scalar_type(), k);
+        c.v_pages = dense(tensor(v_pages, "v_pages"), "v_pages", k.sizes(), k.scalar_type(), k);
         c.num_pages = small(k.size(0));
         c.page_size = small(page);
         c.block_table = static_cast<const int*>(dense(t, "block_table", t.sizes(), at::kInt, k));
@@ -356,18 +363,36 @@ struct CacheIn {
         c.N = small(N);
         cap = std::min<int64_t>(t.size(1) * page, 1 << 24);
     }
+    CacheIn(const CacheIn&) = delete;
+
+    // The scales of 8-bit pages, a block of rows each.
+    void blocks(const Tensor& t, int64_t page) {
+        if (t.dim() != 4 || t.size(1) < 1 || page % t.size(1) != 0)
+            refuse("page_scales must be [num_pages, page_size / block_size, 2, 2], got " + shape_text(t.sizes()));
+        f.scales = static_cast<float*>(dense(t, "page_scales", {k.size(0), t.size(1), 2, kHkv}, at::kFloat, k));
+        f.block_size = small(page / t.size(1));
+    }
+
+    // Refuses a tensor of token rows that is not like the first of them.
+    void same(const Tensor& t, const char* name, const Tensor& token) const {
+        like(t, name, token);
+        if (t.device() != k.device()) refuse(std::string(name) + " must be on the pages' device");
+    }
 };
 
-// k, v, k_pages, v_pages, block_table, cu_q, seq_lens, q, wq, wk, eps, theta, rope, q_out, status
-PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded("paged_append", n, 15, [&]() -> PyObject* {
+// k, v, k_pages, v_pages, (page_scales,) block_table, cu_q, seq_lens, q, wq, wk, eps, theta, rope, q_out, status
+PyObject* append_to(const char* name, bool fp8, PyObject* const* a, Py_ssize_t n) {
+    return guarded(name, n, fp8 ? 16 : 15, [&]() -> PyObject* {
+        const std::string call_name = std::string("sfa_") + name;
         const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
         if (k.dim() != 3) refuse("k must be [N, 2, 64], got " + shape_text(k.sizes()));
         const int64_t lead[1] = {k.size(0)};
-        const CacheIn x(a + 2, lead[0]);
-        like(k, "k", x.k);
-        like(v, "v", x.k);
+        const CacheIn x(a + 2, k, fp8);
+        const Tensor& kind = fp8 ? k : x.k;
+        x.same(k, "k", kind);
+        x.same(v, "v", kind);
         const int64_t ks = token_stride(k, "k", lead, kHkv), vs = token_stride(v, "v", lead, kHkv);
+        a += fp8 ? 1 : 0;
         const bool with_q = a[7] != Py_None;
         if (!with_q && (a[8] != Py_None || a[13] != Py_None)) refuse("wq and q_out go with q");
         const float* wq = dense_or_null<const float>(a[8], "wq", {kD}, at::kFloat, x.k);
@@ -379,34 +404,39 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         unsigned* status = status_word(a[14], x.k);
         c10::cuda::OptionalCUDAGuard guard(x.k.device());
         const auto stream = c10::cuda::getCurrentCUDAStream(x.k.device().index()).stream();
+        auto append = [&](const void* q, int64_t qs, void* out) {
+            return fp8 ? sfa_paged_append_fp8(&p, &x.f, q, qs, k.data_ptr(), ks, v.data_ptr(), vs, wq, wk, (float)eps, rope, out,
+                                              status, stream)
+                       : sfa_paged_append(&p, &x.c, q, qs, k.data_ptr(), ks, v.data_ptr(), vs, wq, wk, (float)eps, rope, out,
+                                          status, stream);
+        };
         if (!with_q) {
-            call("sfa_paged_append", [&] {
-                return sfa_paged_append(&p, &x.c, nullptr, 0, k.data_ptr(), ks, v.data_ptr(), vs, nullptr, wk, (float)eps,
-                                        rope, nullptr, status, stream);
-            });
+            call(call_name.c_str(), [&] { return append(nullptr, 0, nullptr); });
             Py_RETURN_NONE;
         }
         const Tensor& q = tensor(a[7], "q");
-        like(q, "q", x.k);
+        x.same(q, "q", kind);
         const int64_t qs = token_stride(q, "q", lead, kHq);
         Out out(a[13], "q_out", q.sizes(), q.scalar_type(), x.k);
-        call("sfa_paged_append", [&] {
-            return sfa_paged_append(&p, &x.c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, wq, wk, (float)eps,
-                                    rope, out.make(), status, stream);
-        });
+        call(call_name.c_str(), [&] { return append(q.data_ptr(), qs, out.make()); });
         return out.object();
     });
 }
+PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_to("paged_append", false, a, n); }
+PyObject* paged_append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_to("paged_append_fp8", true, a, n); }
 
-// q, k_pages, v_pages, block_table, cu_q, seq_lens, alpha, W, rungs, scale, need_lse, out, lse, status, round_offsets
-PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded("paged_forward", n, 15, [&]() -> PyObject* {
+// q, k_pages, v_pages, (page_scales,) block_table, cu_q, seq_lens, alpha, W, rungs, scale, need_lse, out, lse, status,
+// round_offsets
+PyObject* forward_over(const char* name, bool fp8, PyObject* const* a, Py_ssize_t n) {
+    return guarded(name, n, fp8 ? 16 : 15, [&]() -> PyObject* {
+        const std::string call_name = std::string("sfa_") + name;
         const Tensor& q = tensor(a[0], "q");
         if (q.dim() != 3) refuse("q must be [N, 8, 64], got " + shape_text(q.sizes()));
         const int64_t lead[1] = {q.size(0)};
-        const CacheIn x(a + 1, lead[0]);
-        like(q, "q", x.k);
+        const CacheIn x(a + 1, q, fp8);
+        x.same(q, "q", fp8 ? q : x.k);
         const int64_t qs = token_stride(q, "q", lead, kHq);
+        a += fp8 ? 1 : 0;
         sfa_params p = params(x.S, x.cap, x.dt, 0.0);
         p.alpha = (float)number(a[6]);
         p.W = small(integer(a[7]));
@@ -428,12 +458,171 @@ PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool need_lse = truth(a[10]);
         Out lse(need_lse ? a[12] : Py_None, "lse", lse_shape, at::kFloat, x.k);
         const auto stream = c10::cuda::getCurrentCUDAStream(x.k.device().index()).stream();
-        call("sfa_paged_forward", [&] {
-            return sfa_paged_forward(&p, &x.c, q.data_ptr(), qs, out.make(),
-                                     need_lse ? static_cast<float*>(lse.make()) : nullptr, status, stream);
+        call(call_name.c_str(), [&] {
+            void* o = out.make();
+            float* l = need_lse ? static_cast<float*>(lse.make()) : nullptr;
+            return fp8 ? sfa_paged_forward_fp8(&p, &x.f, q.data_ptr(), qs, o, l, status, stream)
+                       : sfa_paged_forward(&p, &x.c, q.data_ptr(), qs, o, l, status, stream);
         });
         if (!need_lse) return tuple_of({out.object(), Py_NewRef(Py_None)});
         return tuple_of({out.object(), lse.object()});
+    });
+}
+PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) { return forward_over("paged_forward", false, a, n); }
+PyObject* paged_forward_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return forward_over("paged_forward_fp8", true, a, n);
+}
+
+// ------------------------------------- residual addition, norm and 8-bit rows
+
+// Rows of x [..., dim] at one stride.
+struct RowsIn {
+    const Tensor& x;
+    sfa_dtype dt;
+    int64_t N, dim, stride;
+
+    RowsIn(PyObject* o, const char* name) : x(tensor(o, name)) {
+        dt = dtype_of(x);
+        if (!x.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
+        if (x.dim() < 1 || x.size(-1) < 1) refuse(std::string(name) + " must be [..., dim], got " + shape_text(x.sizes()));
+        dim = x.size(-1);
+        N = x.numel() / dim;
+        stride = row_stride(x, name, dim);
+    }
+    // The stride of its rows, which all leading dimensions share.
+    static int64_t row_stride(const Tensor& t, const char* name, int64_t dim) {
+        if (t.numel() <= dim) {
+            if (t.numel() > 0 && t.stride(-1) != 1 && dim > 1) refuse(std::string(name) + ": rows must be contiguous");
+            return dim;
+        }
+        bool one = t.stride(-1) == 1 || dim == 1;
+        int64_t step = -1, rows = 1;
+        for (int64_t i = t.dim() - 2; i >= 0; --i) {
+            if (t.size(i) == 1) continue;
+            if (step < 0) step = t.stride(i);
+            one = one && t.stride(i) == step * rows;
+            rows *= t.size(i);
+        }
+        if (!one || step < dim || step * t.element_size() % 16 != 0)
+            refuse(std::string(name) + ": rows must be contiguous and at one stride of a multiple of 16 bytes, got strides " +
+                   shape_text(t.strides()));
+        return step;
+    }
+    at::IntArrayRef lead() const { return x.sizes().slice(0, x.dim() - 1); }
+};
+
+// x, residual, w, eps, fp8, h, y, scale
+PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded("add_rms_norm", n, 8, [&]() -> PyObject* {
+        const RowsIn in(a[0], "x");
+        const bool sum = a[1] != Py_None, fp8 = truth(a[4]);
+        const Tensor& r = sum ? tensor(a[1], "residual") : in.x;
+        like(r, "residual", in.x);
+        if (r.sizes() != in.x.sizes()) refuse("residual must be " + shape_text(in.x.sizes()) + ", got " + shape_text(r.sizes()));
+        const int64_t rs = RowsIn::row_stride(r, "residual", in.dim);
+        const float* w = static_cast<const float*>(dense(tensor(a[2], "w"), "w", {in.dim}, at::kFloat, in.x));
+        const double eps = number(a[3]);
+        if (!sum && a[5] != Py_None) refuse("out[0] goes with a residual");
+        if (!fp8 && a[7] != Py_None) refuse("out[2] goes with fp8");
+        c10::cuda::OptionalCUDAGuard guard(in.x.device());
+        Out h(sum ? a[5] : Py_None, "out[0]", in.x.sizes(), in.x.scalar_type(), in.x);
+        Out y(a[6], "out[1]", in.x.sizes(), fp8 ? at::kFloat8_e4m3fn : in.x.scalar_type(), in.x);
+        Out s(fp8 ? a[7] : Py_None, "out[2]", in.lead(), at::kFloat, in.x);
+        const auto stream = c10::cuda::getCurrentCUDAStream(in.x.device().index()).stream();
+        call("sfa_add_rms_norm", [&] {
+            void* to_h = sum ? h.make() : nullptr;
+            void* to_y = y.make();
+            return sfa_add_rms_norm(in.dt, small(in.N), small(in.dim), in.x.data_ptr(), in.stride, sum ? r.data_ptr() : nullptr, rs,
+                                    w, (float)eps, to_h, fp8 ? nullptr : to_y, fp8 ? to_y : nullptr,
+                                    fp8 ? static_cast<float*>(s.make()) : nullptr, stream);
+        });
+        PyObject* first = sum ? h.object() : Py_NewRef(a[0]);
+        if (!fp8) return tuple_of({first, y.object()});
+        return tuple_of({first, y.object(), s.object()});
+    });
+}
+
+// x, x8, scale
+PyObject* quantize_rows_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded("quantize_rows_fp8", n, 3, [&]() -> PyObject* {
+        const RowsIn in(a[0], "x");
+        c10::cuda::OptionalCUDAGuard guard(in.x.device());
+        Out y(a[1], "out[0]", in.x.sizes(), at::kFloat8_e4m3fn, in.x), s(a[2], "out[1]", in.lead(), at::kFloat, in.x);
+        const auto stream = c10::cuda::getCurrentCUDAStream(in.x.device().index()).stream();
+        call("sfa_quantize_rows_fp8", [&] {
+            void* to = y.make();
+            return sfa_quantize_rows_fp8(in.dt, small(in.N), small(in.dim), in.x.data_ptr(), in.stride, to,
+                                         static_cast<float*>(s.make()), stream);
+        });
+        return tuple_of({y.object(), s.object()});
+    });
+}
+
+// h, w, dy, dh, eps, workspace, dx, dw
+PyObject* add_rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded("add_rms_norm_backward", n, 8, [&]() -> PyObject* {
+        const RowsIn in(a[0], "h");
+        const auto type = in.x.scalar_type();
+        const void* h = dense(in.x, "h", in.x.sizes(), type, in.x);
+        const float* w = static_cast<const float*>(dense(tensor(a[1], "w"), "w", {in.dim}, at::kFloat, in.x));
+        const void* dy = dense(tensor(a[2], "dy"), "dy", in.x.sizes(), type, in.x);
+        const void* dh = dense_or_null(a[3], "dh", in.x.sizes(), type, in.x);
+        const double eps = number(a[4]);
+        Tensor scratch;
+        void* ws = nullptr;
+        size_t bytes = 0;
+        const bool own_scratch = a[5] == Py_None;
+        if (!own_scratch) {
+            const Tensor& t = tensor(a[5], "workspace");
+            if (t.device() != in.x.device() || !t.is_contiguous())
+                refuse("workspace must be a contiguous tensor on " + in.x.device().str());
+            ws = t.data_ptr();
+            bytes = (size_t)t.nbytes();
+        }
+        c10::cuda::OptionalCUDAGuard guard(in.x.device());
+        Out dx(a[6], "out[0]", in.x.sizes(), type, in.x), dw(a[7], "out[1]", {in.dim}, at::kFloat, in.x);
+        const auto stream = c10::cuda::getCurrentCUDAStream(in.x.device().index()).stream();
+        call("sfa_add_rms_norm_backward", [&] {
+            const int N = small(in.N), dim = small(in.dim);
+            if (own_scratch && (bytes = sfa_add_rms_norm_backward_workspace_size(in.dt, N, dim)) != 0) {
+                scratch = empty({(int64_t)bytes}, at::kByte, in.x);
+                ws = scratch.data_ptr();
+            }
+            void* to = dx.make();
+            return sfa_add_rms_norm_backward(in.dt, N, dim, h, w, (float)eps, dy, dh, to, static_cast<float*>(dw.make()), ws, bytes,
+                                             stream);
+        });
+        return tuple_of({dx.object(), dw.object()});
+    });
+}
+
+// x8, x_scale, w8, w_scale, theta, rope, q, k, v, status
+PyObject* qkv_rope_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded("qkv_rope_fp8", n, 10, [&]() -> PyObject* {
+        const Tensor& x = tensor(a[0], "x8");
+        if (x.dim() != 3 || x.scalar_type() != at::kFloat8_e4m3fn || !x.is_cuda() || !x.is_contiguous())
+            refuse("x8 must be a contiguous float8_e4m3fn [B, T, d_model] CUDA tensor, got " +
+                   std::string(at::toString(x.scalar_type())) + " " + shape_text(x.sizes()));
+        const int64_t B = x.size(0), T = x.size(1), dm = x.size(2), rows = (kHq + 2 * kHkv) * kD;
+        const float* sx = static_cast<const float*>(dense(tensor(a[1], "x_scale"), "x_scale", {B, T}, at::kFloat, x));
+        const void* w = dense(tensor(a[2], "w8"), "w8", {rows, dm}, at::kFloat8_e4m3fn, x);
+        const float* sw = static_cast<const float*>(dense(tensor(a[3], "w_scale"), "w_scale", {rows}, at::kFloat, x));
+        const double theta = number(a[4]);
+        int64_t have;
+        const float* rope = table(a[5], x, &have);
+        if (theta > 0 && have < T && B > 0)
+            refuse("rope has " + std::to_string(have) + " rows, the sequence " + std::to_string(T));
+        const int64_t qs[4] = {B, T, kHq, kD}, ks[4] = {B, T, kHkv, kD};
+        Out q(a[6], "out[0]", qs, at::kBFloat16, x), k(a[7], "out[1]", ks, at::kBFloat16, x), v(a[8], "out[2]", ks, at::kBFloat16, x);
+        unsigned* status = status_word(a[9], x);
+        const sfa_params p = params(B, T, SFA_BF16, theta);
+        c10::cuda::OptionalCUDAGuard guard(x.device());
+        const auto stream = c10::cuda::getCurrentCUDAStream(x.device().index()).stream();
+        call("sfa_qkv_rope_fp8", [&] {
+            void *to_q = q.make(), *to_k = k.make(), *to_v = v.make();
+            return sfa_qkv_rope_fp8(&p, small(dm), x.data_ptr(), sx, w, sw, rope, to_q, to_k, to_v, status, stream);
+        });
+        return tuple_of({q.object(), k.object(), v.object()});
     });
 }
 
@@ -455,6 +644,12 @@ PyMethodDef methods[] = {{"norm_rope", fast(norm_rope), METH_FASTCALL, nullptr},
                          {"norm_rope_backward", fast(norm_rope_backward), METH_FASTCALL, nullptr},
                          {"paged_append", fast(paged_append), METH_FASTCALL, nullptr},
                          {"paged_forward", fast(paged_forward), METH_FASTCALL, nullptr},
+                         {"paged_append_fp8", fast(paged_append_fp8), METH_FASTCALL, nullptr},
+                         {"paged_forward_fp8", fast(paged_forward_fp8), METH_FASTCALL, nullptr},
+                         {"add_rms_norm", fast(add_rms_norm), METH_FASTCALL, nullptr},
+                         {"add_rms_norm_backward", fast(add_rms_norm_backward), METH_FASTCALL, nullptr},
+                         {"quantize_rows_fp8", fast(quantize_rows_fp8), METH_FASTCALL, nullptr},
+                         {"qkv_rope_fp8", fast(qkv_rope_fp8), METH_FASTCALL, nullptr},
                          {"stride_of", fast(stride_of), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

@@ -51,29 +51,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     const float* wp = role == kKey ? a.wk : a.wq;
     Row w{};
     if (wp && role != kValue) w = weights(wp, c);
-    // a step in which every sequence brings one token: each lane's look-up finds its own
-    paged::Where x{};
-    bool live = in_n, found = false;
-    if (warp_t < a.c.S) {
-        x = paged::look(a.c, min(tt, a.c.S - 1));
-        found = x.start == tt && x.end == tt + 1;
-    }
-    if (!__all_sync(kFull, found || !in_n)) {
-        // the sequence of the warp's first token, then the next one, and a search for
-        // tokens that lie further on (there may be any number of sequences without
-        // a token between two of a warp's two to four tokens)
-        live = live && tt < fresh(a.c.cu + a.c.S);
-        x = paged::search(a.c, warp_t);
-        if (x.s >= a.c.S) return;  // it lies behind the last sequence, and so do the others
-        if (live && x.end <= tt && x.s + 1 < a.c.S) x = paged::look(a.c, x.s + 1);
-        for (unsigned behind; (behind = __ballot_sync(kFull, live && x.end <= tt)) != 0u;) {
-            const paged::Where y = paged::search(a.c, __shfl_sync(kFull, tt, __ffs(behind) - 1));
-            if (live && x.end <= tt) {
-                x = y;
-                live = y.s < a.c.S;  // with offsets that decrease a token may be in none
-            }
-        }
-    }
+    bool live;
+    const paged::Where x = paged::each_token(a.c, tt, in_n, warp_t, live);
     if (!live) return;
     const int pos = x.len - (x.end - tt);
     const bool good = pos >= 0 && pos < a.c.cap;

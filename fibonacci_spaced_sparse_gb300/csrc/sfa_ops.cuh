@@ -58,6 +58,30 @@ size_t norm_bwd_workspace(long long N);  // N tokens; 0: none
 cudaError_t launch_norm_bwd(const NormArgs& a, sfa_dtype dt, const void* dqhat, const void* dkhat, void* dq, void* dk,
                             float* dwq, float* dwk, void* ws, cudaStream_t s);
 
+// The residual's addition and the norm of rows (sfa_add_norm.cu).  Strides in
+// elements; what a row is written to is dense.
+struct AddNormArgs {
+    int N, dim;
+    long long xs, rs;      // row strides
+    const void *x, *r;     // r: nullptr for no residual
+    const float* w;
+    float eps, inv_dim;
+    void *h, *y;           // the sum (nullptr: not kept); the norm, or its 8-bit values
+    float* scale;          // of 8-bit rows
+};
+// norm = false: the rows themselves in 8 bits.
+cudaError_t launch_add_norm(const AddNormArgs& a, sfa_dtype dt, bool norm, bool fp8, cudaStream_t s);
+struct AddNormBwdArgs {
+    int N, dim;
+    const void *h, *dy, *dh;  // dh: nullptr for none
+    const float* w;
+    float eps, inv_dim;
+    void* dx;
+    float* dw;
+};
+size_t add_norm_bwd_workspace(int N, int dim);  // 0: none
+cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, sfa_dtype dt, void* ws, cudaStream_t s);
+
 // A paged cache and one step's tokens (sfa_paged in sfa.h).
 struct PagedArgs {
     void *k, *v;
@@ -67,6 +91,8 @@ struct PagedArgs {
     int max_pages, num_pages;
     int shift;             // log2 of the page size
     int cap;               // positions [0, cap) exist
+    float* scales;         // of 8-bit pages: [block of rows][key or value][head]
+    int block_shift;       // log2 of the rows of a block
 };
 struct AppendArgs {
     PagedArgs c;
@@ -78,7 +104,21 @@ struct AppendArgs {
     float eps;
 };
 cudaError_t launch_paged_append(const AppendArgs& a, sfa_dtype dt, cudaStream_t s);
+cudaError_t launch_paged_append_fp8(const AppendArgs& a, sfa_dtype dt, cudaStream_t s);
 cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs, void* o,
                              float* lse, cudaStream_t s);
+cudaError_t launch_paged_fwd_fp8(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs,
+                                 void* o, float* lse, cudaStream_t s);
+
+// The projection of 8-bit rows (sfa_qkv_fp8.cu).
+struct QkvFp8Args {
+    int M, T, dm;           // tokens, positions of a sequence, columns
+    const void *x, *w;
+    const float *sx, *sw;   // scales of the rows of x and w
+    const float2* rope;     // nullptr: no rotation
+    void *q, *k, *v;
+    unsigned* status;
+};
+cudaError_t launch_qkv_fp8(const QkvFp8Args& a, cudaStream_t s);
 
 }  // namespace sfa

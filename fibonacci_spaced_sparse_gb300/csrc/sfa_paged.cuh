@@ -62,6 +62,38 @@ __device__ __forceinline__ Where sequence_of(const PagedArgs& c, int t) {
     return search(c, t);
 }
 
+// The sequence of each lane's own token row tt (min(t, N - 1) of a row t that rises
+// with the lane; in_n: t < N), warp_t the first lane's t; live: it belongs to one.  A step
+// in which every sequence brings one token takes one round of loads.
+__device__ __forceinline__ Where each_token(const PagedArgs& c, int tt, bool in_n, int warp_t, bool& live) {
+    Where x{};
+    bool found = false;
+    live = in_n;
+    if (warp_t < c.S) {
+        x = look(c, min(tt, c.S - 1));
+        found = x.start == tt && x.end == tt + 1;
+    }
+    if (__all_sync(kFull, found || !in_n)) return x;
+    // the sequence of the warp's first token, then the next one, and a search for
+    // tokens that lie further on (there may be any number of sequences without
+    // a token between two of a warp's few tokens)
+    live = live && tt < fresh(c.cu + c.S);
+    x = search(c, warp_t);
+    if (x.s >= c.S) {  // it lies behind the last sequence, and so do the others
+        live = false;
+        return x;
+    }
+    if (live && x.end <= tt && x.s + 1 < c.S) x = look(c, x.s + 1);
+    for (unsigned behind; (behind = __ballot_sync(kFull, live && x.end <= tt)) != 0u;) {
+        const Where y = search(c, __shfl_sync(kFull, tt, __ffs(behind) - 1));
+        if (live && x.end <= tt) {
+            x = y;
+            live = y.s < c.S;  // with offsets that decrease a token may be in none
+        }
+    }
+    return x;
+}
+
 // Row of the pages that holds position pos >= 0 of sequence s; -1 for a page
 // number out of range.  pos < c.cap.
 __device__ __forceinline__ int page_row(const PagedArgs& c, int s, int pos) {
@@ -76,6 +108,12 @@ __device__ __forceinline__ int page_row_if(const PagedArgs& c, int s, int pos, b
     const int page = fresh(c.table + (size_t)s * c.max_pages + (want ? pos >> c.shift : 0));
     const bool in = want && (unsigned)page < (unsigned)c.num_pages;
     return in ? (page << c.shift) + (pos & ((1 << c.shift) - 1)) : -1;
+}
+
+// The scales of the block of 8-bit rows that holds a row of the pages: of its
+// keys, a head each, then of its values.
+__device__ __forceinline__ float* row_scales(const PagedArgs& c, int row) {
+    return c.scales + (size_t)((unsigned)row >> c.block_shift) * (2 * kHkv);
 }
 
 __device__ __forceinline__ void report(unsigned* status) {

@@ -29,21 +29,20 @@
 // With two accumulators the MMAs of the next tile run while the epilogue
 // drains the current one.  Every wait is bounded; a timeout sets
 // SFA_DEVSTAT_WAIT_TIMEOUT and the CTA stops.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <cstring>
 
 #include "sfa_internal.cuh"
 #include "sfa_mma.cuh"
 #include "sfa_ring.cuh"
 #include "sfa_tc.cuh"
+#include "sfa_tma.cuh"
 
 namespace sfa {
 
 namespace {
 
 using namespace mma;
+using namespace tma;
 
 constexpr int BM = 128;                 // tokens per tile (TMEM lanes)
 constexpr int BN = 256;                 // output features per tile (TMEM columns)
@@ -90,29 +89,6 @@ struct QkvParams {
 // bf16 tiles in the 128-byte swizzle (sfa_tc.cuh); a K step of 16 elements
 // advances each descriptor's start address by 32 bytes.
 constexpr uint32_t kIdesc = tc::idesc_bf16(BM, BN, false);
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int c0, int c1) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tmap),
-                 "r"(src), "r"(c0), "r"(c1)
-                 : "memory");
-}
-
-// Wait until at most one committed bulk store of this thread still reads
-// its shared-memory source.
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
-
-__device__ __forceinline__ void sts_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
 
 // ------------------------------------------------------------ the kernel
 
@@ -317,31 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1) qkv_rope_kernel(const __grid_cons
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
 // 2-D map over a row-major bf16 matrix [rows][cols], box of 64 columns x
-// box_rows rows, 128-byte swizzle, zero fill outside (loads) / clipped (stores).
+// box_rows rows.
 bool encode_matrix(CUtensorMap* m, const void* base, int rows, int cols, int box_rows) {
-    auto fn = encode_tiled();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return tma::encode_rows(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols, box_rows);
 }
 
 }  // namespace

@@ -51,8 +51,9 @@
  * checks its arguments as usual and then returns SFA_ERR_CUDA without
  * launching, so that a caller's error handling can be exercised without
  * faulting a GPU.  Calls with nothing to launch (B * T = 0, no token rows) still
- * return SFA_OK, except sfa_backward and sfa_qk_norm_rope_backward, which then
- * still zero dalpha and dtheta (dwq and dwk) and so fail too.
+ * return SFA_OK, except sfa_backward, sfa_qk_norm_rope_backward and
+ * sfa_add_rms_norm_backward, which then still zero dalpha and dtheta (dwq and
+ * dwk; dw) and so fail too.
  */
 #ifndef SFA_H
 #define SFA_H
@@ -283,6 +284,72 @@ SFA_API sfa_status sfa_qkv_rope(const sfa_params *p, int d_model, const void *X,
                                 const float *rope_table, void *Qhat, void *Khat, void *V,
                                 unsigned int *status, cudaStream_t stream);
 
+/* ---- residual addition, norm and 8-bit rows ---------------------------- */
+
+/* 8-bit values are e4m3 ("fn": a sign, four exponent bits, three of mantissa,
+ * largest value 448, no infinity, 0x7f NaN), one byte each, kept with a scale:
+ * x = s c.  A value is rounded to nearest even; one that is not finite becomes
+ * NaN and does not count towards a scale.
+ *
+ * What stands in front of a layer's projection in a model with a residual
+ * stream (the paper's model has no such call): for every row t < N of dim values
+ *   h[t] = x[t] + r[t], rounded to the rows' type,
+ *   y[t] = h[t] / sqrt(mean(h[t]^2) + eps) * w
+ * in fp32.  y is rounded once to the rows' type, or given in 8 bits with a scale
+ * a row, s[t] = max(max |y[t]| / 448, 2^-126).
+ *   dtype: of X, R, H and Y;
+ *   N >= 0 (0: nothing to do); dim: a multiple of 8, 8 .. 16384, else
+ *     SFA_ERR_UNSUPPORTED;
+ *   X, R [N][dim], row t x_stride (r_stride) elements after the row before it: a
+ *     multiple of 16 bytes, at least dim; R may be NULL (h = x);
+ *   w [dim] fp32; eps: finite, >= 0;
+ *   H [N][dim], contiguous, or NULL where the sum is not wanted (or R is NULL);
+ *     H may be X or R itself (with a stride of dim);
+ *   Y [N][dim] contiguous, or Y8 [N][dim] bytes, contiguous, with scale [N] fp32:
+ *     one of the two, the other NULL.
+ * Device pointers 16-byte aligned (Y8 8-byte, scale 4-byte).  One launch; allocates nothing.
+ * Asynchronous on stream. */
+SFA_API sfa_status sfa_add_rms_norm(sfa_dtype dtype, int N, int dim, const void *X, long long x_stride, const void *R,
+                                    long long r_stride, const float *w, float eps, void *H, void *Y, void *Y8,
+                                    float *scale, cudaStream_t stream);
+
+/* Bytes of device workspace sfa_add_rms_norm_backward needs (0: none). */
+SFA_API size_t sfa_add_rms_norm_backward_workspace_size(sfa_dtype dtype, int N, int dim);
+
+/* Gradients of a scalar loss through sfa_add_rms_norm (in the rows' type).  With
+ * r = 1 / sqrt(mean(h^2) + eps), n = h r and g = w dy,
+ *   dx = dr = dh + r (g - n mean(g n)),     dw = sum over rows of dy n.
+ *   H: the sum that the forward kept (X where R was NULL); dY: the gradient of Y;
+ *   dH: that of H from what else reads it, or NULL for none;
+ *   dX [N][dim]: the gradient of X and of R alike; may be dH itself;
+ *   dw [dim] fp32, overwritten (zeros when N = 0);
+ *   workspace: device, 256-byte aligned, contents ignored on entry and clobbered;
+ *     two calls that may overlap need one each; NULL where none is needed.
+ * H, dY, dH and dX [N][dim] are contiguous, of type dtype.  Sums are fp32 in a
+ * fixed order, so results do not change from run to run.  One or two launches;
+ * allocates nothing.  Asynchronous on stream. */
+SFA_API sfa_status sfa_add_rms_norm_backward(sfa_dtype dtype, int N, int dim, const void *H, const float *w, float eps,
+                                             const void *dY, const void *dH, void *dX, float *dw, void *workspace,
+                                             size_t workspace_bytes, cudaStream_t stream);
+
+/* Rows to 8 bits as they are: X8 = round(x / s) with s[t] = max(max |x[t]| / 448,
+ * 2^-126).  For the weights of sfa_qkv_rope_fp8, and for rows that no norm of
+ * this library makes.  Arguments as sfa_add_rms_norm.  One launch. */
+SFA_API sfa_status sfa_quantize_rows_fp8(sfa_dtype dtype, int N, int dim, const void *X, long long x_stride, void *X8,
+                                         float *scale, cudaStream_t stream);
+
+/* sfa_qkv_rope on 8-bit rows and weights:
+ *   [Q | K | V][t][r] = x_scale[t] w_scale[r] sum_c X8[t][c] Wqkv8[r][c],
+ * then the rotation, in fp32, rounded once to bf16.
+ *   p, d_model, rope_table, Qhat, Khat, V, status: as sfa_qkv_rope;
+ *   X8 [B][T][d_model], Wqkv8 [768][d_model] e4m3; x_scale [B][T], w_scale [768] fp32.
+ * Device pointers 16-byte aligned (scales 4-byte).  One launch on the tensor
+ * cores (tcgen05, fp32 accumulation in tensor memory); allocates nothing.
+ * Asynchronous on stream. */
+SFA_API sfa_status sfa_qkv_rope_fp8(const sfa_params *p, int d_model, const void *X8, const float *x_scale,
+                                    const void *Wqkv8, const float *w_scale, const float *rope_table, void *Qhat,
+                                    void *Khat, void *V, unsigned int *status, cudaStream_t stream);
+
 /* ---- failure-path self-test ------------------------------------------- */
 
 /* Exercises the failure path that the pipelined kernels share: every wait on
@@ -484,6 +551,43 @@ SFA_API sfa_status sfa_paged_append(const sfa_params *p, const sfa_paged *c, con
 SFA_API sfa_status sfa_paged_forward(const sfa_params *p, const sfa_paged *c, const void *Q,
                                      long long q_stride, void *O, float *lse,
                                      unsigned int *status, cudaStream_t stream);
+
+/* ---- paged key/value cache in 8 bits ------------------------------------ */
+
+/* A paged cache whose rows are e4m3: half the bytes of a bf16 one.  Rows share a
+ * scale in blocks of block_size consecutive positions of a page, one for the
+ * keys and one for the values of each head: key row j of page g and head h is
+ *   scales[g][j / block_size][0][h] * k_pages[g][j][h][:],
+ * a value row the same with scales[..][1][h]. */
+typedef struct {
+    sfa_paged pages;   /* k_pages, v_pages [num_pages][page_size][Hkv][D] e4m3 */
+    float *scales;     /* device [num_pages][page_size / block_size][2][Hkv] fp32, 16-byte aligned */
+    int block_size;    /* a power of two, 8 .. page_size */
+} sfa_paged_fp8;
+
+/* sfa_paged_append to 8-bit pages.  Keys (normed, rotated) and values stay in fp32
+ * until they are rounded to 8 bits, with the smallest power of two s >= 2^-100 for
+ * which 448 s is at least the size of every finite value that the step brings to
+ * the block, or the block's scale so far, where older rows of the block have one
+ * and it is larger.  Where the scale grows, older rows of the block are written
+ * again with it, c <- round(c s_old / s): exact, but for values that then lie below
+ * 2^-6 s, which are rounded to multiples of 2^-9 s.  A block whose first position
+ * is among the step's tokens starts anew, whatever its scale was.  Rows of a block
+ * behind the step's tokens are left as they are.
+ *   c: as above; a token with a bad position or a bad page is not stored;
+ *   p, Q, K, V, strides, wq, wk, eps, rope_table, Qhat, status: as sfa_paged_append
+ *     (p->dtype: the type of Q, K, V and Qhat).
+ * Two sequences whose tokens go to one block (a page in both tables) race.  One launch;
+ * allocates nothing.  Asynchronous on stream. */
+SFA_API sfa_status sfa_paged_append_fp8(const sfa_params *p, const sfa_paged_fp8 *c, const void *Q, long long q_stride,
+                                        const void *K, long long k_stride, const void *V, long long v_stride,
+                                        const float *wq, const float *wk, float eps, const float *rope_table,
+                                        void *Qhat, unsigned int *status, cudaStream_t stream);
+
+/* sfa_paged_forward over 8-bit pages; p->dtype is the type of Q and O.  Scales need
+ * not be powers of two here: positive and finite will do. */
+SFA_API sfa_status sfa_paged_forward_fp8(const sfa_params *p, const sfa_paged_fp8 *c, const void *Q, long long q_stride,
+                                         void *O, float *lse, unsigned int *status, cudaStream_t stream);
 
 /* ---- device status ----------------------------------------------------- */
 
