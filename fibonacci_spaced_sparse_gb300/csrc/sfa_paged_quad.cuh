@@ -48,8 +48,20 @@
 // rows and zeros.  Nothing of a column's arithmetic depends on another column,
 // so this gives what the first pass would have given without the others' rows,
 // bit for bit.
+//
+// Rows of 8 bits (RowsFp8) come as 16-byte loads, the same 16 dimensions a
+// thread, and are turned into halves, which is exact: both products are f16
+// ones.  A query is scaled by a power of two to a largest element in [1, 2), which
+// its scores take back with the keys' scales, so its halves hold what its bf16
+// values did (but for elements below 2^-14 of the largest, to 2^-25 of it).  A
+// value row's scale joins its probability: p s is rounded to a half, 2^-11 where
+// bf16 pages lose 2^-8, and the running maximum runs over score + log2(s) so that
+// p s stays in range (what is 2^-14 of the largest or less is off by up to 2^-25
+// of it).  The sum for lse takes p alone.  (Turning 8 bits into bf16 instead takes
+// nine operations for four values where halves take two.)
 #pragma once
 
+#include "sfa_fp8.cuh"
 #include "sfa_mma.cuh"
 #include "sfa_paged.cuh"
 
@@ -71,6 +83,24 @@ struct Pair {
     float o[4][4];
     float2 nm, th, l;
 };
+
+// The same with scaled halves; qn: what scales the scores of this thread's columns
+// back.
+struct PairFp8 : Pair {
+    float2 qn;
+};
+
+// 8-bit rows g, g + 8 (bytes 16 t .. 16 t + 15) and their scales.
+struct TileFp8 {
+    uint32_t k[2][4], v[2][4];
+    float ks[2], vs[2];
+};
+
+// Whether a tile's rows have scales.
+template <class X>
+constexpr bool kScaled = false;
+template <>
+constexpr bool kScaled<TileFp8> = true;
 
 __device__ __forceinline__ float2 f2(float x, float y) { return make_float2(x, y); }
 
@@ -117,8 +147,8 @@ __device__ __forceinline__ void load_tile(const char* k, const char* v, int row,
 }
 
 // S^T of a tile and kN pairs: c[0], c[1] row g, c[2], c[3] row g + 8.
-template <int kN>
-__device__ __forceinline__ void scores(const Tile& x, const Pair* U, float (*c)[4]) {
+template <int kN, class P>
+__device__ __forceinline__ void scores(const Tile& x, const P* U, float (*c)[4]) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -137,6 +167,50 @@ __device__ __forceinline__ void value_frag(const Tile& x, int j, uint32_t (&a)[4
     a[1] = movm_t(x.v[0][2 * j + 1]);
     a[2] = movm_t(x.v[1][2 * j]);
     a[3] = movm_t(x.v[1][2 * j + 1]);
+}
+
+// The same of 8-bit rows; word r has dimensions 4 r .. 4 r + 3 of the thread's 16.
+template <int kN, class P>
+__device__ __forceinline__ void scores(const TileFp8& x, const P* U, float (*c)[4]) {
+    uint32_t a[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            a[h][2 * r] = fp8::halves(x.k[h][r] & 0xffffu);
+            a[h][2 * r + 1] = fp8::halves(x.k[h][r] >> 16);
+        }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            if (s == 0)
+                mma16816_f16_z(c[k], a[0][0], a[1][0], a[0][4], a[1][4], U[k].qf[0][0], U[k].qf[0][1]);
+            else
+                mma16816_f16(c[k], a[0][s], a[1][s], a[0][4 + s], a[1][4 + s], U[k].qf[s][0], U[k].qf[s][1]);
+        }
+}
+__device__ __forceinline__ void value_frag(const TileFp8& x, int j, uint32_t (&a)[4]) {
+    a[0] = movm_t(fp8::halves(x.v[0][j] & 0xffffu));
+    a[1] = movm_t(fp8::halves(x.v[0][j] >> 16));
+    a[2] = movm_t(fp8::halves(x.v[1][j] & 0xffffu));
+    a[3] = movm_t(fp8::halves(x.v[1][j] >> 16));
+}
+
+// The value product of a tile and one pair, with the operands' type.
+template <class X>
+__device__ __forceinline__ void value_mma(float (&o)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    if constexpr (kScaled<X>)
+        mma16816_f16(o, a[0], a[1], a[2], a[3], b[0], b[1]);
+    else
+        mma16816(o, a[0], a[1], a[2], a[3], b[0], b[1]);
+}
+template <class X>
+__device__ __forceinline__ void value_mma_z(float (&o)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    if constexpr (kScaled<X>)
+        mma16816_f16_z(o, a[0], a[1], a[2], a[3], b[0], b[1]);
+    else
+        mma16816_z(o, a[0], a[1], a[2], a[3], b[0], b[1]);
 }
 
 // Largest of a column over the eight threads that hold it.
@@ -170,8 +244,8 @@ __device__ __forceinline__ void raise(Pair& U, float2 x) {
 
 // Window tile.  mask: bit 2k (2k + 1) says that row g (g + 8) is in the window
 // of this thread's query of pair k.  kFirst: nothing is accumulated yet.
-template <bool kFirst, class X>
-__device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2, Pair (&U)[2]) {
+template <bool kFirst, class X, class P>
+__device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2, P (&U)[2]) {
     uint32_t b[2][2];
     const float2 sl = f2(sl2, sl2);
     float c[2][4];
@@ -180,11 +254,22 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
     bool over = false;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        lo[k] = __fmul2_rn(f2(c[k][0], c[k][1]), sl);
-        hi[k] = __fmul2_rn(f2(c[k][2], c[k][3]), sl);
+        if constexpr (kScaled<X>) {
+            const float s0 = sl2 * x.ks[0], s1 = sl2 * x.ks[1];
+            lo[k] = __fmul2_rn(f2(c[k][0], c[k][1]), __fmul2_rn(U[k].qn, f2(s0, s0)));
+            hi[k] = __fmul2_rn(f2(c[k][2], c[k][3]), __fmul2_rn(U[k].qn, f2(s1, s1)));
+        } else {
+            lo[k] = __fmul2_rn(f2(c[k][0], c[k][1]), sl);
+            hi[k] = __fmul2_rn(f2(c[k][2], c[k][3]), sl);
+        }
         if (!(mask >> (2 * k) & 1u)) lo[k] = f2(-INFINITY, -INFINITY);
         if (!(mask >> (2 * k + 1) & 1u)) hi[k] = f2(-INFINITY, -INFINITY);
-        top[k] = f2(fmaxf(lo[k].x, hi[k].x), fmaxf(lo[k].y, hi[k].y));
+        if constexpr (kScaled<X>) {
+            const float l0 = __log2f(x.vs[0]), l1 = __log2f(x.vs[1]);
+            top[k] = f2(fmaxf(lo[k].x + l0, hi[k].x + l1), fmaxf(lo[k].y + l0, hi[k].y + l1));
+        } else {
+            top[k] = f2(fmaxf(lo[k].x, hi[k].x), fmaxf(lo[k].y, hi[k].y));
+        }
         if (kFirst) {
             const float2 m = column_max(top[k]);
             U[k].nm = f2(-fmaxf(m.x, kFloor), -fmaxf(m.y, kFloor));
@@ -204,8 +289,13 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
         lo[k] = f2(fast_exp2(lo[k].x), fast_exp2(lo[k].y));
         hi[k] = f2(fast_exp2(hi[k].x), fast_exp2(hi[k].y));
         U[k].l = kFirst ? __fadd2_rn(lo[k], hi[k]) : __fadd2_rn(U[k].l, __fadd2_rn(lo[k], hi[k]));
-        b[k][0] = movm_t(pack_bf16(lo[k].x, lo[k].y));
-        b[k][1] = movm_t(pack_bf16(hi[k].x, hi[k].y));
+        if constexpr (kScaled<X>) {
+            b[k][0] = movm_t(pack_f16(lo[k].x * x.vs[0], lo[k].y * x.vs[0]));
+            b[k][1] = movm_t(pack_f16(hi[k].x * x.vs[1], hi[k].y * x.vs[1]));
+        } else {
+            b[k][0] = movm_t(pack_bf16(lo[k].x, lo[k].y));
+            b[k][1] = movm_t(pack_bf16(hi[k].x, hi[k].y));
+        }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -214,33 +304,44 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (kFirst)
-                mma16816_z(U[k].o[j], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
+                value_mma_z<X>(U[k].o[j], a, b[k]);
             else
-                mma16816(U[k].o[j], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
+                value_mma<X>(U[k].o[j], a, b[k]);
         }
     }
 }
 
 // Rung tiles of kN pairs.  ok: this thread's rung is an entry of its query; t:
 // the rung's fraction.
-template <int kN, class X>
-__device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, float sl2, Pair* U) {
+template <int kN, class X, class P>
+__device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, float sl2, P* U) {
     float c[kN][1][4];
 #pragma unroll
     for (int k = 0; k < kN; ++k) scores<1>(x[k], U + k, c[k]);
     const float u = 1.f - t;
     const float2 tt = f2(t, t), uu = f2(u, u), ts = f2(t * sl2, t * sl2), us = f2(u * sl2, u * sl2);
-    float2 s[kN];
+    float2 s[kN], top[kN];
     bool over = false;
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-        s[k] = __ffma2_rn(ts, f2(c[k][0][0], c[k][0][1]), __fmul2_rn(us, f2(c[k][0][2], c[k][0][3])));
+        if constexpr (kScaled<X>) {
+            const float fs = t * sl2 * x[k].ks[0], ns = u * sl2 * x[k].ks[1];
+            s[k] = __fmul2_rn(__ffma2_rn(f2(fs, fs), f2(c[k][0][0], c[k][0][1]), __fmul2_rn(f2(ns, ns), f2(c[k][0][2], c[k][0][3]))),
+                              U[k].qn);
+        } else {
+            s[k] = __ffma2_rn(ts, f2(c[k][0][0], c[k][0][1]), __fmul2_rn(us, f2(c[k][0][2], c[k][0][3])));
+        }
         if (!ok[k]) s[k] = f2(-INFINITY, -INFINITY);
-        over = over || s[k].x > U[k].th.x || s[k].y > U[k].th.y;
+        top[k] = s[k];
+        if constexpr (kScaled<X>) {
+            const float l = __log2f(fmaxf(t * x[k].vs[0], u * x[k].vs[1]));
+            top[k] = f2(s[k].x + l, s[k].y + l);
+        }
+        over = over || top[k].x > U[k].th.x || top[k].y > U[k].th.y;
     }
     if (__any_sync(kFull, over)) {
 #pragma unroll
-        for (int k = 0; k < kN; ++k) raise(U[k], s[k]);
+        for (int k = 0; k < kN; ++k) raise(U[k], top[k]);
     }
     uint32_t b[kN][2];
 #pragma unroll
@@ -248,9 +349,15 @@ __device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, 
         s[k] = __fadd2_rn(s[k], U[k].nm);
         const float2 p = f2(fast_exp2(s[k].x), fast_exp2(s[k].y));
         U[k].l = __fadd2_rn(U[k].l, p);
-        const float2 far_p = __fmul2_rn(p, tt), near_p = __fmul2_rn(p, uu);
-        b[k][0] = movm_t(pack_bf16(far_p.x, far_p.y));
-        b[k][1] = movm_t(pack_bf16(near_p.x, near_p.y));
+        if constexpr (kScaled<X>) {
+            const float fv = t * x[k].vs[0], nv = u * x[k].vs[1];
+            b[k][0] = movm_t(pack_f16(p.x * fv, p.y * fv));
+            b[k][1] = movm_t(pack_f16(p.x * nv, p.y * nv));
+        } else {
+            const float2 far_p = __fmul2_rn(p, tt), near_p = __fmul2_rn(p, uu);
+            b[k][0] = movm_t(pack_bf16(far_p.x, far_p.y));
+            b[k][1] = movm_t(pack_bf16(near_p.x, near_p.y));
+        }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -258,9 +365,81 @@ __device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, 
         for (int k = 0; k < kN; ++k) {
             uint32_t a[4];
             value_frag(x[k], j, a);
-            mma16816(U[k].o[j], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
+            value_mma<X>(U[k].o[j], a, b[k]);
         }
 }
+
+// The formats of the pages' rows: how a tile is loaded and what becomes of a query.
+struct RowsBf16 {
+    using Tile = paged::Tile;
+    using Pair = paged::Pair;
+    static constexpr int kBytes = 2;  // of an element
+    template <bool kAlone, bool kNatural>
+    static __device__ __forceinline__ void load(const PagedArgs&, int, const char* k, const char* v, int row, int base, Tile& x) {
+        load_tile<kAlone, kNatural>(k, v, row, base, x);
+    }
+    static __device__ __forceinline__ void query(const uint32_t (&w)[8], Pair& U) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            U.qf[j][0] = w[j];
+            U.qf[j][1] = w[4 + j];
+        }
+    }
+};
+
+struct RowsFp8 {
+    using Tile = TileFp8;
+    using Pair = PairFp8;
+    static constexpr int kBytes = 1;
+    template <bool kAlone, bool kNatural>
+    static __device__ __forceinline__ void load(const PagedArgs& c, int g, const char* k, const char* v, int row, int base,
+                                                Tile& x) {
+        const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = __shfl_sync(kFull, row, base + 8 * h + g8);
+            if (kAlone) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) x.k[h][w] = x.v[h][w] = 0u;
+                x.ks[h] = x.vs[h] = 0.f;
+                if (r < 0) continue;
+            }
+            const size_t at = (size_t)(unsigned)r * (kHkv * kD) + 16 * tig;
+            const uint4 a = fresh(reinterpret_cast<const uint4*>(k + at)), b = fresh(reinterpret_cast<const uint4*>(v + at));
+            const float4 s = fresh(reinterpret_cast<const float4*>(row_scales(c, r)));
+            static_assert(kHkv == 2, "a block's scales are one load");
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                x.k[h][w] = word(a, w);
+                x.v[h][w] = word(b, w);
+            }
+            x.ks[h] = g ? s.y : s.x;
+            x.vs[h] = g ? s.w : s.z;
+        }
+    }
+    // The row's halves, its largest element in [1, 2) (an infinite one stays so).
+    static __device__ __forceinline__ void query(const uint32_t (&w)[8], Pair& U) {
+        const int tig = threadIdx.x & 3;
+        float2 v[8];
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = unpack_bf16(w[j]);
+            top = fmaxf(top, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        const int e = min(max(__float_as_int(top) >> 23, 1), 253);
+        const float f = __int_as_float((254 - e) << 23), back = __int_as_float(e << 23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            U.qf[j][0] = pack_f16(v[j].x * f, v[j].y * f);
+            U.qf[j][1] = pack_f16(v[4 + j].x * f, v[4 + j].y * f);
+        }
+        // column n is lane 4 n's; this thread's scores are of columns 2 tig and 2 tig + 1
+        U.qn = f2(__shfl_sync(kFull, back, 8 * tig), __shfl_sync(kFull, back, 8 * tig + 4));
+    }
+};
 
 struct Quad {
     int s, t0, cnt, i0, last, g;
@@ -279,13 +458,13 @@ struct Entry {
 // whose results are not finite (they are not written).  kNatural: the sums of
 // the scores run over the dimensions in their natural order.  kDeep: four tiles
 // of rows in registers instead of two.
-template <bool kAlone, bool kNatural, bool kDeep = false>
+template <bool kAlone, bool kNatural, bool kDeep = false, class F = RowsBf16>
 __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, int only) {
     const int lane = threadIdx.x & 31, g8 = lane >> 2, tig = lane & 3;
     const int W = P.a.W, i0 = Q.i0, last = Q.last;
     const float sl2 = P.a.scale * kLog2e;
-    const char* kb = static_cast<const char*>(P.c.k) + Q.g * (kD * 2);
-    const char* vb = static_cast<const char*>(P.c.v) + Q.g * (kD * 2);
+    const char* kb = static_cast<const char*>(P.c.k) + Q.g * (kD * F::kBytes);
+    const char* vb = static_cast<const char*>(P.c.v) + Q.g * (kD * F::kBytes);
     // this lane's row of the window: position i0 - W + lane
     bool want = lane < W + 4 && i0 - W + lane >= 0 && i0 - W + lane <= last && (!kAlone || (lane >= only && lane <= only + W));
     const int wrow = paged::page_row_if(P.c, Q.s, i0 - W + lane, want);
@@ -304,7 +483,8 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
     };
     int row = nt > 0 ? rung_rows(0) : -1, next = kDeep && nt > 1 ? rung_rows(1) : -1;
     const int fill = kAlone ? -1 : max(__shfl_sync(kFull, wrow, W), 0);  // the first query's own row
-    Pair U[2];
+    using Tile = typename F::Tile;
+    typename F::Pair U[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int qt = Q.t0 + min(2 * k + (g8 >> 2), Q.cnt - 1);
@@ -322,11 +502,7 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
                 w[4 + j] = word(b, j);
             }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            U[k].qf[j][0] = w[j];
-            U[k].qf[j][1] = w[4 + j];
-        }
+        F::query(w, U[k]);
     }
     // window rows of this thread's queries
     unsigned mask[2] = {0u, 0u};
@@ -342,7 +518,9 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
             if (!(w >> (16 * (e >> 2) + 8 * (e & 1) + g8) & 1u)) mask[e >> 2] &= ~(1u << (e & 3));
     }
     const int my_i = (g8 >> 2) == (tig >> 1) ? i0 + (tig >> 1) : -(1 << 30);  // its own rung's query, or none
-    auto load = [&](int r, int half, Tile& x) { load_tile<kAlone, kNatural>(kb, vb, r >= 0 ? r : fill, 16 * half, x); };
+    auto load = [&](int r, int half, Tile& x) {
+        F::template load<kAlone, kNatural>(P.c, Q.g, kb, vb, r >= 0 ? r : fill, 16 * half, x);
+    };
     // of rung tile t with the rows r
     auto entry_of = [&](int t, int r) {
         Entry y;
@@ -428,7 +606,8 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
         const bool stores = qq < Q.cnt && (kAlone ? qq == only : !(redo >> qq & 1u));
         const unsigned who_stores = __ballot_sync(kFull, stores);
         if (!stores) continue;
-        // l >= 2^-8 (the entry at the maximum, at most the margin below it), or 0 with no entry: zeros
+        // l >= 2^-8 (the entry at the maximum, at most the margin below it; with 8-bit rows that
+        // over the largest scale), or 0 with no entry: zeros
         const float2 f = f2(in && l.x != 0.f ? fast_rcp(l.x) : 0.f, in && l.y != 0.f ? fast_rcp(l.y) : 0.f);
         const size_t at = (size_t)(Q.t0 + qq) * kHq + Q.g * kG + 2 * (tig & 1);
         // dimensions 16 (g8 / 2) + g8 % 2 + 2 d, d = 0 .. 7, of both columns; lane ^ 4 has
@@ -460,6 +639,67 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
         }
     }
     return redo;
+}
+
+// ----------------------------------------------------------------- the kernel
+
+// Two tiles of rows on their way or in use, at 168 registers (12 warps a SM), or
+// four (kDeep) at 242 (8 warps), where that keeps every warp resident (us, two and
+// four: one chunk of 512 tokens 4.4 and 4.2, of 2048 7.0 and 5.6; of 3100 6.8 and
+// 9.3, 512 chunks of 2 5.7 and 8.2, 1000 of 16 43 and 49).
+constexpr int kQuadWarps = 4, kDeepSlots = kSms * 2 * kQuadWarps / kHkv;
+
+// A call of its own, so that the rare pass takes no registers of the common one
+// (and one for each kernel: they differ in their registers).
+template <class F, bool kDeep>
+__device__ __noinline__ void one_alone(const PagedFwd& P, const Quad& Q, int only) {
+    quad_pass<true, false, false, F>(P, Q, only);
+}
+
+template <class F, bool kDeep>
+__global__ void __launch_bounds__(kQuadWarps * 32, kDeep ? 2 : 3) quad_kernel(const __grid_constant__ PagedFwd P) {
+    __shared__ int rn[SFA_MAX_RUNGS], rc[SFA_MAX_RUNGS];
+    __shared__ float rt[SFA_MAX_RUNGS];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x < SFA_MAX_RUNGS) {
+        const Rung r = P.a.r[threadIdx.x];
+        rn[threadIdx.x] = r.n;
+        rc[threadIdx.x] = threadIdx.x < P.a.nr ? r.c : 0x7fffffff;
+        rt[threadIdx.x] = r.t;
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // slots of four queries: sequence s starts at slot cu[s] / 4 + s, which
+    // leaves room for ceil(tokens / 4) before the next one's
+    const int slot = (int)(blockIdx.x / kHkv) * kQuadWarps + warp;
+    Quad Q;
+    Q.g = blockIdx.x % kHkv;
+    const paged::Where x = paged::last_at_most(P.c, slot, [](int start, int s) { return (start >> 2) + s; });
+    const int end = x.end;
+    Q.s = x.s;
+    Q.t0 = x.start + 4 * (slot - (x.start >> 2) - x.s);
+    if (Q.t0 < 0 || Q.t0 >= P.c.N || Q.t0 >= end) return;
+    Q.cnt = min(4, min(end, P.c.N) - Q.t0);
+    Q.i0 = x.len - (end - Q.t0);                       // position of the first query
+    Q.last = min(Q.i0 + Q.cnt, P.c.cap) - 1;           // no row behind it is read
+    Q.rn = rn;
+    Q.rc = rc;
+    Q.rt = rt;
+    if (__any_sync(kFull, lane < Q.cnt && (Q.i0 + lane < 0 || Q.i0 + lane >= P.c.cap)) && lane == 0)
+        paged::report(P.c.status);
+    for (unsigned redo = quad_pass<false, false, kDeep, F>(P, Q, -1); redo; redo &= redo - 1)
+        one_alone<F, kDeep>(P, Q, __ffs(redo) - 1);
+}
+
+// Slots of four queries at most (quad_kernel has their places).
+inline long long quad_slots(const PagedArgs& c) { return (long long)c.N / 4 + c.S; }
+
+template <class F>
+cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
+    const long long slots = quad_slots(P.c);
+    void (*const kernel)(PagedFwd) = slots <= kDeepSlots ? quad_kernel<F, true> : quad_kernel<F, false>;
+    return launch_early(kernel, (unsigned)((slots + kQuadWarps - 1) / kQuadWarps * kHkv), kQuadWarps * 32, 0, s, P);
 }
 
 }  // namespace paged
