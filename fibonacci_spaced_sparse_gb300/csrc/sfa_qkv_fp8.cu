@@ -12,13 +12,16 @@
 //                      row) into an mbarrier ring;
 //   warp 1:            one lane issues tcgen05.mma (kind::f8f6f4, M = 128, K = 32)
 //                      into one of two accumulators in tensor memory;
-//   warps 2..9:        the epilogue, two warps a quarter of the lanes, which take
-//                      the heads in turn: a thread has one token's 64 features of
-//                      a head, scales and rotates them and stages them for a TMA
-//                      store of the warp's 32 rows.
+//   the other warps:   the epilogue, a warp for 32 tokens and one head of the
+//                      tile.  The accumulator is read as fragments (16 rows x 8
+//                      columns a quad of lanes at a time) rather than a row a lane:
+//                      a warp then reads the rotation's table in 64-byte pieces of
+//                      eight rows, where a row a lane costs a cache line a lane and
+//                      load (32 x 1024 tokens 32.7 us), and stmatrix puts the rounded
+//                      rows where a TMA store takes them from.
 // What the SMs fetch from L2 is the limit before the tensor cores are: a tile of
 // 128 x 192 takes 40 KB a k-block.  Where a CTA's 192 rows of W8 fit beside the
-// ring (kResident: d_model <= 640) they are loaded once, every CTA keeps to
+// ring (kResident: d_model <= 512) they are loaded once, every CTA keeps to
 // its quarter of the features, and a k-block is the 16 KB of X8 alone.
 //
 // Every wait is bounded; a timeout sets SFA_DEVSTAT_WAIT_TIMEOUT and the CTA
@@ -43,15 +46,14 @@ constexpr int BM = 128;                    // tokens of a tile (TMEM lanes)
 constexpr int BK = 128;                    // columns of a k-block: 128 bytes
 constexpr int kSteps = BK / 32;            // MMAs of a k-block
 constexpr uint32_t kXBytes = BM * BK;      // 16 KB
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kRows = (kHq + 2 * kHkv) * kD;         // 768 output features
 constexpr uint32_t kStoreBytes = 32 * kD * 2;        // a warp's 32 rows of one head
-constexpr int kMaxResident = 5;                      // k-blocks of W8 that stay in shared memory
+constexpr int kMaxResident = 4;                      // k-blocks of W8 that stay in shared memory
 
 template <int kHeads, bool kResident>
 struct Shape {
     static constexpr int kBN = kHeads * kD, kTiles = kRows / kBN;
+    static constexpr int kEpiWarps = 4 * kHeads, kThreads = 32 * (2 + kEpiWarps);
     static constexpr int kStages = kHeads == 1 ? 6 : 4;
     static constexpr uint32_t kWBytes = kBN * BK;    // of a k-block
     static constexpr uint32_t kStageBytes = kXBytes + (kResident ? 0 : kWBytes);
@@ -81,7 +83,7 @@ struct Params {
 };
 
 template <int kHeads, bool kResident>
-__global__ void __launch_bounds__(kThreads, 1) qkv_fp8_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(Shape<kHeads, kResident>::kThreads, 1) qkv_fp8_kernel(const __grid_constant__ Params P) {
     using S = Shape<kHeads, kResident>;
     constexpr uint32_t kIdesc = tc::idesc_e4m3(BM, S::kBN);
     extern __shared__ unsigned char smem_raw[];
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) qkv_fp8_kernel(const __grid_const
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, kEpiWarps);
+            mbar_init(bar_tempty + 8 * b, S::kEpiWarps);
         }
         for (int b = 0; b < kMaxResident; ++b) mbar_init(bar_w + 8 * b, 1);
         *abort_flag = 0;
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) qkv_fp8_kernel(const __grid_const
     }
     if (warp == 1) tc::alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), S::kTmemCols);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = threadIdx.x; i < kRows; i += kThreads) sw[i] = fresh(P.sw + i);
+    for (int i = threadIdx.x; i < kRows; i += S::kThreads) sw[i] = fresh(P.sw + i);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -188,91 +190,87 @@ __global__ void __launch_bounds__(kThreads, 1) qkv_fp8_kernel(const __grid_const
         }
         __syncwarp();
     } else {
-        // epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 (its rows)
-        const int lb = 32 * (warp & 3), half = (warp - 2) >> 2;
+        // epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 (its rows) of head
+        // (w - 2) / 4; this thread's are rows g8, g8 + 8, g8 + 16, g8 + 24 of them
+        const int lb = 32 * (warp & 3), h = (warp - 2) >> 2, g8 = lane >> 2, tig = lane & 3;
         const uint32_t sbuf = stores + (uint32_t)(warp - 2) * kStoreBytes;
+        // of the staged rows (128 bytes, 16-byte chunk c of row r at c ^ (r & 7), the
+        // swizzle of the store map) this lane gives stmatrix the row lane % 16 of a
+        // half, in the first or the last four chunks
+        const int srow = lane & 15, schunk = lane >> 4 << 2;
         int j = 0;
         for (int t = blockIdx.x; t < P.tiles; t += gridDim.x, ++j) {
-            const int buf = j & 1;
-            const int m0 = (t / S::kTiles) * BM, n0 = (t % S::kTiles) * S::kBN;
-            const int m = m0 + lb + lane;
-            // this token's scale and the (cos, sin) row of its position, on their way
+            const int buf = j & 1, m0 = (t / S::kTiles) * BM + lb;
+            const int hh = t % S::kTiles * kHeads + h;  // Q heads 0..7, K heads 8..9, V heads 10..11
+            const bool rot = P.rope != nullptr && hh < kHq + kHkv;
+            // the tokens' scales and the (cos, sin) of their positions are on their way
             // while the tile is computed
-            const float sxm = m < P.M ? fresh(P.sx + m) : 0.f;
-            float4 cs[kPairs / 2];
-            if (P.rope && n0 < (kHq + kHkv) * kD) {
-                const float4* tr = reinterpret_cast<const float4*>(P.rope + (size_t)(m < P.M ? m % P.T : 0) * kPairs);
+            float sx[4];
+            float4 cs[4][4];
 #pragma unroll
-                for (int i = 0; i < kPairs / 2; ++i) cs[i] = fresh(tr + i);
+            for (int r = 0; r < 4; ++r) {
+                const int m = m0 + 8 * r + g8;
+                sx[r] = m < P.M ? fresh(P.sx + m) : 0.f;
+                if (!rot) continue;
+                const float4* row = reinterpret_cast<const float4*>(P.rope + (size_t)(m < P.M ? m % P.T : 0) * kPairs) + tig;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cs[r][i] = fresh(row + 4 * i);  // pairs 8 i + 2 tig and the next one
             }
-            if (!mbar_wait(bar_tfull + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag)) {
+            if (!ring::warp_wait(bar_tfull + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag)) {
                 if (lane == 0) *abort_flag = 1;
                 break;
             }
-            if (*abort_flag) break;
+            if (__any_sync(kFull, *abort_flag != 0)) break;
             tc::fence_after();
-#pragma unroll 1
-            for (int h = (j * kHeads + half) & 1; h < kHeads; h += 2) {
-                uint32_t xu[32], yu[32];
-                const uint32_t ta = tmem + ((uint32_t)lb << 16) + (uint32_t)buf * S::kAccCols + (uint32_t)(h * kD);
-                tc::ld_x32(ta, xu);
-                tc::ld_x32(ta + kPairs, yu);
+            if (lane == 0) bulk_wait_read();  // the store before has read the staged rows
+            __syncwarp();
+            const float2* sw2 = reinterpret_cast<const float2*>(sw + hh * kD) + tig;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t acc[32];
+                tc::ld_frag_x8(tmem + ((uint32_t)(lb + 16 * half) << 16) + (uint32_t)buf * S::kAccCols + (uint32_t)(h * kD), acc);
                 tc::wait_ld();
-                tc::hold(xu);
-                tc::hold(yu);
-                const int hh = n0 / kD + h;  // Q heads 0..7, K heads 8..9, V heads 10..11
-                const bool rot = P.rope != nullptr && hh < kHq + kHkv;
-                const float4* wx = reinterpret_cast<const float4*>(sw + hh * kD);
-                uint32_t xo[16], yo[16];
+                tc::hold(acc);
+                if (half == 1) {
+                    // this warp has read its part of the accumulator
+                    tc::fence_before();
+                    __syncwarp();
+                    mbar_arrive_if(bar_tempty + 8 * buf, lane == 0);
+                }
+                const uint32_t sr = 16 * half + srow, sb = sbuf + sr * 128u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 a = wx[i], b = wx[8 + i];
-                    const float wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-                    float x[4], y[4];
+                for (int i = 0; i < 4; ++i) {
+                    const float2 wx = sw2[4 * i], wy = sw2[16 + 4 * i];
+                    uint32_t out[4];  // columns of 8 i and their partners, rows g8 and g8 + 8
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = __uint_as_float(xu[4 * i + e]) * (sxm * wa[e]);
-                        y[e] = __uint_as_float(yu[4 * i + e]) * (sxm * wb[e]);
-                    }
-                    if (rot) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 q = cs[2 * i + e / 2];  // pairs 4 i + e and its neighbour
-                            const float c = e & 1 ? q.z : q.x, s = e & 1 ? q.w : q.y;
-                            const float u = x[e], v = y[e];
-                            x[e] = __fmaf_rn(u, c, __fmul_rn(-v, s));
-                            y[e] = __fmaf_rn(v, c, __fmul_rn(u, s));
+                    for (int e = 0; e < 2; ++e) {
+                        const float s = sx[2 * half + e];
+                        float x0 = __uint_as_float(acc[4 * i + 2 * e]) * (s * wx.x);
+                        float x1 = __uint_as_float(acc[4 * i + 2 * e + 1]) * (s * wx.y);
+                        float y0 = __uint_as_float(acc[16 + 4 * i + 2 * e]) * (s * wy.x);
+                        float y1 = __uint_as_float(acc[16 + 4 * i + 2 * e + 1]) * (s * wy.y);
+                        if (rot) {
+                            const float4 c = cs[2 * half + e][i];
+                            const float u0 = x0, u1 = x1;
+                            x0 = __fmaf_rn(u0, c.x, __fmul_rn(-y0, c.y));
+                            y0 = __fmaf_rn(y0, c.x, __fmul_rn(u0, c.y));
+                            x1 = __fmaf_rn(u1, c.z, __fmul_rn(-y1, c.w));
+                            y1 = __fmaf_rn(y1, c.z, __fmul_rn(u1, c.w));
                         }
+                        out[e] = pack_bf16(x0, x1);
+                        out[2 + e] = pack_bf16(y0, y1);
                     }
-                    xo[2 * i] = pack_bf16(x[0], x[1]);
-                    xo[2 * i + 1] = pack_bf16(x[2], x[3]);
-                    yo[2 * i] = pack_bf16(y[0], y[1]);
-                    yo[2 * i + 1] = pack_bf16(y[2], y[3]);
-                }
-                // stage the warp's 32 rows (row = lane, 128 bytes, 16-byte chunk c
-                // at c ^ (lane & 7): the 128-byte swizzle of the store map)
-                if (lane == 0) bulk_wait_read();  // the store before has read the buffer
-                __syncwarp();
-                const uint32_t rb = sbuf + (uint32_t)lane * 128u;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    sts_u4(rb + (uint32_t)(((c ^ lane) & 7) << 4), xo[4 * c], xo[4 * c + 1], xo[4 * c + 2], xo[4 * c + 3]);
-                    sts_u4(rb + (uint32_t)((((4 + c) ^ lane) & 7) << 4), yo[4 * c], yo[4 * c + 1], yo[4 * c + 2],
-                           yo[4 * c + 3]);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0 && m0 + lb < P.M) {
-                    const CUtensorMap* map = hh < kHq ? &P.qmap : hh < kHq + kHkv ? &P.kmap : &P.vmap;
-                    const int col = (hh < kHq ? hh : hh < kHq + kHkv ? hh - kHq : hh - kHq - kHkv) * kD;
-                    tma_store_2d(map, sbuf, col, m0 + lb);  // rows past M are not written
-                    bulk_commit();
+                    stsm_x4(sb + (((uint32_t)(schunk + i) ^ (sr & 7u)) << 4), out[0], out[1], out[2], out[3]);
                 }
             }
-            // this warp has read its part of the accumulator
-            tc::fence_before();
+            fence_proxy_async();
             __syncwarp();
-            mbar_arrive_if(bar_tempty + 8 * buf, lane == 0);
+            if (lane == 0 && m0 < P.M) {
+                const CUtensorMap* map = hh < kHq ? &P.qmap : hh < kHq + kHkv ? &P.kmap : &P.vmap;
+                const int col = (hh < kHq ? hh : hh < kHq + kHkv ? hh - kHq : hh - kHq - kHkv) * kD;
+                tma_store_2d(map, sbuf, col, m0);  // rows past M are not written
+                bulk_commit();
+            }
         }
         if (lane == 0) bulk_wait_all();
         if (*abort_flag && lane == 0 && warp == 2 && P.status) atomicOr(P.status, SFA_DEVSTAT_WAIT_TIMEOUT);
@@ -300,7 +298,7 @@ cudaError_t launch(Params& P, const QkvFp8Args& a, int sms, int dev, cudaStream_
     }
     // with W8 in place a CTA keeps its features: a grid of whole rows of tiles
     const int most = kResident ? sms / S::kTiles * S::kTiles : sms;
-    return launch_early(qkv_fp8_kernel<kHeads, kResident>, (unsigned)(P.tiles < most ? P.tiles : most), kThreads, smem, s, P);
+    return launch_early(qkv_fp8_kernel<kHeads, kResident>, (unsigned)(P.tiles < most ? P.tiles : most), S::kThreads, smem, s, P);
 }
 
 }  // namespace
