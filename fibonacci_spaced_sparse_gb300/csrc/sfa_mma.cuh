@@ -257,6 +257,13 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t x) {
     return __bfloat1622float2(h);
 }
 
+// log2 by the hardware approximation, denormals as zeros.
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // 1 / x by the hardware approximation (relative error below 2^-22 for the
 // normal positive x it is used on -- row sums of at least 1 -- far below the
 // bf16 rounding that follows).

@@ -265,7 +265,7 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
         if (!(mask >> (2 * k) & 1u)) lo[k] = f2(-INFINITY, -INFINITY);
         if (!(mask >> (2 * k + 1) & 1u)) hi[k] = f2(-INFINITY, -INFINITY);
         if constexpr (kScaled<X>) {
-            const float l0 = __log2f(x.vs[0]), l1 = __log2f(x.vs[1]);
+            const float l0 = fast_log2(x.vs[0]), l1 = fast_log2(x.vs[1]);
             top[k] = f2(fmaxf(lo[k].x + l0, hi[k].x + l1), fmaxf(lo[k].y + l0, hi[k].y + l1));
         } else {
             top[k] = f2(fmaxf(lo[k].x, hi[k].x), fmaxf(lo[k].y, hi[k].y));
@@ -334,7 +334,7 @@ __device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, 
         if (!ok[k]) s[k] = f2(-INFINITY, -INFINITY);
         top[k] = s[k];
         if constexpr (kScaled<X>) {
-            const float l = __log2f(fmaxf(t * x[k].vs[0], u * x[k].vs[1]));
+            const float l = fast_log2(fmaxf(t * x[k].vs[0], u * x[k].vs[1]));
             top[k] = f2(s[k].x + l, s[k].y + l);
         }
         over = over || top[k].x > U[k].th.x || top[k].y > U[k].th.y;
@@ -643,21 +643,26 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
 
 // ----------------------------------------------------------------- the kernel
 
-// Two tiles of rows on their way or in use, at 168 registers (12 warps a SM), or
-// four (kDeep) at 242 (8 warps), where that keeps every warp resident (us, two and
-// four: one chunk of 512 tokens 4.4 and 4.2, of 2048 7.0 and 5.6; of 3100 6.8 and
-// 9.3, 512 chunks of 2 5.7 and 8.2, 1000 of 16 43 and 49).
-constexpr int kQuadWarps = 4, kDeepSlots = kSms * 2 * kQuadWarps / kHkv;
+// kBlocks a SM: two tiles of rows on their way or in use, at 168 registers (3, 12
+// warps a SM), or four at 242 (2, 8 warps), where that keeps every warp resident
+// (us, two and four: one chunk of 512 tokens 4.4 and 4.2, of 2048 7.0 and 5.6; of
+// 3100 6.8 and 9.3, 512 chunks of 2 5.7 and 8.2, 1000 of 16 43 and 49).  A tile of
+// 8-bit rows has half the words, so that two fit 128 registers as well (4, 16
+// warps), which pays where 12 warps a SM do not hold all (us, 3 and 4: 64 chunks of
+// up to 100 tokens, one wave of 3, 8.2 and 9.9; 1000 of 4 12.7 and 11.2, 32 of
+// 1024 57.6 and 53.1).
+constexpr int kQuadWarps = 4;
+constexpr long long quad_wave(int blocks) { return kSms * (long long)blocks * kQuadWarps / kHkv; }  // slots at once
 
 // A call of its own, so that the rare pass takes no registers of the common one
 // (and one for each kernel: they differ in their registers).
-template <class F, bool kDeep>
+template <class F, int kBlocks>
 __device__ __noinline__ void one_alone(const PagedFwd& P, const Quad& Q, int only) {
     quad_pass<true, false, false, F>(P, Q, only);
 }
 
-template <class F, bool kDeep>
-__global__ void __launch_bounds__(kQuadWarps * 32, kDeep ? 2 : 3) quad_kernel(const __grid_constant__ PagedFwd P) {
+template <class F, int kBlocks>
+__global__ void __launch_bounds__(kQuadWarps * 32, kBlocks) quad_kernel(const __grid_constant__ PagedFwd P) {
     __shared__ int rn[SFA_MAX_RUNGS], rc[SFA_MAX_RUNGS];
     __shared__ float rt[SFA_MAX_RUNGS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -688,8 +693,8 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kDeep ? 2 : 3) quad_kernel(co
     Q.rt = rt;
     if (__any_sync(kFull, lane < Q.cnt && (Q.i0 + lane < 0 || Q.i0 + lane >= P.c.cap)) && lane == 0)
         paged::report(P.c.status);
-    for (unsigned redo = quad_pass<false, false, kDeep, F>(P, Q, -1); redo; redo &= redo - 1)
-        one_alone<F, kDeep>(P, Q, __ffs(redo) - 1);
+    for (unsigned redo = quad_pass<false, false, kBlocks == 2, F>(P, Q, -1); redo; redo &= redo - 1)
+        one_alone<F, kBlocks>(P, Q, __ffs(redo) - 1);
 }
 
 // Slots of four queries at most (quad_kernel has their places).
@@ -698,7 +703,10 @@ inline long long quad_slots(const PagedArgs& c) { return (long long)c.N / 4 + c.
 template <class F>
 cudaError_t launch_quads(const PagedFwd& P, cudaStream_t s) {
     const long long slots = quad_slots(P.c);
-    void (*const kernel)(PagedFwd) = slots <= kDeepSlots ? quad_kernel<F, true> : quad_kernel<F, false>;
+    void (*kernel)(PagedFwd) = slots <= quad_wave(2) ? quad_kernel<F, 2> : quad_kernel<F, 3>;
+    if constexpr (F::kBytes == 1) {
+        if (slots > quad_wave(3)) kernel = quad_kernel<F, 4>;
+    }
     return launch_early(kernel, (unsigned)((slots + kQuadWarps - 1) / kQuadWarps * kHkv), kQuadWarps * 32, 0, s, P);
 }
 
