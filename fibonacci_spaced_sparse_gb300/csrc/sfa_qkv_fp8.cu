@@ -12,13 +12,16 @@
 //                      row) into an mbarrier ring;
 //   warp 1:            one lane issues tcgen05.mma (kind::f8f6f4, M = 128, K = 32)
 //                      into one of two accumulators in tensor memory;
-//   the other warps:   the epilogue, a warp for 32 tokens and one head of the
-//                      tile.  The accumulator is read as fragments (16 rows x 8
-//                      columns a quad of lanes at a time) rather than a row a lane:
-//                      a warp then reads the rotation's table in 64-byte pieces of
-//                      eight rows, where a row a lane costs a cache line a lane and
-//                      load (32 x 1024 tokens 32.7 us), and stmatrix puts the rounded
-//                      rows where a TMA store takes them from.
+//   the other warps:   the epilogue, four warps a tile, 32 tokens each; two sets of
+//                      four take the tiles in turn, so that one has its tokens'
+//                      (cos, sin) rows by the time its accumulator is done (a set of
+//                      12 warps, one a head, waits for them in every tile: 21.1 us
+//                      for 32 x 1024 tokens).  The accumulator is read as fragments
+//                      (16 rows x 8 columns a quad of lanes at a time) rather than a
+//                      row a lane: a warp then reads the rotation's table in 64-byte
+//                      pieces of eight rows, where a row a lane costs a cache line a
+//                      lane and load (32.7 us), and stmatrix puts the rounded rows
+//                      where a TMA store takes them from.
 // What the SMs fetch from L2 is the limit before the tensor cores are: a tile of
 // 128 x 192 takes 40 KB a k-block.  Where a CTA's 192 rows of W8 fit beside the
 // ring (kResident: d_model <= 512) they are loaded once, every CTA keeps to
@@ -47,14 +50,16 @@ constexpr int BK = 128;                    // columns of a k-block: 128 bytes
 constexpr int kSteps = BK / 32;            // MMAs of a k-block
 constexpr uint32_t kXBytes = BM * BK;      // 16 KB
 constexpr int kRows = (kHq + 2 * kHkv) * kD;         // 768 output features
-constexpr uint32_t kStoreBytes = 32 * kD * 2;        // a warp's 32 rows of one head
+constexpr uint32_t kStoreBytes = 16 * kD * 2;        // a warp's 16 rows of a head on their way out
 constexpr int kMaxResident = 4;                      // k-blocks of W8 that stay in shared memory
 
 template <int kHeads, bool kResident>
 struct Shape {
     static constexpr int kBN = kHeads * kD, kTiles = kRows / kBN;
-    static constexpr int kEpiWarps = 4 * kHeads, kThreads = 32 * (2 + kEpiWarps);
-    static constexpr int kStages = kHeads == 1 ? 6 : 4;
+    static constexpr int kSets = kHeads == 1 ? 1 : 2;  // of epilogue warps
+    static constexpr int kEpiWarps = 8 * kSets, kThreads = 32 * (2 + kEpiWarps);
+    static constexpr int kStages = kHeads == 1 ? 6 : kResident ? 3 : 4;
+    static constexpr int kOuts = kResident ? 2 : 1;  // heads' rows of a warp on their way out
     static constexpr uint32_t kWBytes = kBN * BK;    // of a k-block
     static constexpr uint32_t kStageBytes = kXBytes + (kResident ? 0 : kWBytes);
     static constexpr uint32_t kAccCols = kHeads == 1 ? 64 : 256, kTmemCols = 2 * kAccCols;
@@ -64,7 +69,7 @@ struct Shape {
     static constexpr uint32_t kScales = 1024, kData = kScales + 1024 * 3;  // 768 floats
     static constexpr uint32_t resident(int nkb) { return kResident ? (uint32_t)nkb * kWBytes : 0u; }
     static constexpr size_t smem(int nkb) {
-        return 1024 + kData + resident(nkb) + kStages * (size_t)kStageBytes + kEpiWarps * (size_t)kStoreBytes;
+        return 1024 + kData + resident(nkb) + kStages * (size_t)kStageBytes + kEpiWarps * kOuts * (size_t)kStoreBytes;
     }
     static_assert(kRows % kBN == 0 && kAbort + 4 <= kScales && kRows * 4 <= kData - kScales, "layout");
     static_assert(kData % 1024 == 0 && kWBytes % 1024 == 0 && kStageBytes % 1024 == 0, "swizzle periods");
@@ -75,12 +80,14 @@ static_assert(Shape<3, true>::smem(kMaxResident) <= 232448 && Shape<3, false>::s
 
 struct Params {
     CUtensorMap xmap, wmap;         // X8 [M][dm], box 128 x 128; W8 [768][dm], box 128 x kBN
-    CUtensorMap qmap, kmap, vmap;   // outputs as [M][512], [M][128], [M][128], box 64 x 32 (stores)
+    CUtensorMap qmap, kmap, vmap;   // outputs as [M][512], [M][128], [M][128], box 64 x 16 (stores)
     const float *sx, *sw;
     const float2* rope;
     unsigned* status;
     int M, T, nkb, tiles;           // tiles: of all features, features the faster index
 };
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 template <int kHeads, bool kResident>
 __global__ void __launch_bounds__(Shape<kHeads, kResident>::kThreads, 1) qkv_fp8_kernel(const __grid_constant__ Params P) {
@@ -93,12 +100,15 @@ __global__ void __launch_bounds__(Shape<kHeads, kResident>::kThreads, 1) qkv_fp8
     const uint32_t bar_tfull = base + S::kTFull, bar_tempty = base + S::kTEmpty;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(hdr + S::kSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(hdr + S::kAbort);
-    float* sw = reinterpret_cast<float*>(hdr + S::kScales);
     const uint32_t wbase = base + S::kData, stages = wbase + S::resident(P.nkb);
     const uint32_t stores = stages + S::kStages * S::kStageBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 32) {
+        prefetch_map(&P.xmap);
+        prefetch_map(&P.wmap);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(bar_full + 8 * s, 1);
@@ -106,7 +116,7 @@ __global__ void __launch_bounds__(Shape<kHeads, kResident>::kThreads, 1) qkv_fp8
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, S::kEpiWarps);
+            mbar_init(bar_tempty + 8 * b, 8);
         }
         for (int b = 0; b < kMaxResident; ++b) mbar_init(bar_w + 8 * b, 1);
         *abort_flag = 0;
@@ -114,7 +124,6 @@ __global__ void __launch_bounds__(Shape<kHeads, kResident>::kThreads, 1) qkv_fp8
     }
     if (warp == 1) tc::alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), S::kTmemCols);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = threadIdx.x; i < kRows; i += S::kThreads) sw[i] = fresh(P.sw + i);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -190,31 +199,40 @@ __global__ void __launch_bounds__(Shape<kHeads, kResident>::kThreads, 1) qkv_fp8
         }
         __syncwarp();
     } else {
-        // epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 (its rows) of head
-        // (w - 2) / 4; this thread's are rows g8, g8 + 8, g8 + 16, g8 + 24 of them
-        const int lb = 32 * (warp & 3), h = (warp - 2) >> 2, g8 = lane >> 2, tig = lane & 3;
-        const uint32_t sbuf = stores + (uint32_t)(warp - 2) * kStoreBytes;
-        // of the staged rows (128 bytes, 16-byte chunk c of row r at c ^ (r & 7), the
-        // swizzle of the store map) this lane gives stmatrix the row lane % 16 of a
-        // half, in the first or the last four chunks
-        const int srow = lane & 15, schunk = lane >> 4 << 2;
-        int j = 0;
-        for (int t = blockIdx.x; t < P.tiles; t += gridDim.x, ++j) {
-            const int buf = j & 1, m0 = (t / S::kTiles) * BM + lb;
-            const int hh = t % S::kTiles * kHeads + h;  // Q heads 0..7, K heads 8..9, V heads 10..11
-            const bool rot = P.rope != nullptr && hh < kHq + kHkv;
+        // epilogue: warp w reads 16 of TMEM lanes 32 (w % 4) .. + 31 (its rows) of every
+        // second tile; this thread's rows are g8 and g8 + 8 of them
+        const int ew = warp - 2, set = ew >> 3, g8 = lane >> 2, tig = lane & 3;
+        const int lb = 32 * (warp & 3) + 16 * (ew >> 2 & 1);
+        const uint32_t sbuf = stores + (uint32_t)ew * (S::kOuts * kStoreBytes);
+        float* swm = reinterpret_cast<float*>(hdr + S::kScales);
+        for (int i = threadIdx.x - 64; i < kRows; i += 32 * S::kEpiWarps) swm[i] = fresh(P.sw + i);
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * S::kEpiWarps) : "memory");  // of the epilogue's warps
+        int outs = 0;
+        // of the 16 staged rows (128 bytes, 16-byte chunk c of row r at c ^ (r & 7), the
+        // swizzle of the store map) this lane gives stmatrix row lane % 16, in the first
+        // or the last four chunks
+        const uint32_t srow = (uint32_t)(lane & 15) * 128u, schunk = (uint32_t)(lane >> 4 << 2);
+        for (int j = set; blockIdx.x + j * gridDim.x < P.tiles; j += S::kSets) {
+            const int t = blockIdx.x + j * gridDim.x, buf = j & 1, m0 = t / S::kTiles * BM + lb, h0 = t % S::kTiles * kHeads;
             // the tokens' scales and the (cos, sin) of their positions are on their way
             // while the tile is computed
-            float sx[4];
-            float4 cs[4][4];
+            const bool rotates = P.rope != nullptr && h0 < kHq + kHkv;
+            float2 sx[2], cs[2][4], sn[2][4];  // pairs 8 i + 2 tig and the next one
+            const int p0 = rotates ? m0 % P.T + g8 : 0;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < 2; ++r) {
                 const int m = m0 + 8 * r + g8;
-                sx[r] = m < P.M ? fresh(P.sx + m) : 0.f;
-                if (!rot) continue;
-                const float4* row = reinterpret_cast<const float4*>(P.rope + (size_t)(m < P.M ? m % P.T : 0) * kPairs) + tig;
+                sx[r] = both(m < P.M ? fresh(P.sx + m) : 0.f);
+                if (!rotates) continue;
+                int pos = p0 + 8 * r;
+                if (pos >= P.T) pos = P.T >= 16 ? pos - P.T : pos % P.T;
+                const float4* row = reinterpret_cast<const float4*>(P.rope + (size_t)pos * kPairs) + tig;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) cs[r][i] = fresh(row + 4 * i);  // pairs 8 i + 2 tig and the next one
+                for (int i = 0; i < 4; ++i) {
+                    const float4 v = fresh(row + 4 * i);
+                    cs[r][i] = make_float2(v.x, v.z);
+                    sn[r][i] = make_float2(v.y, v.w);
+                }
             }
             if (!ring::warp_wait(bar_tfull + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag)) {
                 if (lane == 0) *abort_flag = 1;
@@ -222,54 +240,53 @@ __global__ void __launch_bounds__(Shape<kHeads, kResident>::kThreads, 1) qkv_fp8
             }
             if (__any_sync(kFull, *abort_flag != 0)) break;
             tc::fence_after();
-            if (lane == 0) bulk_wait_read();  // the store before has read the staged rows
-            __syncwarp();
-            const float2* sw2 = reinterpret_cast<const float2*>(sw + hh * kD) + tig;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            const uint32_t acc0 = tmem + ((uint32_t)lb << 16) + (uint32_t)buf * S::kAccCols;
+#pragma unroll 1
+            for (int h = 0; h < kHeads; ++h) {
+                const int hh = h0 + h;  // Q heads 0..7, K heads 8..9, V heads 10..11
+                const bool rot = rotates && hh < kHq + kHkv;
                 uint32_t acc[32];
-                tc::ld_frag_x8(tmem + ((uint32_t)(lb + 16 * half) << 16) + (uint32_t)buf * S::kAccCols + (uint32_t)(h * kD), acc);
+                tc::ld_frag_x8(acc0 + (uint32_t)(h * kD), acc);
+                const float2* sw = reinterpret_cast<const float2*>(swm + hh * kD) + tig;
+                const uint32_t to = sbuf + (S::kOuts == 2 ? (uint32_t)(outs++ & 1) * kStoreBytes : 0u);
+                if (lane == 0) {  // the store that last took its rows from here has read them
+                    if (S::kOuts == 2)
+                        bulk_wait_read1();
+                    else
+                        bulk_wait_read();
+                }
                 tc::wait_ld();
                 tc::hold(acc);
-                if (half == 1) {
-                    // this warp has read its part of the accumulator
-                    tc::fence_before();
-                    __syncwarp();
-                    mbar_arrive_if(bar_tempty + 8 * buf, lane == 0);
-                }
-                const uint32_t sr = 16 * half + srow, sb = sbuf + sr * 128u;
+                if (h == kHeads - 1) tc::fence_before();  // this warp has read its part of the accumulator
+                __syncwarp();
+                mbar_arrive_if(bar_tempty + 8 * buf, h == kHeads - 1 && lane == 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 wx = sw2[4 * i], wy = sw2[16 + 4 * i];
+                    const float2 wx = sw[4 * i], wy = sw[16 + 4 * i];
                     uint32_t out[4];  // columns of 8 i and their partners, rows g8 and g8 + 8
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float s = sx[2 * half + e];
-                        float x0 = __uint_as_float(acc[4 * i + 2 * e]) * (s * wx.x);
-                        float x1 = __uint_as_float(acc[4 * i + 2 * e + 1]) * (s * wx.y);
-                        float y0 = __uint_as_float(acc[16 + 4 * i + 2 * e]) * (s * wy.x);
-                        float y1 = __uint_as_float(acc[16 + 4 * i + 2 * e + 1]) * (s * wy.y);
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t* a = acc + 4 * i + 2 * r;
+                        float2 x = __fmul2_rn(make_float2(__uint_as_float(a[0]), __uint_as_float(a[1])), __fmul2_rn(wx, sx[r]));
+                        float2 y = __fmul2_rn(make_float2(__uint_as_float(a[16]), __uint_as_float(a[17])), __fmul2_rn(wy, sx[r]));
                         if (rot) {
-                            const float4 c = cs[2 * half + e][i];
-                            const float u0 = x0, u1 = x1;
-                            x0 = __fmaf_rn(u0, c.x, __fmul_rn(-y0, c.y));
-                            y0 = __fmaf_rn(y0, c.x, __fmul_rn(u0, c.y));
-                            x1 = __fmaf_rn(u1, c.z, __fmul_rn(-y1, c.w));
-                            y1 = __fmaf_rn(y1, c.z, __fmul_rn(u1, c.w));
+                            const float2 u = x, c = cs[r][i], n = sn[r][i];
+                            x = make_float2(fmaf(u.x, c.x, -(y.x * n.x)), fmaf(u.y, c.y, -(y.y * n.y)));
+                            y = __ffma2_rn(y, c, __fmul2_rn(u, n));
                         }
-                        out[e] = pack_bf16(x0, x1);
-                        out[2 + e] = pack_bf16(y0, y1);
+                        out[r] = pack_bf16(x.x, x.y);
+                        out[2 + r] = pack_bf16(y.x, y.y);
                     }
-                    stsm_x4(sb + (((uint32_t)(schunk + i) ^ (sr & 7u)) << 4), out[0], out[1], out[2], out[3]);
+                    stsm_x4(to + srow + (((schunk + i) ^ (lane & 7u)) << 4), out[0], out[1], out[2], out[3]);
                 }
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0 && m0 < P.M) {
-                const CUtensorMap* map = hh < kHq ? &P.qmap : hh < kHq + kHkv ? &P.kmap : &P.vmap;
-                const int col = (hh < kHq ? hh : hh < kHq + kHkv ? hh - kHq : hh - kHq - kHkv) * kD;
-                tma_store_2d(map, sbuf, col, m0);  // rows past M are not written
-                bulk_commit();
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0 && m0 < P.M) {
+                    const CUtensorMap* map = hh < kHq ? &P.qmap : hh < kHq + kHkv ? &P.kmap : &P.vmap;
+                    const int col = (hh < kHq ? hh : hh < kHq + kHkv ? hh - kHq : hh - kHq - kHkv) * kD;
+                    tma_store_2d(map, to, col, m0);  // rows past M are not written
+                    bulk_commit();
+                }
             }
         }
         if (lane == 0) bulk_wait_all();
@@ -308,8 +325,8 @@ cudaError_t launch_qkv_fp8(const QkvFp8Args& a, cudaStream_t s) {
     std::memset(&P, 0, sizeof(P));
     const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     if (!encode_rows(&P.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.x, a.M, a.dm, BM) ||
-        !encode_rows(&P.qmap, bf16, 2, a.q, a.M, kHq * kD, 32) || !encode_rows(&P.kmap, bf16, 2, a.k, a.M, kHkv * kD, 32) ||
-        !encode_rows(&P.vmap, bf16, 2, a.v, a.M, kHkv * kD, 32))
+        !encode_rows(&P.qmap, bf16, 2, a.q, a.M, kHq * kD, 16) || !encode_rows(&P.kmap, bf16, 2, a.k, a.M, kHkv * kD, 16) ||
+        !encode_rows(&P.vmap, bf16, 2, a.v, a.M, kHkv * kD, 16))
         return cudaErrorInvalidValue;
     P.sx = a.sx;
     P.sw = a.sw;
