@@ -9,10 +9,12 @@
 // than the one that older rows of the block were written with, those are written
 // again (c <- round(c s_old / s_new), exact but for what becomes subnormal).
 //
-// One warp has a block's keys or values of one head: nobody else touches its
-// rows or its scale, so there are no atomics and no second launch.  Four lanes
-// hold a head row (sfa_heads.cuh), eight rows a warp at a time.  Blocks are found
-// in one of two ways: warps for N / R + 2 S places, where sequence s starts at
+// A thread block has a block of rows, kSplit warps its keys or values of one head:
+// nobody else touches those rows or their scale, so there are no atomics and no second
+// launch.  Four lanes hold a head row (sfa_heads.cuh), eight rows a warp at a time,
+// sixteen in registers between the two passes, so a block of up to 64 rows is read
+// once (64 rows read twice by one warp: 15.0 us for 16 prompts of up to 2048 tokens).
+// Blocks of rows are found in one of two ways: warps for N / R + 2 S places, where sequence s starts at
 // place cu[s] / R + 2 s, which leaves room for all blocks that its tokens can
 // touch; or, where sequences bring about one token each, a warp for every token,
 // which has the token's block if the token is the first there.  Queries are rows
@@ -30,29 +32,34 @@ namespace {
 
 using namespace heads;
 
-constexpr int kThreads = 128;
-constexpr int kRoles = 2 * kHkv;          // warps of a block of rows: keys and values of each head
-constexpr int kQuads = kHq / 2;           // quads of a token's queries
-constexpr int kQueries = kThreads / 4 / kQuads;  // tokens of a thread block of queries
-static_assert(kRoles * 32 == kThreads, "a thread block has one block of rows");
+constexpr int kRoles = 2 * kHkv;  // of a block of rows: keys and values of each head
+template <int kSplit>
+constexpr int kThreads = 32 * kRoles * kSplit;
+
+// Query rows of a quad: four share their token's angles where there are many bf16
+// tokens, two otherwise (us, four and two: 16 prompts of up to 2048 tokens 8.0 and 8.3,
+// fp32 15.4 and 12.9, 100 sequences of two tokens 3.8 and 3.25).
+constexpr int kFourFrom = 4096;
 
 struct Fp8Append {
     AppendArgs a;
     int query_blocks;  // thread blocks of queries, in front
+    bool four;         // query rows of a quad, not two
 };
 
-template <typename T>
+template <typename T, int kEach>
 __device__ __forceinline__ void queries(const AppendArgs& a, int block) {
-    const int quad = block * (kThreads / 4) + (threadIdx.x >> 2), c = threadIdx.x & 3;
+    constexpr int kQuads = kHq / kEach;  // of a token
+    const int quad = block * (int)(blockDim.x / 4) + (threadIdx.x >> 2), c = threadIdx.x & 3;
     const int t = quad / kQuads, role = quad % kQuads;
     const int warp_t = __shfl_sync(kFull, t, 0);
     if (warp_t >= a.c.N) return;
     const bool in_n = t < a.c.N;
     const int tt = in_n ? t : a.c.N - 1;
-    const T* src = static_cast<const T*>(a.q) + (size_t)tt * a.qs + role * 2 * kD;
-    Raw<T> raw[2];
-    fetch(src, c, raw[0]);
-    fetch(src + kD, c, raw[1]);
+    const T* src = static_cast<const T*>(a.q) + (size_t)tt * a.qs + role * kEach * kD;
+    Raw<T> raw[kEach];
+#pragma unroll
+    for (int h = 0; h < kEach; ++h) fetch(src + h * kD, c, raw[h]);
     Row w{};
     if (a.wq) w = weights(a.wq, c);
     bool live;
@@ -62,10 +69,10 @@ __device__ __forceinline__ void queries(const AppendArgs& a, int block) {
     const bool good = pos >= 0 && pos < a.c.cap;
     Angles rot;
     if (a.rope && good) rot = angles(a.rope, pos, c);
-    T* dst = static_cast<T*>(a.qhat) + (size_t)t * (kHq * kD) + role * 2 * kD;
+    T* dst = static_cast<T*>(a.qhat) + (size_t)t * (kHq * kD) + role * kEach * kD;
     const unsigned mask = 0xfu << (threadIdx.x & 28);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kEach; ++h) {
         Row y = open(raw[h]);
         if (a.wq) scale(y, inv_rms(y, a.eps, mask), w);
         if (a.rope && good) rotate(y, rot);
@@ -95,19 +102,29 @@ __device__ __forceinline__ uint2 again(uint2 u, float f) {
     return codes_of(v, f);
 }
 
-// kKept: rows of a block are at most 8 kKept and stay in registers between the
-// two passes; 0: any number, read twice.
-template <typename T, int kKept, bool kPerToken>
-__global__ void __launch_bounds__(kThreads) append_fp8_kernel(const __grid_constant__ Fp8Append P) {
+// kKept: rows of a block are at most 8 kKept kSplit and stay in registers between
+// the two passes; 0: any number, read twice.  With many tokens 24 warps a SM, at 80
+// registers, are faster than what fits without a limit, 16 (us for 16 prompts of up to
+// 2048 tokens 8.3 and 8.9), with single tokens they are slower (256 of them 3.2 and
+// 3.0).
+template <typename T, int kKept, int kSplit, bool kPerToken>
+__global__ void __launch_bounds__(kThreads<kSplit>, kPerToken ? 1 : 6 / kSplit)
+    append_fp8_kernel(const __grid_constant__ Fp8Append P) {
     const AppendArgs& a = P.a;
+    __shared__ float tops[kRoles][kSplit];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((int)blockIdx.x < P.query_blocks) {
-        queries<T>(a, blockIdx.x);
+        if (sizeof(T) == 2 && P.four)
+            queries<T, 4>(a, blockIdx.x);
+        else
+            queries<T, 2>(a, blockIdx.x);
         return;
     }
-    const int unit = (int)blockIdx.x - P.query_blocks, role = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quad = lane >> 2, c = lane & 3, shift = a.c.block_shift;
+    const int unit = (int)blockIdx.x - P.query_blocks, role = (threadIdx.x >> 5) % kRoles, lane = threadIdx.x & 31;
+    const int part = threadIdx.x / (32 * kRoles), quad = 8 * part + (lane >> 2), c = lane & 3;
+    const int shift = a.c.block_shift;
+    constexpr int kStep = 8 * kSplit;  // rows of a role's warps together
     const bool key = role < kHkv;
     const int head = role & (kHkv - 1);
     // the block of rows: positions base .. base + R - 1 of sequence x.s, whose new
@@ -141,6 +158,33 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(const __grid_const
     const int last = min(min(end, a.c.cap) - base, 1 << shift);
     if (min(end - base, 1 << shift) > max(last, first) && threadIdx.x == 0) paged::report(a.c.status);
     if (first >= last) return;
+    const T* src = static_cast<const T*>(key ? a.kn : a.vn) + head * kD;
+    const long long stride = key ? a.ks : a.vs;
+    const int t0 = x.start + (base - at);  // the token row of the block's first position
+    Row w{};
+    if (key && a.wk) w = weights(a.wk, c);
+    auto is_new = [&](int j) { return j >= first && j < last; };
+    auto row_of = [&](int j, const Raw<T>& raw, const Angles& rot) {  // new row j of the block (zeros where there is none)
+        Row y = open(raw);
+        if (key) {
+            if (a.wk) scale(y, inv_rms(y, a.eps), w);
+            if (a.rope) rotate(y, rot);
+            if (!is_new(j)) y = Row{};  // (0 / 0 with eps = 0)
+        }
+        return y;
+    };
+    auto load = [&](int j, Raw<T>& raw, Angles& rot) {
+        raw = Raw<T>{};
+        rot = Angles{};
+        if (!is_new(j)) return;
+        fetch(src + (long long)(t0 + j) * stride, c, raw);
+        if (key && a.rope) rot = angles(a.rope, base + j, c);
+    };
+    // the new rows are on their way while the page and the scale so far are looked up
+    Raw<T> raw[kKept ? kKept : 1];
+    Angles rot[kKept ? kKept : 1];
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) load(kStep * i + quad, raw[i], rot[i]);
     const int row0 = paged::page_row(a.c, x.s, base);
     if (row0 < 0) {
         if (threadIdx.x == 0) paged::report(a.c.status);
@@ -148,77 +192,82 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(const __grid_const
     }
     float* sp = paged::row_scales(a.c, row0) + (key ? 0 : kHkv) + head;
     const float old = first > 0 ? fresh(sp) : 0.f;
-    const T* src = static_cast<const T*>(key ? a.kn : a.vn) + head * kD;
-    const long long stride = key ? a.ks : a.vs;
-    const int t0 = x.start + (base - at);  // the token row of the block's first position
-    Row w{};
-    if (key && a.wk) w = weights(a.wk, c);
-    auto row_of = [&](int j) {  // new row j of the block (zeros where there is none)
-        Raw<T> raw{};
-        const bool in = j >= first && j < last;
-        if (in) fetch(src + (long long)(t0 + j) * stride, c, raw);
-        Row y = open(raw);
-        if (key) {
-            if (a.wk) scale(y, inv_rms(y, a.eps), w);
-            if (a.rope && in) rotate(y, angles(a.rope, base + j, c));
-            if (!in) y = Row{};  // (0 / 0 with eps = 0)
-        }
-        return y;
-    };
     Row kept[kKept ? kKept : 1];
     float top = 0.f;
+    auto again_row = [&](int j) {
+        load(j, raw[0], rot[0]);
+        return row_of(j, raw[0], rot[0]);
+    };
     if (kKept) {
 #pragma unroll
         for (int i = 0; i < kKept; ++i) {
-            kept[i] = row_of(8 * i + quad);
+            kept[i] = row_of(kStep * i + quad, raw[i], rot[i]);
             top = fmaxf(top, top_of(kept[i]));
         }
     } else {
-        for (int j = first & ~7; j < last; j += 8) top = fmaxf(top, top_of(row_of(j + quad)));
+        for (int j = first & -kStep; j < last; j += kStep) top = fmaxf(top, top_of(again_row(j + quad)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    if (kSplit > 1) {  // (what ends a warp above ends the others as well)
+        if (lane == 0) tops[role][part] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSplit; ++i) top = fmaxf(top, tops[role][i]);
+    }
     const float s = fmaxf(fp8::block_scale(top), old), inv = 1.f / s;
     unsigned char* dst = static_cast<unsigned char*>(key ? a.c.k : a.c.v) + (size_t)row0 * (kHkv * kD) + head * kD + 8 * c;
     auto put8 = [&](int j, const Row& y) {
-        if (j < first || j >= last) return;
+        if (!is_new(j)) return;
         unsigned char* p = dst + (size_t)j * (kHkv * kD);
         *reinterpret_cast<uint2*>(p) = codes_of(y.x, inv);
         *reinterpret_cast<uint2*>(p + kPairs) = codes_of(y.y, inv);
     };
     if (kKept) {
 #pragma unroll
-        for (int i = 0; i < kKept; ++i) put8(8 * i + quad, kept[i]);
+        for (int i = 0; i < kKept; ++i) put8(kStep * i + quad, kept[i]);
     } else {
-        for (int j = first & ~7; j < last; j += 8) put8(j + quad, row_of(j + quad));
+        for (int j = first & -kStep; j < last; j += kStep) put8(j + quad, again_row(j + quad));
     }
     if (first > 0 && s > old) {
         const float f = old / s;
-        for (int j = quad; j < first; j += 8) {
+        for (int j = quad; j < first; j += kStep) {
             uint2* p = reinterpret_cast<uint2*>(dst + (size_t)j * (kHkv * kD));
             const uint2 u = fresh(p), v = fresh(p + kPairs / 8);
             p[0] = again(u, f);
             p[kPairs / 8] = again(v, f);
         }
     }
-    if (lane == 0) *sp = s;
+    if (lane == 0 && part == 0) *sp = s;
 }
 
-template <typename T, int kKept>
-cudaError_t launch_blocks(const Fp8Append& P, cudaStream_t s) {
-    const PagedArgs& c = P.a.c;
-    const bool per_token = c.N <= 2LL * c.S;
-    const long long units = per_token ? c.N : ((long long)c.N >> c.block_shift) + 2LL * c.S;
-    return launch_early(per_token ? append_fp8_kernel<T, kKept, true> : append_fp8_kernel<T, kKept, false>,
-                        (unsigned)(P.query_blocks + units), kThreads, 0, s, P);
+template <typename T, int kKept, int kSplit, bool kPerToken>
+cudaError_t launch_blocks(const AppendArgs& a, cudaStream_t s) {
+    const bool four = sizeof(T) == 2 && a.c.N >= kFourFrom;
+    const int tokens = kThreads<kSplit> / 4 / (kHq / (four ? 4 : 2));  // of a thread block of queries
+    const Fp8Append P = {a, a.q ? (a.c.N + tokens - 1) / tokens : 0, four};
+    const long long units = kPerToken ? a.c.N : ((long long)a.c.N >> a.c.block_shift) + 2LL * a.c.S;
+    return launch_early(append_fp8_kernel<T, kKept, kSplit, kPerToken>, (unsigned)(P.query_blocks + units), kThreads<kSplit>, 0,
+                        s, P);
 }
 
+// A thread block a token where sequences bring about one each: one row or two then have
+// to be read, whatever the size of a block of rows (us, a token and a place: 256 single
+// tokens 3.0 and 3.2, 1000 sequences of two 8.3 and 7.5).
 template <typename T>
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
-    const Fp8Append P = {a, a.q ? (a.c.N + kQueries - 1) / kQueries : 0};
-    return a.c.block_shift == 3   ? launch_blocks<T, 1>(P, s)
-           : a.c.block_shift == 4 ? launch_blocks<T, 2>(P, s)
-                                  : launch_blocks<T, 0>(P, s);
+    const int shift = a.c.block_shift;
+    if (2LL * a.c.N <= 3LL * a.c.S)
+        return shift == 3   ? launch_blocks<T, 1, 1, true>(a, s)
+               : shift == 4 ? launch_blocks<T, 2, 1, true>(a, s)
+                            : launch_blocks<T, 0, 1, true>(a, s);
+    switch (shift) {
+        case 3: return launch_blocks<T, 1, 1, false>(a, s);
+        case 4: return launch_blocks<T, 2, 1, false>(a, s);
+        case 5: return launch_blocks<T, 2, 2, false>(a, s);
+        case 6: return launch_blocks<T, 2, 4, false>(a, s);
+        default: return launch_blocks<T, 0, 4, false>(a, s);
+    }
 }
 
 }  // namespace
