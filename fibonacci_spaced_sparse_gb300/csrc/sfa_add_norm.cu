@@ -185,8 +185,14 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_kernel(const AddNorm
 
 // ------------------------------------------------------------------ backward
 
-// Blocks of the backward pass at most: each writes one partial sum of dw.
-constexpr int kBwdBlocks = kSms * 3;
+// Blocks of the backward pass a SM, as many as are resident (48 registers with eight
+// bf16 values a lane, 57 fp32 ones, 80 and 94 with sixteen): each writes one partial sum
+// of dw (us, with one block a SM less and with one more: 32 x 1024 tokens of 512 30.1,
+// 24.4, of 256 15.6, 14.1).  Two rows a warp on their way together, at 112 registers and
+// two blocks, are no faster (24.9).
+template <typename T, int kV>
+constexpr int kBwdEach = kV == 1 ? (sizeof(T) == 2 ? 5 : 4) : (sizeof(T) == 2 ? 3 : 2);
+constexpr int kBwdBlocks = kSms * 5;  // at most
 
 // Block b writes dx of its rows (b, b + gridDim, ... in groups of kRows) and its
 // part of dw to partial[b]; the launch after it sums the parts in a fixed order.
@@ -203,17 +209,14 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const Add
     for (int j = 0; j < kV; ++j) dw[j] = Eight{};
     int turn = 0;
     for (long long row0 = (long long)blockIdx.x * kGroups; row0 < a.N; row0 += (long long)gridDim.x * kGroups, turn ^= 1) {
-        const long long row = row0 + group;
-        const bool live = row < a.N;
-        const long long at = (live ? row : a.N - 1) * a.dim;  // idle warps repeat the last row; it counts once
+        const bool live = row0 + group < a.N;
+        const long long at = (live ? row0 + group : a.N - 1) * a.dim;  // idle warps repeat the last row; it counts once
         Piece<T> ph[kV], pg[kV], pd[kV];
-        bool in[kV];
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int e = 8 * (j * 32 * kW + i);
-            in[j] = e < a.dim;
             ph[j] = pg[j] = pd[j] = Piece<T>{};
-            if (in[j]) {
+            if (e < a.dim) {
                 fetch(static_cast<const T*>(a.h) + at + e, ph[j]);
                 fetch(static_cast<const T*>(a.dy) + at + e, pg[j]);
                 if (a.dh) fetch(static_cast<const T*>(a.dh) + at + e, pd[j]);
@@ -222,8 +225,9 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const Add
         float2 square = both(0.f), cross = both(0.f);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
+            const int e = 8 * (j * 32 * kW + i);
             Piece<float> w{};
-            if (in[j]) fetch(a.w + 8 * (j * 32 * kW + i), w);
+            if (e < a.dim) fetch(a.w + e, w);
             const Eight h = open(ph[j]), g = open(pg[j]), ww = open(w);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -251,8 +255,9 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const Add
         const float2 rr = both(r), m = both(-r * r * (sc * a.inv_dim));  // dx = dh + r (g + h m)
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
+            const int e = 8 * (j * 32 * kW + i);
             Piece<float> w{};
-            if (in[j]) fetch(a.w + 8 * (j * 32 * kW + i), w);
+            if (e < a.dim) fetch(a.w + e, w);
             const Eight h = open(ph[j]), g = open(pg[j]), ww = open(w);
             Eight d = open(pd[j]);
 #pragma unroll
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const Add
             }
             Piece<T> p;
             close(d, p);
-            if (live && in[j]) put(static_cast<T*>(a.dx) + at + 8 * (j * 32 * kW + i), p);
+            if (live && e < a.dim) put(static_cast<T*>(a.dx) + at + e, p);
         }
     }
     float* mine = partial + (size_t)blockIdx.x * a.dim;
@@ -345,15 +350,17 @@ cudaError_t launch_rows(const AddNormArgs& a, cudaStream_t s) {
     });
 }
 
+// Blocks of the backward pass, in the split that by_width chooses.
+template <typename T>
 int bwd_blocks(int N, int dim) {
     const int warps = dim <= 512 ? 1 : dim <= 1024 ? 2 : dim <= 2048 ? 4 : 8, rows = 8 / warps;
-    const int steps = (N + rows - 1) / rows;
-    return steps < kBwdBlocks ? steps : kBwdBlocks;
+    const int steps = (N + rows - 1) / rows, most = kSms * (dim <= 256 ? kBwdEach<T, 1> : kBwdEach<T, 2>);
+    return steps < most ? steps : most;
 }
 
 template <typename T>
 cudaError_t launch_bwd(const AddNormBwdArgs& a, float* ws, cudaStream_t s) {
-    const int blocks = bwd_blocks(a.N, a.dim);
+    const int blocks = bwd_blocks<T>(a.N, a.dim);
     float* partial = blocks > 1 ? ws : a.dw;
     const cudaError_t e = by_width(a.dim, [&](auto v, auto w) {
         return launch_early(add_norm_bwd_kernel<T, v(), w()>, (unsigned)blocks, kRowThreads<w()>, 0, s, a, partial);
@@ -375,8 +382,8 @@ cudaError_t launch_add_norm(const AddNormArgs& a, sfa_dtype dt, bool norm, bool 
                  : launch_rows<float, To::kSame>(a, s);
 }
 
-size_t add_norm_bwd_workspace(int N, int dim) {
-    const int blocks = bwd_blocks(N, dim);
+size_t add_norm_bwd_workspace(sfa_dtype dt, int N, int dim) {
+    const int blocks = dt == SFA_BF16 ? bwd_blocks<__nv_bfloat16>(N, dim) : bwd_blocks<float>(N, dim);
     return blocks > 1 ? (size_t)blocks * dim * sizeof(float) : 0;
 }
 

@@ -79,7 +79,7 @@ struct AddNormBwdArgs {
     void* dx;
     float* dw;
 };
-size_t add_norm_bwd_workspace(int N, int dim);  // 0: none
+size_t add_norm_bwd_workspace(sfa_dtype dt, int N, int dim);  // 0: none
 cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, sfa_dtype dt, void* ws, cudaStream_t s);
 
 // A paged cache and one step's tokens (sfa_paged in sfa.h).

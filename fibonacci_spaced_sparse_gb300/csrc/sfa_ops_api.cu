@@ -333,7 +333,7 @@ SFA_API sfa_status sfa_quantize_rows_fp8(sfa_dtype dtype, int N, int dim, const 
 }
 
 SFA_API size_t sfa_add_rms_norm_backward_workspace_size(sfa_dtype dtype, int N, int dim) {
-    return check_rows(dtype, N, dim) != SFA_OK || N == 0 ? 0 : sfa::add_norm_bwd_workspace(N, dim);
+    return check_rows(dtype, N, dim) != SFA_OK || N == 0 ? 0 : sfa::add_norm_bwd_workspace(dtype, N, dim);
 }
 
 SFA_API sfa_status sfa_add_rms_norm_backward(sfa_dtype dtype, int N, int dim, const void* H, const float* w, float eps,
@@ -349,7 +349,7 @@ SFA_API sfa_status sfa_add_rms_norm_backward(sfa_dtype dtype, int N, int dim, co
     if (!H || !dY || !dX || !w || !aligned16(H) || !aligned16(dY) || !aligned16(dH) || !aligned16(dX) || !aligned16(w) ||
         !std::isfinite(eps) || eps < 0.f)
         return SFA_ERR_INVALID_ARG;
-    const size_t need = sfa::add_norm_bwd_workspace(N, dim);
+    const size_t need = sfa::add_norm_bwd_workspace(dtype, N, dim);
     if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need))
         return SFA_ERR_INVALID_ARG;
     const sfa::AddNormBwdArgs a = {N, dim, H, dY, dH, w, eps, 1.f / (float)dim, dX, dw};

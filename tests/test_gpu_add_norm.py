@@ -170,7 +170,7 @@ def backward64(h, w, dy, dh=None, eps=EPS):
     if dh is not None:
         dx = dx + dh.double()
         size = size + dh.double().abs()
-    rows = -(-h.shape[0] // 456) + 40
+    rows = -(-h.shape[0] // 304) + 40
     return dx, (dy * n).sum(0), 200 * U * size, (45 + rows) * U * (dy * n).abs().sum(0)
 
 
@@ -221,7 +221,7 @@ def test_backward_many_rows_in_place_and_given_buffers(dtype):
         h, dy, dh, w = _rows(N, dim, dtype), _rows(N, dim, dtype, 1), _rows(N, dim, dtype, 2), _weight(dim)
         want, want_w, bx, bw = backward64(h, w, dy, dh)
         own = dh.cuda()
-        need = 4 * dim * 456
+        need = 4 * dim * 760
         room = torch.full((dim + 8,), 7.0, device="cuda")
         ws = torch.full((need + 256,), 0xff, dtype=torch.uint8, device="cuda")
         dx, dw = api.sfa_add_rms_norm_backward(h.cuda(), w.cuda(), dy.cuda(), own, out=(own, room[4:4 + dim]), workspace=ws[:need])
@@ -266,7 +266,7 @@ def test_captured_steps_in_a_row(N, dim, dtype):
     x, r, dh, h, y = bufs
     y8, s = torch.zeros((N, dim), dtype=torch.uint8, device="cuda").view(FP8), torch.zeros(N, device="cuda")
     dx, dw = torch.zeros((N, dim), dtype=DT[dtype], device="cuda"), torch.zeros(dim, device="cuda")
-    ws = torch.zeros(4 * dim * 456, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(4 * dim * 760, dtype=torch.uint8, device="cuda")
 
     def step():
         api.sfa_add_rms_norm(x, r, w, out=(h, y))
