@@ -104,7 +104,8 @@ _SIGS = {
     "sfa_qkv_rope_fp8": ([_PP, ctypes.c_int] + [_VP] * 10, ctypes.c_int),
     "sfa_paged_append_fp8": ([_PP, _C8, _VP, _LL, _VP, _LL, _VP, _LL, _VP, _VP, ctypes.c_float, _VP, _VP, _VP, _VP],
                              ctypes.c_int),
-    "sfa_paged_forward_fp8": ([_PP, _C8, _VP, _LL, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "sfa_paged_forward_fp8_workspace_size": ([_PP, _C8], ctypes.c_size_t),
+    "sfa_paged_forward_fp8": ([_PP, _C8, _VP, _LL, _VP, _VP, _VP, ctypes.c_size_t, _VP, _VP], ctypes.c_int),
     "sfa_backward_workspace_size": ([_PP], ctypes.c_size_t),
     "sfa_backward": ([_PP] + [_VP] * 13 + [ctypes.c_size_t, _VP, _VP], ctypes.c_int),
     "sfa_read_status": ([_VP, ctypes.POINTER(ctypes.c_uint), _VP], ctypes.c_int),

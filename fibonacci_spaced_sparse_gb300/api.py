@@ -538,17 +538,19 @@ def sfa_paged_append_fp8(k, v, k_pages, v_pages, page_scales, block_table, cu_q,
 
 
 def sfa_paged_forward_fp8(q, k_pages, v_pages, page_scales, block_table, cu_q, seq_lens, *, alpha: float, W: int,
-                          rungs=FIBONACCI_BASE, scale: float = 0.0, need_lse: bool = True, out=None, lse=None, status=None,
-                          stream=None, round_offsets: bool = False):
+                          rungs=FIBONACCI_BASE, scale: float = 0.0, need_lse: bool = True, out=None, lse=None, workspace=None,
+                          status=None, stream=None, round_offsets: bool = False):
     """sfa_paged_forward over a cache of 8-bit rows, as sfa_paged_append_fp8 fills
-    it; q and the results in bf16 or fp32.  Everything else as there."""
+    it; q and the results in bf16 or fp32.  Everything else as there.
+    ``workspace`` (uint8) may supply the scratch of calls with long chunks; calls
+    that may overlap need one each."""
     if stream is not None:
         with _on(stream):
             return sfa_paged_forward_fp8(q, k_pages, v_pages, page_scales, block_table, cu_q, seq_lens, alpha=alpha, W=W,
-                                         rungs=rungs, scale=scale, need_lse=need_lse, out=out, lse=lse, status=status,
-                                         round_offsets=round_offsets)
+                                         rungs=rungs, scale=scale, need_lse=need_lse, out=out, lse=lse, workspace=workspace,
+                                         status=status, round_offsets=round_offsets)
     return _native().paged_forward_fp8(q, k_pages, v_pages, page_scales, block_table, cu_q, seq_lens, alpha, W, rungs, scale,
-                                       need_lse, out, lse, status, round_offsets)
+                                       need_lse, out, lse, status, round_offsets, workspace)
 
 
 def sfa_read_status(status: torch.Tensor, stream=None) -> int:

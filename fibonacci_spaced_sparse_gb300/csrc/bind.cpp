@@ -168,6 +168,29 @@ struct Out {
     }
 };
 
+// A workspace: the given one, or a new one of the size that need() asks for.
+struct Scratch {
+    Tensor made;
+    const Tensor& ref;
+    const bool own;
+    void* ptr = nullptr;
+    size_t bytes = 0;
+    Scratch(PyObject* o, const Tensor& r) : ref(r), own(o == Py_None) {
+        if (own) return;
+        const Tensor& t = tensor(o, "workspace");
+        if (t.device() != r.device() || !t.is_contiguous())
+            refuse("workspace must be a contiguous tensor on " + r.device().str());
+        ptr = t.data_ptr();
+        bytes = (size_t)t.nbytes();
+    }
+    void need(size_t n) {
+        if (!own || n == 0) return;
+        made = empty({(int64_t)n}, at::kByte, ref);
+        ptr = made.data_ptr();
+        bytes = n;
+    }
+};
+
 double number(PyObject* o) {
     const double x = PyFloat_AsDouble(o);
     if (x == -1.0 && PyErr_Occurred()) throw python_error();
@@ -426,9 +449,9 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return app
 PyObject* paged_append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_to("paged_append_fp8", true, a, n); }
 
 // q, k_pages, v_pages, (page_scales,) block_table, cu_q, seq_lens, alpha, W, rungs, scale, need_lse, out, lse, status,
-// round_offsets
+// round_offsets(, workspace)
 PyObject* forward_over(const char* name, bool fp8, PyObject* const* a, Py_ssize_t n) {
-    return guarded(name, n, fp8 ? 16 : 15, [&]() -> PyObject* {
+    return guarded(name, n, fp8 ? 17 : 15, [&]() -> PyObject* {
         const std::string call_name = std::string("sfa_") + name;
         const Tensor& q = tensor(a[0], "q");
         if (q.dim() != 3) refuse("q must be [N, 8, 64], got " + shape_text(q.sizes()));
@@ -458,10 +481,12 @@ PyObject* forward_over(const char* name, bool fp8, PyObject* const* a, Py_ssize_
         const bool need_lse = truth(a[10]);
         Out lse(need_lse ? a[12] : Py_None, "lse", lse_shape, at::kFloat, x.k);
         const auto stream = c10::cuda::getCurrentCUDAStream(x.k.device().index()).stream();
+        Scratch scratch(fp8 ? a[15] : Py_None, x.k);
         call(call_name.c_str(), [&] {
             void* o = out.make();
             float* l = need_lse ? static_cast<float*>(lse.make()) : nullptr;
-            return fp8 ? sfa_paged_forward_fp8(&p, &x.f, q.data_ptr(), qs, o, l, status, stream)
+            if (fp8) scratch.need(sfa_paged_forward_fp8_workspace_size(&p, &x.f));
+            return fp8 ? sfa_paged_forward_fp8(&p, &x.f, q.data_ptr(), qs, o, l, scratch.ptr, scratch.bytes, status, stream)
                        : sfa_paged_forward(&p, &x.c, q.data_ptr(), qs, o, l, status, stream);
         });
         if (!need_lse) return tuple_of({out.object(), Py_NewRef(Py_None)});
@@ -568,29 +593,16 @@ PyObject* add_rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const void* dy = dense(tensor(a[2], "dy"), "dy", in.x.sizes(), type, in.x);
         const void* dh = dense_or_null(a[3], "dh", in.x.sizes(), type, in.x);
         const double eps = number(a[4]);
-        Tensor scratch;
-        void* ws = nullptr;
-        size_t bytes = 0;
-        const bool own_scratch = a[5] == Py_None;
-        if (!own_scratch) {
-            const Tensor& t = tensor(a[5], "workspace");
-            if (t.device() != in.x.device() || !t.is_contiguous())
-                refuse("workspace must be a contiguous tensor on " + in.x.device().str());
-            ws = t.data_ptr();
-            bytes = (size_t)t.nbytes();
-        }
+        Scratch scratch(a[5], in.x);
         c10::cuda::OptionalCUDAGuard guard(in.x.device());
         Out dx(a[6], "out[0]", in.x.sizes(), type, in.x), dw(a[7], "out[1]", {in.dim}, at::kFloat, in.x);
         const auto stream = c10::cuda::getCurrentCUDAStream(in.x.device().index()).stream();
         call("sfa_add_rms_norm_backward", [&] {
             const int N = small(in.N), dim = small(in.dim);
-            if (own_scratch && (bytes = sfa_add_rms_norm_backward_workspace_size(in.dt, N, dim)) != 0) {
-                scratch = empty({(int64_t)bytes}, at::kByte, in.x);
-                ws = scratch.data_ptr();
-            }
+            scratch.need(sfa_add_rms_norm_backward_workspace_size(in.dt, N, dim));
             void* to = dx.make();
-            return sfa_add_rms_norm_backward(in.dt, N, dim, h, w, (float)eps, dy, dh, to, static_cast<float*>(dw.make()), ws, bytes,
-                                             stream);
+            return sfa_add_rms_norm_backward(in.dt, N, dim, h, w, (float)eps, dy, dh, to, static_cast<float*>(dw.make()),
+                                             scratch.ptr, scratch.bytes, stream);
         });
         return tuple_of({dx.object(), dw.object()});
     });

@@ -107,8 +107,9 @@ cudaError_t launch_paged_append(const AppendArgs& a, sfa_dtype dt, cudaStream_t 
 cudaError_t launch_paged_append_fp8(const AppendArgs& a, sfa_dtype dt, cudaStream_t s);
 cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs, void* o,
                              float* lse, cudaStream_t s);
+size_t paged_fwd_fp8_workspace(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt);  // 0: none
 cudaError_t launch_paged_fwd_fp8(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs,
-                                 void* o, float* lse, cudaStream_t s);
+                                 void* o, float* lse, void* ws, cudaStream_t s);
 
 // The projection of 8-bit rows (sfa_qkv_fp8.cu).
 struct QkvFp8Args {

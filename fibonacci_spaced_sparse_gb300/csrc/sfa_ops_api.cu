@@ -294,16 +294,29 @@ SFA_API sfa_status sfa_paged_append_fp8(const sfa_params* p, const sfa_paged_fp8
     return launched(sfa::launch_paged_append_fp8(a, p->dtype, stream));
 }
 
+SFA_API size_t sfa_paged_forward_fp8_workspace_size(const sfa_params* p, const sfa_paged_fp8* c) {
+    LayerArgs l;
+    sfa::PagedArgs a;
+    if (!c || validate_paged(p, &l) != SFA_OK || c->pages.N < 1 || c->pages.N > kMaxRows || p->B == 0 ||
+        check_paged(p, &c->pages, nullptr, &a) != SFA_OK)
+        return 0;
+    return sfa::paged_fwd_fp8_workspace(l, a, p->dtype);
+}
+
 SFA_API sfa_status sfa_paged_forward_fp8(const sfa_params* p, const sfa_paged_fp8* c, const void* Q, long long q_stride,
-                                         void* O, float* lse, unsigned int* status, cudaStream_t stream) {
+                                         void* O, float* lse, void* workspace, size_t workspace_bytes, unsigned int* status,
+                                         cudaStream_t stream) {
     LayerArgs l;
     sfa::PagedArgs a;
     bool nothing;
     sfa_status st = check_forward(p, c ? &c->pages : nullptr, Q, q_stride, O, lse, status, &l, &a, &nothing);
     if (st != SFA_OK || nothing) return st;
     if ((st = check_blocks(c, &a)) != SFA_OK) return st;
+    const size_t need = sfa::paged_fwd_fp8_workspace(l, a, p->dtype);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need))
+        return SFA_ERR_INVALID_ARG;
     if (sfa::fault_injected()) return SFA_ERR_CUDA;
-    return launched(sfa::launch_paged_fwd_fp8(l, a, p->dtype, Q, q_stride, O, lse, stream));
+    return launched(sfa::launch_paged_fwd_fp8(l, a, p->dtype, Q, q_stride, O, lse, workspace, stream));
 }
 
 SFA_API sfa_status sfa_add_rms_norm(sfa_dtype dtype, int N, int dim, const void* X, long long x_stride, const void* R,

@@ -1,6 +1,16 @@
 // sfa_paged_fp8.cu -- attention of a step's tokens over a paged cache of 8-bit
 // rows (sfa_paged_forward_fp8 in include/sfa.h): the kernels of
-// sfa_paged_fwd.cu on such rows, and the rule between them.
+// sfa_paged_fwd.cu on such rows, and the rules between them.
+//
+// Long chunks: a row is an entry of some ten queries' key lists and stands in as many
+// tiles, and turning it from 8 bits costs more than the bytes it saves once it is in
+// L2.  So the rows that the chunks can reach are turned into bf16 once, into pages of
+// their own in the caller's workspace, and the kernel for long chunks of bf16 pages
+// runs on those (32 x 1024 tokens: 53.1 us for quads on 8-bit rows).
+// Sequence s reaches from position c - back on, c its rows before the step and back the
+// farthest row of a key list.  Its pages start at place (cu[s] >> shift) + s * extra of
+// the workspace, and at position 64 h of the sequence: all positions move by that, which
+// changes no mask, since every entry of a query exists from position back on.
 #include "sfa_paged_quad.cuh"
 #include "sfa_paged_rows.cuh"
 
@@ -9,12 +19,119 @@ namespace sfa {
 using namespace paged;
 
 namespace {
-constexpr int kQuadsFrom = 305;
+
+struct Expand {
+    PagedArgs c;
+    uint4 *k, *v;         // bf16 rows, [places][rows of a page][Hkv][D]
+    int *table, *lens;    // [S][cols], [S]: the pages and lengths that the attention sees
+    int back, extra;      // rows, pages before a sequence's chunk
+    int shift, cols;      // log2 of the rows of such a page; entries of a sequence
+    int cap, places;      // positions [0, cap) exist, as it sees them; pages
+};
+
+constexpr int kExpandRows = 16, kRowChunks = kHkv * kD / 16;  // of a thread block; 16-byte pieces of a row
+constexpr int kExpandThreads = 2 * kExpandRows * kRowChunks;  // a piece of keys or values each
+
+// 16 codes and their scale as bf16.
+__device__ __forceinline__ void expand16(uint4 u, float s, uint4* to) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 v = fp8::values2(j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu);
+        o[j] = pack_bf16(v.x * s, v.y * s);
+    }
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// A thread block for 16 rows of a page.
+__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ Expand E) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PagedArgs& c = E.c;
+    const int parts = E.shift - 4, place = blockIdx.x >> parts, part = blockIdx.x & ((1 << parts) - 1);
+    static_assert(kExpandRows == 1 << 4, "parts of a page");
+    const paged::Where x = paged::last_at_most(c, place, [&](int start, int s) { return (start >> E.shift) + s * E.extra; });
+    const int n = place - (x.start >> E.shift) - x.s * E.extra;  // of the sequence's pages
+    if (n < 0) return;
+    // first page that is read, and the one that becomes number 0: the same, but where the
+    // sequence's length passes the capacity, which then has to stay where it is
+    const int before = x.len - max(x.end - x.start, 0), first = max(before - E.back, 0) >> E.shift;
+    const int h = x.len > c.cap ? (c.cap - E.cap) >> E.shift : first;
+    if (n == 0 && part == 0 && threadIdx.x == 0) E.lens[x.s] = x.len - (h << E.shift);
+    const int index = first + n, at = index - h;
+    if (index > (min(x.len, c.cap) - 1) >> E.shift || at < 0 || at >= E.cols) return;
+    const int row0 = paged::page_row(c, x.s, index << E.shift);
+    if (part == 0 && threadIdx.x == 0) E.table[(size_t)x.s * E.cols + at] = row0 < 0 ? -1 : place;
+    if (row0 < 0) return;
+    const bool value = threadIdx.x >= kExpandThreads / 2;
+    const int piece = threadIdx.x % (kExpandThreads / 2), row = part * kExpandRows + piece / kRowChunks;
+    const size_t i = (size_t)row0 * kRowChunks + part * kExpandRows * kRowChunks + piece;
+    const uint4 u = fresh(static_cast<const uint4*>(value ? c.v : c.k) + i);
+    const int head = piece % kRowChunks / (kRowChunks / kHkv);
+    const float s = fresh(paged::row_scales(c, row0 + row) + (value ? kHkv : 0) + head);
+    expand16(u, s, (value ? E.v : E.k) + 2 * ((((size_t)place << E.shift) + part * kExpandRows) * kRowChunks + piece));
+}
+
+constexpr int kQuadsFrom = 305, kTilesEach = 32;  // as in sfa_paged_fwd.cu
+// Tokens from which rows are expanded (us, quads and expanded: one chunk of 4800 10.0
+// and 14.1, of 6000 14.4 and 14.4, of 8000 16.4 and 14.5, of 12000 24.1 and 22.6; 16
+// chunks of 512 behind 2000 rows 17.0 and 15.7; 32 x 1024 in pages of 64 rows 52.9 and
+// 37.1, of 16 53.7 and 41.0).
+constexpr int kExpandFrom = 7000;
+
+// Whether a call's rows are expanded, and how.
+bool expands(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, Expand* E) {
+    if (dt != SFA_BF16 || a.W > 28 || c.shift < 4 || c.N < kExpandFrom || c.N < kTilesEach * (long long)c.S) return false;
+    E->c = c;
+    E->shift = c.shift < 6 ? c.shift : 6;
+    E->back = a.W;
+    for (int i = 0; i < a.nr; ++i) E->back = E->back > a.r[i].n + 1 ? E->back : a.r[i].n + 1;
+    E->extra = (E->back >> E->shift) + 3;
+    // (at most three rows expanded for one of the chunks, and a table of no more words)
+    const long long own = c.N >> E->shift, reach = (long long)c.S * E->extra, cols = own + E->extra;
+    if (reach > 2 * own || cols * c.S > 4LL * c.N) return false;
+    E->cols = (int)cols;
+    E->places = (int)(own + reach);
+    const int rows = 1 << E->shift;
+    const long long room = cols * rows - (rows - c.cap % rows) % rows;
+    E->cap = c.cap <= room ? c.cap : (int)room;
+    return true;
+}
+
+size_t page_bytes(const Expand& E) { return ((size_t)E.places << E.shift) * kHkv * kD * 2; }
+
+}  // namespace
+
+size_t paged_fwd_fp8_workspace(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt) {
+    Expand E;
+    return expands(a, c, dt, &E) ? 2 * page_bytes(E) + ((size_t)E.cols + 1) * c.S * sizeof(int) : 0;
 }
 
 cudaError_t launch_paged_fwd_fp8(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs,
-                                 void* o, float* lse, cudaStream_t s) {
+                                 void* o, float* lse, void* ws, cudaStream_t s) {
     const PagedFwd P = {a, c, q, qs, o, lse};
+    Expand E;
+    if (expands(a, c, dt, &E)) {
+        char* at = static_cast<char*>(ws);
+        E.k = reinterpret_cast<uint4*>(at);
+        E.v = reinterpret_cast<uint4*>(at + page_bytes(E));
+        E.table = reinterpret_cast<int*>(at + 2 * page_bytes(E));
+        E.lens = E.table + (size_t)E.cols * c.S;
+        const cudaError_t e = launch_early(expand_kernel, (unsigned)E.places << (E.shift - 4), kExpandThreads, 0, s, E);
+        if (e != cudaSuccess) return e;
+        PagedFwd B = P;
+        B.c.k = E.k;
+        B.c.v = E.v;
+        B.c.table = E.table;
+        B.c.lens = E.lens;
+        B.c.max_pages = E.cols;
+        B.c.num_pages = E.places;
+        B.c.shift = E.shift;
+        B.c.cap = E.cap;
+        return launch_paged_tiles(B, s);
+    }
     if (dt == SFA_BF16 && a.W <= 28 && c.N >= kQuadsFrom && c.N >= 2 * (long long)c.S) return launch_quads<RowsFp8>(P, s);
     return dt == SFA_BF16 ? launch_rows<__nv_bfloat16, __nv_fp8_e4m3>(P, s) : launch_rows<float, __nv_fp8_e4m3>(P, s);
 }

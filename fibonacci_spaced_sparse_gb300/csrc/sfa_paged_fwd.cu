@@ -29,7 +29,7 @@ constexpr int kQuadsFrom = 305;
 // of 28 14.6 and 16.5, 256 of 16 12.2 and 13.1; 8 chunks of 512 beside 56 single
 // tokens 8.7 and 8.9, beside 192 9.1 and 13.3).  A smaller call would wait for
 // the host besides, which makes the tiles' maps in 3 us.
-constexpr int kQuadsWave = kSms * 3 * kQuadWarps / kHkv, kTilesEach = 32;
+constexpr int kTilesEach = 32;
 
 }  // namespace
 
@@ -39,7 +39,7 @@ cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype d
     // the tensor-core kernels load 32 bytes of a row at a time
     const bool wide = ((reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) & 31u) == 0;
     if (dt == SFA_BF16 && a.W <= 28 && wide) {
-        if (quad_slots(c) > kQuadsWave && c.N >= kTilesEach * (long long)c.S && c.shift >= 4)
+        if (quad_slots(c) > quad_wave(3) && c.N >= kTilesEach * (long long)c.S && c.shift >= 4)
             return launch_paged_tiles(P, s);
         if (c.N >= kQuadsFrom && c.N >= 2 * (long long)c.S) return launch_quads<RowsBf16>(P, s);
     }

@@ -584,10 +584,21 @@ SFA_API sfa_status sfa_paged_append_fp8(const sfa_params *p, const sfa_paged_fp8
                                         const float *wq, const float *wk, float eps, const float *rope_table,
                                         void *Qhat, unsigned int *status, cudaStream_t stream);
 
+/* Bytes of device workspace sfa_paged_forward_fp8 needs (0: none).  The long chunks
+ * of a bf16 call are attended over bf16 copies of the rows that they reach. */
+SFA_API size_t sfa_paged_forward_fp8_workspace_size(const sfa_params *p, const sfa_paged_fp8 *c);
+
 /* sfa_paged_forward over 8-bit pages; p->dtype is the type of Q and O.  Scales need
- * not be powers of two here: positive and finite will do. */
+ * not be powers of two here: anything from 2^-100 to 2^100 will do (a value times a
+ * scale that is no power of two is rounded to bf16 where rows are copied).
+ *   workspace: device, 256-byte aligned, contents ignored on entry and clobbered;
+ *     two calls that may overlap need one each; NULL where none is needed.
+ * One launch, or two with a workspace.  Errors of the results as sfa_paged_forward's;
+ * without a workspace probabilities on the tensor cores are rounded to fp16 instead
+ * of bf16, and the error of O is 1.7e-3 of its norm there too. */
 SFA_API sfa_status sfa_paged_forward_fp8(const sfa_params *p, const sfa_paged_fp8 *c, const void *Q, long long q_stride,
-                                         void *O, float *lse, unsigned int *status, cudaStream_t stream);
+                                         void *O, float *lse, void *workspace, size_t workspace_bytes,
+                                         unsigned int *status, cudaStream_t stream);
 
 /* ---- device status ----------------------------------------------------- */
 

@@ -81,6 +81,11 @@ class Cache8(Cache):
         return pages + [sc.view(self.num_pages, self.page // self.block, 2, HKV)]
 
 
+def expanded(cache):
+    """Whether a bf16 call on this cache runs on bf16 copies of its rows."""
+    return cache.dtype == "bf16" and cache.N >= 7000
+
+
 def half_bound(cache, W, plan):
     """What the tensor-core kernel's halves add to the bound of o, for each token
     row and query head: a probability times its value row's scale is rounded to a

@@ -59,9 +59,9 @@ def _append(lib, c, p=None, q=FAKE, qs=512, k=FAKE, ks=128, v=FAKE, vs=128, wq=F
                                     eps, tab, qh, NULL, NULL)
 
 
-def _fwd(lib, c, p=None, q=FAKE, qs=512, o=FAKE, lse=NULL, status=NULL):
+def _fwd(lib, c, p=None, q=FAKE, qs=512, o=FAKE, lse=NULL, ws=NULL, nbytes=0, status=NULL):
     return lib.sfa_paged_forward_fp8((p or _p(rope_theta=0.0)).ref(), ctypes.byref(c) if c is not None else None, q, qs, o, lse,
-                                     status, NULL)
+                                     ws, nbytes, status, NULL)
 
 
 @pytest.mark.parametrize("call", [_norm, _quantize, _bwd])
@@ -144,6 +144,23 @@ def test_append_and_forward_refusals(lib):
     assert _fwd(lib, c, p=_p(rope_theta=0.0, W=-1)) == BAD and _fwd(lib, c, p=_p(rope_theta=0.0, alpha=0.0)) == BAD
 
 
+def test_forward_workspace(lib):
+    def size(c, **kw):
+        return lib.sfa_paged_forward_fp8_workspace_size(_p(**{"T": 4096, "rope_theta": 0.0, **kw}).ref(), ctypes.byref(c))
+    long = _cache(N=8000, num_pages=1024, max_pages=256)
+    need = size(long)
+    # bf16 keys and values of the tokens and of what lies before two chunks, in pages of 16 rows
+    assert 2 * 8000 * 256 < need < 2 * (8000 + 2 * 1100) * 256 + (1 << 16)
+    assert size(_cache(N=6999, num_pages=1024, max_pages=256)) == 0
+    assert size(long, dtype=torch.float32) == 0 and size(long, W=29) == 0 and size(long, B=251) == 0 and size(long, B=0) == 0
+    assert size(long, rungs=(4000.0,), B=4) == 0                      # rows far back that few queries read
+    assert size(_cache(N=8000, num_pages=1024, max_pages=256, page_size=8, block=8)) == 0
+    assert size(_cache(N=8000, num_pages=0)) == 0 and lib.sfa_paged_forward_fp8_workspace_size(_p().ref(), None) == 0
+    p = _p(T=4096, rope_theta=0.0)
+    assert _fwd(lib, long, p=p) == BAD and _fwd(lib, long, p=p, ws=FAKE, nbytes=need - 1) == BAD
+    assert _fwd(lib, long, p=p, ws=FAKE + 128, nbytes=need) == BAD
+
+
 CHILD = r"""
 import json, sys
 sys.path.insert(0, "tests")
@@ -154,7 +171,8 @@ print(json.dumps([t._norm(lib), t._norm(lib, r=None, h=None), t._norm(lib, h=Non
                   t._quantize(lib), t._quantize(lib, xs=520), t._bwd(lib), t._bwd(lib, N=8, ws=None), t._bwd(lib, N=0, h=None),
                   t._bwd(lib, dh=t.FAKE), t._qkv(lib), t._qkv(lib, p=t._p(rope_theta=0.0), tab=None), t._qkv(lib, dm=16384),
                   t._append(lib, t._cache()), t._append(lib, t._cache(block=8), q=None, qh=None, wq=None, wk=None),
-                  t._fwd(lib, t._cache()), t._fwd(lib, t._cache(page_size=256, block=256))]))
+                  t._fwd(lib, t._cache()), t._fwd(lib, t._cache(page_size=256, block=256)),
+                  t._fwd(lib, t._cache(N=8000, num_pages=1024, max_pages=256), ws=t.FAKE, nbytes=1 << 30)]))
 print(json.dumps([t._norm(lib, x=None), t._append(lib, t._cache(scales=None)), t._fwd(lib, t._cache(N=0))]))
 """
 
@@ -164,7 +182,7 @@ def test_accepted_calls_reach_the_launch(lib):
     r = subprocess.run([sys.executable, "-c", CHILD], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
     got = [json.loads(x) for x in r.stdout.strip().splitlines()[-2:]]
-    assert got[0] == [_lib.SFA_ERR_CUDA] * 17 and got[1] == [BAD, BAD, OK]
+    assert got[0] == [_lib.SFA_ERR_CUDA] * 18 and got[1] == [BAD, BAD, OK]
 
 
 def test_binding_refuses_before_the_library(lib):

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from fibonacci_spaced_sparse_gb300 import api
-from _fp8 import FP8, NAN_CODE, Cache8, block_scale, codes, half_bound
+from _fp8 import FP8, NAN_CODE, Cache8, block_scale, codes, expanded, half_bound
 from _paged import D, DT, HALF_STEP, HKV, HQ, U, attention64, head64, rung_list, within
 
 pytestmark = pytest.mark.gpu
@@ -19,6 +19,8 @@ SINGLES = [(1, c) for c in (0, 1, 7, 8, 12, 13, 15, 16, 20, 21, 89, 144, 986, 98
 RAGGED = [(5, 0), (0, 33), (1, 21), (37, 95), (0, 0), (2, 1000), (130, 3), (1, 0)]
 CHUNK = [(503, 0)]
 LONG = [(1803, 70), (0, 9), (2402, 0), (1, 1200), (33, 986)]
+# enough tokens for bf16 copies of the rows (7000, and 32 a sequence)
+LONGER = [(3803, 70), (0, 9), (3302, 0), (1, 1200), (133, 986)]
 MANY = [(0, 5)] * 3 + [(1, 40 + s) for s in range(40)] + [(3, 0)] * 5 + [(0, 0)] * 2
 
 
@@ -34,10 +36,11 @@ def _forward(cache, pages=None, **kw):
 
 def _reference(cache, bad_rows=(), **kw):
     """attention64 and its bounds: those of fp32 arithmetic, and for bf16 what the
-    halves of the tensor-core kernels add (a probability's 2^-11 of the size of
-    the output's sum, which attention64 gives for bf16's 2^-8, and half_bound)."""
-    o, lse, bo, bl = attention64(cache, bad_rows=bad_rows, **kw)
-    if cache.dtype == "bf16":
+    halves of the tensor-core kernel add (a probability's 2^-11 of the size of the
+    output's sum, which attention64 gives for bf16's 2^-8, and half_bound), or bf16
+    probabilities over copied rows, which are exact with scales that are powers of two."""
+    o, lse, bo, bl = attention64(cache, bad_rows=bad_rows, tensor_cores=expanded(cache), **kw)
+    if cache.dtype == "bf16" and not expanded(cache):
         wide = attention64(cache, bad_rows=bad_rows, tensor_cores=True, **kw)[2]
         plan = rung_list(kw["alpha"], kw["W"], kw["rungs"], kw.get("round_offsets", False))
         bo = bo + (wide - bo) * 2.0 ** -3 + half_bound(cache, kw["W"], plan)
@@ -58,7 +61,8 @@ def _check(cache, got, ref, what=""):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("lens,page,block", [(ONE, 16, 16), (SINGLES, 16, 16), (SINGLES, 8, 8), (RAGGED, 64, 16), (CHUNK, 32, 8),
                                              (MANY, 16, 16), (MANY, 256, 64), (LONG, 16, 16), (LONG, 64, 32), (LONG, 8, 8),
-                                             (LONG, 2048, 2048)])
+                                             (LONG, 2048, 2048), (LONGER, 16, 8), (LONGER, 64, 16), (LONGER, 8, 8),
+                                             (LONGER, 1024, 128)])
 def test_forward_against_definition(lens, page, block, dtype):
     cache = Cache8(lens, page, dtype, block, seed=len(lens) + page)
     kw = dict(alpha=0.87, W=12, rungs=FIB)
@@ -80,17 +84,18 @@ def test_windows(W, dtype):
 
 @pytest.mark.parametrize("W", [0, 1, 7, 12, 13, 28, 29])
 def test_windows_of_long_chunks(W):
-    cache = Cache8([(4001, 37), (160, 0)], 32, "bf16", 16, seed=W)
-    kw = dict(alpha=0.71, W=W, rungs=FIB)
-    got = _forward(cache, **kw)
-    assert got[2] == 0
-    _check(cache, got, _reference(cache, **kw))
+    for lens in ([(4001, 37), (160, 0)], [(7001, 2037), (160, 0)]):
+        cache = Cache8(lens, 32, "bf16", 16, seed=W)
+        kw = dict(alpha=0.71, W=W, rungs=FIB)
+        got = _forward(cache, **kw)
+        assert got[2] == 0
+        _check(cache, got, _reference(cache, **kw))
 
 
 @pytest.mark.parametrize("alpha,rungs,rounded", [(1.0, FIB, False), (1.5, api.pow2_base(2048), False), (0.77, FIB, True),
                                                  (1.0, (), False), (1.3, (40.5,), False), (1.0, (30.0, 30.0, 14.25), False),
                                                  (1.1, tuple(13.0 + 0.4 * k for k in range(32)), False)])
-@pytest.mark.parametrize("lens", [[(70, 60), (1, 1500), (9, 1490)], [(470, 600), (31, 1490)], [(4100, 500)]])
+@pytest.mark.parametrize("lens", [[(70, 60), (1, 1500), (9, 1490)], [(470, 600), (31, 1490)], [(4100, 500)], [(7100, 4000)]])
 def test_rung_lists(lens, alpha, rungs, rounded):
     for dtype in ("bf16", "f32") if lens[0][0] < 4000 else ("bf16",):
         cache = Cache8(lens, 32, dtype, 16, seed=3)
@@ -126,7 +131,7 @@ def test_scales_that_differ_widely(lens, dtype):
 def test_scales_far_from_one(power, dtype):
     """Values' scales at the ends of what a float holds: the output scales with
     them exactly (powers of two), lse stays."""
-    for lens in ([(20, 70), (1, 90)], [(700, 30)], [(4100, 30)]):
+    for lens in ([(20, 70), (1, 90)], [(700, 30)], [(4100, 30)], [(7100, 30)]):
         cache = Cache8(lens, 16, dtype, 16, seed=6)
         kp, vp, sc = cache.pages8()
         kw = dict(alpha=0.9, W=12, rungs=FIB)
@@ -144,7 +149,8 @@ def test_scales_far_from_one(power, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lens", [[(400, 200)], [(1, 300 + 7 * s) for s in range(20)], [(900, 0), (1, 500)], [(4200, 150)]])
+@pytest.mark.parametrize("lens", [[(400, 200)], [(1, 300 + 7 * s) for s in range(20)], [(900, 0), (1, 500)], [(4200, 150)],
+                                  [(7200, 3150), (33, 8)]])
 def test_bad_values_reach_only_the_queries_that_read_them(lens, dtype):
     """A NaN key element, a NaN value element and a block whose values' scale is NaN:
     the queries that read them get what the formula gives, the others what they
@@ -174,13 +180,18 @@ def test_bad_values_reach_only_the_queries_that_read_them(lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("lens", [[(30, 70), (1, 90)], [(1, 99), (1, 40)], [(640, 60), (3, 5)], [(4200, 60), (3, 5)]])
-def test_bad_pages_are_left_out_and_reported(lens, dtype):
-    cache = Cache8(lens, 8, dtype, 8, seed=15)
+@pytest.mark.parametrize("lens,page", [([(30, 70), (1, 90)], 8), ([(1, 99), (1, 40)], 8), ([(640, 60), (3, 5)], 8),
+                                       ([(4200, 60), (3, 5)], 8), ([(7200, 60), (3, 5)], 16), ([(7200, 5060), (30, 5)], 128)])
+def test_bad_pages_are_left_out_and_reported(lens, page, dtype):
+    if dtype == "f32" and lens[0][0] > 5000:
+        pytest.skip("the copied rows are bf16's")
+    cache = Cache8(lens, page, dtype, 8, seed=15)
     length = lens[0][0] + lens[0][1]
-    mid, last = length // 16, (length - 1) // 8
+    mid, last = length // (2 * page), (length - 1) // page
+    if lens[0][1] > 5000:
+        mid = (lens[0][1] + 3000) // page
     cache.table[0, mid], cache.table[0, last] = cache.num_pages, -7
-    bad = [(0, i) for i in range(length) if i // 8 in (mid, last)]
+    bad = [(0, i) for i in range(length) if i // page in (mid, last)]
     kw = dict(alpha=0.87, W=4, rungs=FIB)
     got = _forward(cache, **kw)
     assert got[2] == 0x2
@@ -188,8 +199,10 @@ def test_bad_pages_are_left_out_and_reported(lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("more", [0, 700, 4200])
+@pytest.mark.parametrize("more", [0, 700, 4200, 7200])
 def test_bad_positions_give_zeros(dtype, more):
+    if dtype == "f32" and more > 5000:
+        pytest.skip("the copied rows are bf16's")
     cache = Cache8([(4, 0), (20 + more, 10), (3, 60)], 16, dtype, 16, seed=18)
     cap = cache.max_pages * 16
     seq = torch.tensor([2, 30 + more, cap + 2], dtype=torch.int32).cuda()
@@ -205,7 +218,44 @@ def test_bad_positions_give_zeros(dtype, more):
     within(lse[4:end], ref[1][4:end], ref[3][4:end])
 
 
-@pytest.mark.parametrize("lens", [SINGLES, RAGGED, LONG])
+def test_copied_rows_of_sequences_far_into_a_wide_table():
+    """Chunks that start far behind the first position, in a table so wide that the
+    copies' own is narrower, beside a sequence whose length passes its capacity: two
+    tokens at the last positions, which have no pages, and one behind them."""
+    page = 16
+    cache = Cache8([(7000, 20000), (500, 11000), (3, 0)], page, "bf16", 16, seed=8)
+    wide = torch.full((3, 2100), -1, dtype=torch.int32)
+    wide[:, :cache.max_pages] = cache.table
+    cap = 2100 * page
+    seq = cache.seq.clone()
+    seq[2] = cap + 1
+    kw = dict(alpha=0.9, W=12, rungs=FIB)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = api.sfa_paged_forward_fp8(cache.q.cuda(), *cache.pages8(), wide.cuda(), cache.meta()[1], seq.cuda(), status=status, **kw)
+    assert api.sfa_read_status(status) == 0x2
+    ref = _reference(cache, **kw)
+    within(o[:7500], ref[0][:7500], ref[2][:7500])
+    within(lse[:7500], ref[1][:7500], ref[3][:7500])
+    assert bool((o[7500:7503] == 0).all()) and bool(torch.isneginf(lse[7500:7502]).all()) and bool((lse[7502] == 0).all())
+
+
+def test_copied_rows_with_other_scales():
+    """Scales that are no powers of two: a copied element is off by 2^-8 of itself, so a
+    score by 2^-8 scale |q| |k| and 2^-8 of the output's sum more."""
+    cache = Cache8([(7200, 30)], 16, "bf16", 8, seed=5, powers=False)
+    kw = dict(alpha=0.93, W=12, rungs=FIB)
+    got = _forward(cache, **kw)
+    ref = _reference(cache, **kw)
+    used = int(cache.cu[-1])
+    q = cache.q[:used].double().norm(dim=-1)
+    k = cache.k[0].double().norm(dim=-1).amax(0).repeat_interleave(HQ // HKV)
+    delta = 2.0 ** -8 * 0.125 * q * k                                         # [tokens, heads]
+    size = (torch.from_numpy(ref[2][:used]) - 2.0 ** -8 * torch.from_numpy(ref[0][:used]).abs()) * 2.0 ** 8   # sum p |v| at least
+    within(got[0][:used], ref[0][:used], torch.from_numpy(ref[2][:used]) + (2 * delta[..., None] + 2.0 ** -8) * size)
+    within(got[1][:used], ref[1][:used], torch.from_numpy(ref[3][:used]) + delta)
+
+
+@pytest.mark.parametrize("lens", [SINGLES, RAGGED, LONG, LONGER])
 def test_packed_queries_other_stream_and_no_lse(lens):
     cache = Cache8(lens, 16, "bf16", 16, seed=41)
     wide = torch.randn((cache.N, 12 * D)).to(torch.bfloat16).cuda()
@@ -226,12 +276,13 @@ def test_packed_queries_other_stream_and_no_lse(lens):
 def test_cache_rows_past_32_bits(dtype):
     """Pages whose bytes lie past 2^32."""
     rows = (1 << 25) + (1 << 20)          # 128 bytes a row
-    cache = Cache8([(70, 30), (1, 500), (600 if dtype == "f32" else 4100, 0)], 64, dtype, 16, seed=5, num_pages=rows // 64)
-    assert int(cache.table[0, 0]) * 64 * HKV * D > 1 << 32
-    kw = dict(alpha=0.87, W=12, rungs=FIB)
-    got = _forward(cache, **kw)
-    assert got[2] == 0
-    _check(cache, got, _reference(cache, **kw))
+    for n in (600,) if dtype == "f32" else (4100, 7100):
+        cache = Cache8([(70, 30), (1, 500), (n, 0)], 64, dtype, 16, seed=5, num_pages=rows // 64)
+        assert int(cache.table[0, 0]) * 64 * HKV * D > 1 << 32
+        kw = dict(alpha=0.87, W=12, rungs=FIB)
+        got = _forward(cache, **kw)
+        assert got[2] == 0
+        _check(cache, got, _reference(cache, **kw))
 
 
 # -------------------------------------------------------------------- append
@@ -500,7 +551,7 @@ def test_append_twice_changes_nothing():
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
-@pytest.mark.parametrize("pad_to", [64, 900, 4200])
+@pytest.mark.parametrize("pad_to", [64, 900, 4200, 8000])
 def test_captured_step_replayed_with_other_lengths(pad_to):
     """One captured step (append, then attention) of a fixed number of token rows,
     replayed with other lengths, tables and inputs, equals the calls alone."""
