@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_kernel(const AddNorm
 // ------------------------------------------------------------------ backward
 
 // Blocks of the backward pass a SM, as many as are resident (48 registers with eight
-// bf16 values a lane, 57 fp32 ones, 80 and 94 with sixteen): each writes one partial sum
+// bf16 values a lane, 58 fp32 ones, 80 and 122 with sixteen): each writes one partial sum
 // of dw (us, with one block a SM less and with one more: 32 x 1024 tokens of 512 30.1,
 // 24.4, of 256 15.6, 14.1).  Two rows a warp on their way together, at 112 registers and
 // two blocks, are no faster (24.9).
@@ -194,9 +194,14 @@ template <typename T, int kV>
 constexpr int kBwdEach = kV == 1 ? (sizeof(T) == 2 ? 5 : 4) : (sizeof(T) == 2 ? 3 : 2);
 constexpr int kBwdBlocks = kSms * 5;  // at most
 
+// Blocks up to which the weights are held in registers, two blocks a SM; above that they
+// are read again (from L1) in every row, which leaves room for a third (us, held and read:
+// 2000 bf16 tokens of 512 4.2 and 5.2, 32 x 1024 29.6 and 24.6).
+constexpr int kHeldBlocks = kSms * 2;
+
 // Block b writes dx of its rows (b, b + gridDim, ... in groups of kRows) and its
 // part of dw to partial[b]; the launch after it sums the parts in a fixed order.
-template <typename T, int kV, int kW>
+template <typename T, int kV, int kW, bool kHeld>
 __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const AddNormBwdArgs a, float* partial) {
     constexpr int kGroups = kRows<kW>, kWide = 256 * kV * kW;  // columns held
     __shared__ float sums[2][2][kGroups][kW];
@@ -204,9 +209,22 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const Add
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int group = threadIdx.x / (32 * kW), i = threadIdx.x % (32 * kW);
-    Eight dw[kV];
+    Eight dw[kV], wt[kV];
 #pragma unroll
-    for (int j = 0; j < kV; ++j) dw[j] = Eight{};
+    for (int j = 0; j < kV; ++j) {
+        const int e = 8 * (j * 32 * kW + i);
+        Piece<float> w{};
+        if (kHeld && e < a.dim) fetch(a.w + e, w);
+        wt[j] = open(w);
+        dw[j] = Eight{};
+    }
+    auto weight = [&](int j) {
+        if (kHeld) return wt[j];
+        const int e = 8 * (j * 32 * kW + i);
+        Piece<float> w{};
+        if (e < a.dim) fetch(a.w + e, w);
+        return open(w);
+    };
     int turn = 0;
     for (long long row0 = (long long)blockIdx.x * kGroups; row0 < a.N; row0 += (long long)gridDim.x * kGroups, turn ^= 1) {
         const bool live = row0 + group < a.N;
@@ -225,10 +243,7 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const Add
         float2 square = both(0.f), cross = both(0.f);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-            const int e = 8 * (j * 32 * kW + i);
-            Piece<float> w{};
-            if (e < a.dim) fetch(a.w + e, w);
-            const Eight h = open(ph[j]), g = open(pg[j]), ww = open(w);
+            const Eight h = open(ph[j]), g = open(pg[j]), ww = weight(j);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 square = __ffma2_rn(h.f[k], h.f[k], square);
@@ -256,9 +271,7 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const Add
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int e = 8 * (j * 32 * kW + i);
-            Piece<float> w{};
-            if (e < a.dim) fetch(a.w + e, w);
-            const Eight h = open(ph[j]), g = open(pg[j]), ww = open(w);
+            const Eight h = open(ph[j]), g = open(pg[j]), ww = weight(j);
             Eight d = open(pd[j]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -363,7 +376,11 @@ cudaError_t launch_bwd(const AddNormBwdArgs& a, float* ws, cudaStream_t s) {
     const int blocks = bwd_blocks<T>(a.N, a.dim);
     float* partial = blocks > 1 ? ws : a.dw;
     const cudaError_t e = by_width(a.dim, [&](auto v, auto w) {
-        return launch_early(add_norm_bwd_kernel<T, v(), w()>, (unsigned)blocks, kRowThreads<w()>, 0, s, a, partial);
+        auto* kernel = add_norm_bwd_kernel<T, v(), w(), true>;
+        if constexpr (kSms * kBwdEach<T, (v() > 1 ? 2 : 1)> > kHeldBlocks) {
+            if (blocks > kHeldBlocks) kernel = add_norm_bwd_kernel<T, v(), w(), false>;
+        }
+        return launch_early(kernel, (unsigned)blocks, kRowThreads<w()>, 0, s, a, partial);
     });
     if (e != cudaSuccess || blocks == 1) return e;
     return launch_early(add_norm_dw_kernel, (unsigned)(a.dim / kFinCols), (unsigned)(kFinCols * kFinRows), 0, s,
