@@ -194,7 +194,7 @@ constexpr int kMaxDim = 1 << 14;  // columns of a row
 sfa_status check_rows(sfa_dtype dtype, int N, int dim) {
     if (dtype != SFA_BF16 && dtype != SFA_F32) return SFA_ERR_INVALID_ARG;
     if (N < 0 || dim < 1) return SFA_ERR_INVALID_ARG;
-    return dim % 8 || dim > kMaxDim ? SFA_ERR_UNSUPPORTED : SFA_OK;
+    return N > kMaxRows || dim % 8 || dim > kMaxDim ? SFA_ERR_UNSUPPORTED : SFA_OK;
 }
 bool strided_ok(sfa_dtype dtype, int dim, const void* x, long long stride) {
     const int es = dtype == SFA_BF16 ? 2 : 4;

@@ -298,7 +298,7 @@ SFA_API sfa_status sfa_qkv_rope(const sfa_params *p, int d_model, const void *X,
  * in fp32.  y is rounded once to the rows' type, or given in 8 bits with a scale
  * a row, s[t] = max(max |y[t]| / 448, 2^-126).
  *   dtype: of X, R, H and Y;
- *   N >= 0 (0: nothing to do); dim: a multiple of 8, 8 .. 16384, else
+ *   N: 0 (nothing to do) .. 2^28; dim: a multiple of 8, 8 .. 16384; else
  *     SFA_ERR_UNSUPPORTED;
  *   X, R [N][dim], row t x_stride (r_stride) elements after the row before it: a
  *     multiple of 16 bytes, at least dim; R may be NULL (h = x);

@@ -68,7 +68,7 @@ def _fwd(lib, c, p=None, q=FAKE, qs=512, o=FAKE, lse=NULL, ws=NULL, nbytes=0, st
 def test_row_shapes(lib, call):
     for bad in (dict(dt=2), dict(dt=-1), dict(N=-1), dict(dim=0), dict(dim=-8)):
         assert call(lib, **bad) == BAD, bad
-    for bad in (dict(dim=4), dict(dim=500), dict(dim=16392), dict(dim=1 << 20)):
+    for bad in (dict(dim=4), dict(dim=500), dict(dim=16392), dict(dim=1 << 20), dict(N=(1 << 28) + 1), dict(N=(1 << 31) - 1, dim=8)):
         assert call(lib, **bad) == UNSUP, bad
     if call is not _bwd:
         assert call(lib, N=0, x=NULL) == OK
