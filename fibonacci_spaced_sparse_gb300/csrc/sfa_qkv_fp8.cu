@@ -12,16 +12,16 @@
 //                      row) into an mbarrier ring;
 //   warp 1:            one lane issues tcgen05.mma (kind::f8f6f4, M = 128, K = 32)
 //                      into one of two accumulators in tensor memory;
-//   the other warps:   the epilogue, four warps a tile, 32 tokens each; two sets of
-//                      four take the tiles in turn, so that one has its tokens'
-//                      (cos, sin) rows by the time its accumulator is done (a set of
-//                      12 warps, one a head, waits for them in every tile: 21.1 us
-//                      for 32 x 1024 tokens).  The accumulator is read as fragments
-//                      (16 rows x 8 columns a quad of lanes at a time) rather than a
-//                      row a lane: a warp then reads the rotation's table in 64-byte
-//                      pieces of eight rows, where a row a lane costs a cache line a
-//                      lane and load (32.7 us), and stmatrix puts the rounded rows
-//                      where a TMA store takes them from.
+//   the other warps:   the epilogue.  A warp takes 16 tokens, eight warps 128; but for
+//                      kSmall there are two such sets, which take the tiles in turn
+//                      (kTall: a half of the tile each), so that one has its tokens'
+//                      (cos, sin) rows by the time its accumulator is done.  The
+//                      accumulator is read as fragments (16 rows x 8 columns a quad of
+//                      lanes at a time) rather than a row a lane: a warp then reads the
+//                      rotation's table in 64-byte pieces of eight rows, where a row a
+//                      lane costs a cache line a lane and load (32 x 1024 tokens at
+//                      d_model 512: 32.7 us that way, 18.0 us as it is), and stmatrix
+//                      puts the rounded rows where a TMA store takes them from.
 // What an SM fetches is the limit before the tensor cores are: a tile of 128 x 192
 // takes 40 KB a k-block, 100 bytes a clock at the rate of the products, and an SM was
 // seen to take 58.  Where a CTA's 192 rows of W8 fit beside the ring (kResident:

@@ -73,6 +73,21 @@ def test_model_shape_sampled():
     assert all(torch.equal(x, y) for x, y in zip(again, out))
 
 
+@pytest.mark.parametrize("B,T,dm", [(1, 5000, 1472), (4, 5000, 4096), (1, 5000, 640), (3, 2731, 2048), (1, 8157, 4096)])
+@pytest.mark.parametrize("theta", [1e4, 0.0])
+def test_weights_through_the_ring_sampled(B, T, dm, theta):
+    """Wide rows, whose weights do not stay in shared memory: tiles of 128 and of 256
+    tokens, one and several of them a block, the last one ragged."""
+    a = _draw(B, T, dm)
+    rows = sorted({0, 127, 128, 255, 256, T - 1, B * T - 1} | set(np.random.default_rng(1).integers(0, B * T, 150).tolist()))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = api.sfa_qkv_rope_fp8(*a, rope_theta=theta, status=status)
+    assert api.sfa_read_status(status) == 0
+    _check(out, *a, theta, rows=rows)
+    again = api.sfa_qkv_rope_fp8(*a, rope_theta=theta)
+    assert all(torch.equal(x, y) for x, y in zip(again, out))
+
+
 @pytest.mark.parametrize("M", [3, 2000])
 def test_values_that_are_not_finite_stay_in_their_row(M):
     a = _draw(1, M, 512)
