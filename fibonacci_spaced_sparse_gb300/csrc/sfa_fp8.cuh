@@ -48,7 +48,6 @@ __device__ __forceinline__ float2 values2(uint32_t two) {
 constexpr float kLeastRow = 1.17549435e-38f;  // 2^-126
 __device__ __forceinline__ float row_scale(float amax) { return fmaxf(amax * (1.f / kTop), kLeastRow); }
 
-
 // Scale of a block of cached rows: the smallest power of two s >= 2^-100 with
 // amax <= 448 s (448 = 1.75 * 2^8).  A power of two, so that rows that are
 // already there move to a larger one without a rounding, but for what then lies

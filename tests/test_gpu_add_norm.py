@@ -296,6 +296,33 @@ def test_captured_steps_in_a_row(N, dim, dtype):
         assert all(torch.equal(a.view(torch.uint8), b) for a, b in zip((h, y, y8, s, dx, dw), want[i]))
 
 
+def test_one_tensor_as_both_addends():
+    """x beside itself: h = 2 x (exact), and the leaf gets the gradient twice."""
+    x, w = _rows(37, 320, "f32").cuda().requires_grad_(), _weight(320).cuda()
+    a, b = _rows(37, 320, "f32", 2).cuda(), _rows(37, 320, "f32", 3).cuda()
+    h, y = api.AddRMSNorm.apply(x, x, w)
+    assert torch.equal(h, 2 * x)
+    ((h * a).sum() + (y * b).sum()).backward()
+    dx, _ = api.sfa_add_rms_norm_backward(h.detach(), w, b, a)
+    assert torch.equal(x.grad, 2 * dx)
+
+
+def test_calls_at_once():
+    """Backward passes on two streams, each with a scratch of its own."""
+    w = _weight(512).cuda()
+    args = [(_rows(30000, 512, "bf16", i).cuda(), w, _rows(30000, 512, "bf16", 5 + i).cuda()) for i in range(2)]
+    want = [api.sfa_add_rms_norm_backward(*a) for a in args]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in args]
+    got = [[] for _ in args]
+    for _ in range(5):
+        for i, a in enumerate(args):
+            got[i].append(api.sfa_add_rms_norm_backward(*a, stream=sides[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y) for g in got[i] for x, y in zip(g, want[i]))
+
+
 def test_other_stream():
     x, r, w = _rows(3000, 512, "bf16").cuda(), _rows(3000, 512, "bf16", 1).cuda(), _weight(512).cuda()
     want = api.sfa_add_rms_norm(x, r, w, fp8=True)

@@ -255,6 +255,27 @@ def test_copied_rows_with_other_scales():
     within(got[1][:used], ref[1][:used], torch.from_numpy(ref[3][:used]) + delta)
 
 
+@pytest.mark.parametrize("n,before", [(1, 1300), (300, 200), (1800, 900), (4001, 1000)])
+def test_pages_of_two_sequences(n, before):
+    """Two sequences that read the same pages (a prefix that they share), against the
+    same calls with a copy of the pages each; and both calls at once, on two streams."""
+    cache = Cache8([(n, before)], 16, "bf16", 16, seed=n)
+    pages, table = cache.pages8(), cache.table.cuda()
+    q = torch.randn((2 * n, HQ, D), generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).cuda()
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    seq = torch.full((2,), n + before, dtype=torch.int32, device="cuda")
+    kw = dict(alpha=0.87, W=12, rungs=FIB)
+    twice = [torch.cat((x.view(torch.uint8), x.view(torch.uint8))).view(x.dtype) for x in pages]
+    calls = [(*twice, torch.cat((table, table + cache.num_pages))), (*pages, torch.cat((table, table)))]
+    want = [api.sfa_paged_forward_fp8(q, *c, cu, seq, **kw) for c in calls]
+    assert all(torch.equal(x, y) for x, y in zip(*want))
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in calls]
+    got = [api.sfa_paged_forward_fp8(q, *c, cu, seq, stream=s, **kw) for _ in range(4) for c, s in zip(calls, sides)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for g in got for x, y in zip(g, want[0]))
+
+
 @pytest.mark.parametrize("lens", [SINGLES, RAGGED, LONG, LONGER])
 def test_packed_queries_other_stream_and_no_lse(lens):
     cache = Cache8(lens, 16, "bf16", 16, seed=41)
