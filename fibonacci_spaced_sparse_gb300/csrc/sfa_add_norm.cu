@@ -10,10 +10,12 @@
 // the backward pass three in and one out, with some ten operations a value.  A
 // row is held in registers by kW warps, kV pieces of eight values a lane, so it
 // is read once whatever is computed from it; sums over it are a warp's shuffles,
-// and one exchange through shared memory where several warps hold it.
+// and one exchange through shared memory where several warps hold it.  32 x 1024 bf16
+// tokens of 512: forward 21.3 us, backward 23.1 (93 and 86 % of the copy rate).
 #include <type_traits>
 
 #include "sfa_fp8.cuh"
+#include "sfa_heads.cuh"
 #include "sfa_ops.cuh"
 
 namespace sfa {
@@ -185,25 +187,42 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_kernel(const AddNorm
 
 // ------------------------------------------------------------------ backward
 
-// Blocks of the backward pass a SM, as many as are resident (48 registers with eight
-// bf16 values a lane, 58 fp32 ones, 80 and 122 with sixteen): each writes one partial sum
-// of dw (us, with one block a SM less and with one more: 32 x 1024 tokens of 512 30.1,
-// 24.4, of 256 15.6, 14.1).  Two rows a warp on their way together, at 112 registers and
-// two blocks, are no faster (24.9).
+// Forms of the backward pass.
+//   kHeld: the weights in registers;
+//   kRead: the weights read again (from L1) twice in every row, which leaves registers
+//          for more blocks or for a wider row;
+//   kAhead: the weights in registers, and while a row is computed the next one is on its
+//           way to shared memory, each lane's own pieces (no barrier, no registers).
+enum class Form { kHeld, kRead, kAhead };
+
+// The form of long calls, by the pieces of a row that a lane has (times in us).
+//   One: kRead, which fits five blocks a SM (32 x 1024 bf16 tokens of 256: 14.1, ahead 17.3).
+//   Two, bf16: kAhead (held, read and ahead: 32 x 1024 of 512 29.6, 24.6 and 23.1; read and
+//     ahead: 5000 of 512 6.9 and 5.3, 4096 of 4096 26.8 and 24.4; a third and a fourth row on
+//     their way, 32 x 1024 of 512: 23.9 and 24.4).  fp32: kHeld (4083 of 320 6.2, ahead 8.9).
+//   Four: kRead, the only one without many spills (1024 bf16 of 16384 38.4, ahead 48.8).
 template <typename T, int kV>
-constexpr int kBwdEach = kV == 1 ? (sizeof(T) == 2 ? 5 : 4) : (sizeof(T) == 2 ? 3 : 2);
+constexpr Form kLong = kV != 2 ? Form::kRead : sizeof(T) == 2 ? Form::kAhead : Form::kHeld;
+
+// Blocks a SM in the split that by_width chooses, as many as are resident: each writes one
+// partial sum of dw (us, with one less or more: 32 x 1024 bf16 tokens of 256 15.6 with four,
+// 14.1 with five; 2048 of 8192 26.3 with one, 28.0 with two).
+template <typename T>
+int bwd_each(int dim) {
+    return dim > 4096 ? 1 : dim > 256 ? 2 : sizeof(T) == 2 ? 5 : 4;
+}
 constexpr int kBwdBlocks = kSms * 5;  // at most
 
-// Blocks up to which the weights are held in registers, two blocks a SM; above that they
-// are read again (from L1) in every row, which leaves room for a third (us, held and read:
-// 2000 bf16 tokens of 512 4.2 and 5.2, 32 x 1024 29.6 and 24.6).
+// One piece a lane: blocks up to which the weights are held, two a SM.
 constexpr int kHeldBlocks = kSms * 2;
 
 // Block b writes dx of its rows (b, b + gridDim, ... in groups of kRows) and its
 // part of dw to partial[b]; the launch after it sums the parts in a fixed order.
-template <typename T, int kV, int kW, bool kHeld>
+template <typename T, int kV, int kW, Form kForm>
 __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const AddNormBwdArgs a, float* partial) {
     constexpr int kGroups = kRows<kW>, kWide = 256 * kV * kW;  // columns held
+    constexpr bool kHeld = kForm != Form::kRead, kAhead = kForm == Form::kAhead;
+    extern __shared__ uint4 ahead[];  // kAhead: [2 rows][h, dy, dh][kV][threads]
     __shared__ float sums[2][2][kGroups][kW];
     __shared__ float part[kGroups > 1 ? kGroups : 1][kGroups > 1 ? kWide : 1];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -225,16 +244,40 @@ __global__ void __launch_bounds__(kRowThreads<kW>) add_norm_bwd_kernel(const Add
         if (e < a.dim) fetch(a.w + e, w);
         return open(w);
     };
+    // the pieces of the warp's row of h, dy and dh: to shared memory, and back
+    auto slot = [&](int t, int which, int j) { return ahead + ((t * 3 + which) * kV + j) * kRowThreads<kW> + threadIdx.x; };
+    auto send = [&](long long row0, int t) {
+        const long long at = (row0 + group < a.N ? row0 + group : a.N - 1) * a.dim;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const int e = 8 * (j * 32 * kW + i);
+            if (row0 >= a.N || e >= a.dim) continue;
+            heads::copy16(slot(t, 0, j), static_cast<const T*>(a.h) + at + e);
+            heads::copy16(slot(t, 1, j), static_cast<const T*>(a.dy) + at + e);
+            if (a.dh) heads::copy16(slot(t, 2, j), static_cast<const T*>(a.dh) + at + e);
+        }
+        heads::copies_end();
+    };
+    if constexpr (kAhead) send((long long)blockIdx.x * kGroups, 0);
     int turn = 0;
     for (long long row0 = (long long)blockIdx.x * kGroups; row0 < a.N; row0 += (long long)gridDim.x * kGroups, turn ^= 1) {
         const bool live = row0 + group < a.N;
         const long long at = (live ? row0 + group : a.N - 1) * a.dim;  // idle warps repeat the last row; it counts once
         Piece<T> ph[kV], pg[kV], pd[kV];
+        if constexpr (kAhead) {
+            send(row0 + (long long)gridDim.x * kGroups, turn ^ 1);
+            heads::copies_wait<1>();
+        }
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int e = 8 * (j * 32 * kW + i);
             ph[j] = pg[j] = pd[j] = Piece<T>{};
-            if (e < a.dim) {
+            if constexpr (kAhead) {
+                if (e >= a.dim) continue;
+                ph[j].u = *slot(turn, 0, j);
+                pg[j].u = *slot(turn, 1, j);
+                if (a.dh) pd[j].u = *slot(turn, 2, j);
+            } else if (e < a.dim) {
                 fetch(static_cast<const T*>(a.h) + at + e, ph[j]);
                 fetch(static_cast<const T*>(a.dy) + at + e, pg[j]);
                 if (a.dh) fetch(static_cast<const T*>(a.dh) + at + e, pd[j]);
@@ -367,7 +410,7 @@ cudaError_t launch_rows(const AddNormArgs& a, cudaStream_t s) {
 template <typename T>
 int bwd_blocks(int N, int dim) {
     const int warps = dim <= 512 ? 1 : dim <= 1024 ? 2 : dim <= 2048 ? 4 : 8, rows = 8 / warps;
-    const int steps = (N + rows - 1) / rows, most = kSms * (dim <= 256 ? kBwdEach<T, 1> : kBwdEach<T, 2>);
+    const int steps = (N + rows - 1) / rows, most = kSms * bwd_each<T>(dim);
     return steps < most ? steps : most;
 }
 
@@ -376,11 +419,27 @@ cudaError_t launch_bwd(const AddNormBwdArgs& a, float* ws, cudaStream_t s) {
     const int blocks = bwd_blocks<T>(a.N, a.dim);
     float* partial = blocks > 1 ? ws : a.dw;
     const cudaError_t e = by_width(a.dim, [&](auto v, auto w) {
-        auto* kernel = add_norm_bwd_kernel<T, v(), w(), true>;
-        if constexpr (kSms * kBwdEach<T, (v() > 1 ? 2 : 1)> > kHeldBlocks) {
-            if (blocks > kHeldBlocks) kernel = add_norm_bwd_kernel<T, v(), w(), false>;
+        constexpr int kR = kRows<w()>;
+        constexpr Form kMany = kLong<T, v()>, kFew = v() == 4 ? kMany : Form::kHeld;
+        const bool many = kMany == Form::kAhead ? (a.N + kR - 1) / kR > blocks : blocks > kHeldBlocks;
+        auto* kernel = add_norm_bwd_kernel<T, v(), w(), kFew>;
+        size_t smem = 0;
+        if (many && kMany != kFew) {
+            kernel = add_norm_bwd_kernel<T, v(), w(), kMany>;
+            if (kMany == Form::kAhead) {
+                smem = (size_t)2 * 3 * v() * kRowThreads<w()> * sizeof(uint4);
+                int dev = 0;
+                cudaError_t e = cudaGetDevice(&dev);
+                if (e != cudaSuccess) return e;
+                static CtxSetting configured[64];
+                if (!ctx_setting_holds(configured[dev & 63], smem)) {
+                    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                    if (e != cudaSuccess) return e;
+                    ctx_setting_done(configured[dev & 63], smem);
+                }
+            }
         }
-        return launch_early(kernel, (unsigned)blocks, kRowThreads<w()>, 0, s, a, partial);
+        return launch_early(kernel, (unsigned)blocks, kRowThreads<w()>, smem, s, a, partial);
     });
     if (e != cudaSuccess || blocks == 1) return e;
     return launch_early(add_norm_dw_kernel, (unsigned)(a.dim / kFinCols), (unsigned)(kFinCols * kFinRows), 0, s,
