@@ -140,7 +140,8 @@ struct PagedFwd {
 
 }  // namespace paged
 
-// The kernel for long chunks (sfa_paged_tile.cu).
-cudaError_t launch_paged_tiles(const paged::PagedFwd& P, cudaStream_t s);
+// The kernel for long chunks (sfa_paged_tile.cu).  copied: the pages are copies of 8-bit
+// rows.
+cudaError_t launch_paged_tiles(const paged::PagedFwd& P, bool copied, cudaStream_t s);
 
 }  // namespace sfa

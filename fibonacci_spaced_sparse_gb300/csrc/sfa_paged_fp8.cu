@@ -6,7 +6,9 @@
 // tiles, and turning it from 8 bits costs more than the bytes it saves once it is in
 // L2.  So the rows that the chunks can reach are turned into bf16 once, into pages of
 // their own in the caller's workspace, and the kernel for long chunks of bf16 pages
-// runs on those (32 x 1024 tokens: 53.1 us for quads on 8-bit rows).
+// runs on those (32 x 1024 tokens: 39.8 us, and 53.1 for quads on 8-bit rows), with its
+// probabilities in two parts (PairSplit; rounded to bf16 once, as over bf16 pages, 37.1 us and
+// an error of O of 2.0e-3 of its norm instead of 1.7e-3).
 // Sequence s reaches from position c - back on, c its rows before the step and back the
 // farthest row of a key list.  Its pages start at place (cu[s] >> shift) + s * extra of
 // the workspace, and at position 64 h of the sequence: all positions move by that, which
@@ -75,10 +77,9 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
 }
 
 constexpr int kQuadsFrom = 305, kTilesEach = 32;  // as in sfa_paged_fwd.cu
-// Tokens from which rows are expanded (us, quads and expanded: one chunk of 4800 10.0
-// and 14.1, of 6000 14.4 and 14.4, of 8000 16.4 and 14.5, of 12000 24.1 and 22.6; 16
-// chunks of 512 behind 2000 rows 17.0 and 15.7; 32 x 1024 in pages of 64 rows 52.9 and
-// 37.1, of 16 53.7 and 41.0).
+// Tokens from which rows are expanded (us, quads and expanded: one chunk of 8000 16.4 and
+// 15.4, of 12000 24.1 and 24.1; 16 chunks of 512 behind 2000 rows 17.0 and 16.1; 32 x 1024
+// in pages of 64 rows 52.9 and 39.8, of 16 53.7 and 42.6).
 constexpr int kExpandFrom = 7000;
 
 // Whether a call's rows are expanded, and how.
@@ -130,7 +131,7 @@ cudaError_t launch_paged_fwd_fp8(const LayerArgs& a, const PagedArgs& c, sfa_dty
         B.c.num_pages = E.places;
         B.c.shift = E.shift;
         B.c.cap = E.cap;
-        return launch_paged_tiles(B, s);
+        return launch_paged_tiles(B, true, s);
     }
     if (dt == SFA_BF16 && a.W <= 28 && c.N >= kQuadsFrom && c.N >= 2 * (long long)c.S) return launch_quads<RowsFp8>(P, s);
     return dt == SFA_BF16 ? launch_rows<__nv_bfloat16, __nv_fp8_e4m3>(P, s) : launch_rows<float, __nv_fp8_e4m3>(P, s);

@@ -59,6 +59,11 @@
 // p s stays in range (what is 2^-14 of the largest or less is off by up to 2^-25
 // of it).  The sum for lse takes p alone.  (Turning 8 bits into bf16 instead takes
 // nine operations for four values where halves take two.)
+//
+// Long chunks of 8-bit rows are attended over exact bf16 copies (PairSplit).  There
+// a probability is the sum of two bf16 parts, p = hi + lo with lo = p - hi rounded,
+// which leaves 2^-16 of it, and the value product is made of both: 4 more MMAs a
+// tile and pair, so that a long chunk is no less exact than a short one.
 #pragma once
 
 #include "sfa_fp8.cuh"
@@ -89,6 +94,13 @@ struct Pair {
 struct PairFp8 : Pair {
     float2 qn;
 };
+
+// A pair whose probabilities go into the value product in two parts.
+struct PairSplit : Pair {};
+template <class P>
+constexpr bool kSplit = false;
+template <>
+constexpr bool kSplit<PairSplit> = true;
 
 // 8-bit rows g, g + 8 (bytes 16 t .. 16 t + 15) and their scales.
 struct TileFp8 {
@@ -242,11 +254,17 @@ __device__ __forceinline__ void raise(Pair& U, float2 x) {
     }
 }
 
+// What rounding x and y to the two bf16 of w left.
+__device__ __forceinline__ uint32_t rest_of(uint32_t w, float x, float y) {
+    const float2 h = unpack_bf16(w);
+    return pack_bf16(x - h.x, y - h.y);
+}
+
 // Window tile.  mask: bit 2k (2k + 1) says that row g (g + 8) is in the window
 // of this thread's query of pair k.  kFirst: nothing is accumulated yet.
 template <bool kFirst, class X, class P>
 __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2, P (&U)[2]) {
-    uint32_t b[2][2];
+    uint32_t b[2][2], rest[2][2];
     const float2 sl = f2(sl2, sl2);
     float c[2][4];
     scores<2>(x, U, c);
@@ -293,8 +311,14 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
             b[k][0] = movm_t(pack_f16(lo[k].x * x.vs[0], lo[k].y * x.vs[0]));
             b[k][1] = movm_t(pack_f16(hi[k].x * x.vs[1], hi[k].y * x.vs[1]));
         } else {
-            b[k][0] = movm_t(pack_bf16(lo[k].x, lo[k].y));
-            b[k][1] = movm_t(pack_bf16(hi[k].x, hi[k].y));
+            b[k][0] = pack_bf16(lo[k].x, lo[k].y);
+            b[k][1] = pack_bf16(hi[k].x, hi[k].y);
+            if constexpr (kSplit<P>) {
+                rest[k][0] = movm_t(rest_of(b[k][0], lo[k].x, lo[k].y));
+                rest[k][1] = movm_t(rest_of(b[k][1], hi[k].x, hi[k].y));
+            }
+            b[k][0] = movm_t(b[k][0]);
+            b[k][1] = movm_t(b[k][1]);
         }
     }
 #pragma unroll
@@ -307,6 +331,7 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
                 value_mma_z<X>(U[k].o[j], a, b[k]);
             else
                 value_mma<X>(U[k].o[j], a, b[k]);
+            if constexpr (kSplit<P>) value_mma<X>(U[k].o[j], a, rest[k]);
         }
     }
 }
@@ -343,7 +368,7 @@ __device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, 
 #pragma unroll
         for (int k = 0; k < kN; ++k) raise(U[k], top[k]);
     }
-    uint32_t b[kN][2];
+    uint32_t b[kN][2], rest[kN][2];
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
         s[k] = __fadd2_rn(s[k], U[k].nm);
@@ -355,8 +380,14 @@ __device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, 
             b[k][1] = movm_t(pack_f16(p.x * nv, p.y * nv));
         } else {
             const float2 far_p = __fmul2_rn(p, tt), near_p = __fmul2_rn(p, uu);
-            b[k][0] = movm_t(pack_bf16(far_p.x, far_p.y));
-            b[k][1] = movm_t(pack_bf16(near_p.x, near_p.y));
+            b[k][0] = pack_bf16(far_p.x, far_p.y);
+            b[k][1] = pack_bf16(near_p.x, near_p.y);
+            if constexpr (kSplit<P>) {
+                rest[k][0] = movm_t(rest_of(b[k][0], far_p.x, far_p.y));
+                rest[k][1] = movm_t(rest_of(b[k][1], near_p.x, near_p.y));
+            }
+            b[k][0] = movm_t(b[k][0]);
+            b[k][1] = movm_t(b[k][1]);
         }
     }
 #pragma unroll
@@ -366,6 +397,7 @@ __device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, 
             uint32_t a[4];
             value_frag(x[k], j, a);
             value_mma<X>(U[k].o[j], a, b[k]);
+            if constexpr (kSplit<P>) value_mma<X>(U[k].o[j], a, rest[k]);
         }
 }
 
@@ -385,6 +417,11 @@ struct RowsBf16 {
             U.qf[j][1] = w[4 + j];
         }
     }
+};
+
+// bf16 copies of 8-bit rows.
+struct RowsCopied : RowsBf16 {
+    using Pair = PairSplit;
 };
 
 struct RowsFp8 {

@@ -49,7 +49,6 @@ namespace sfa {
 namespace {
 
 using namespace mma;
-using paged::Pair;
 using paged::PagedFwd;
 using paged::Quad;
 using paged::kLn2;
@@ -109,8 +108,8 @@ struct SharedTile {
     uint32_t k, v;
 };
 
-template <int kN>
-__device__ __forceinline__ void scores(const SharedTile& x, const Pair* U, float (*c)[4]) {
+template <int kN, class P>
+__device__ __forceinline__ void scores(const SharedTile& x, const P* U, float (*c)[4]) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         uint32_t a0, a1, a2, a3;
@@ -360,7 +359,9 @@ __device__ void produce(const TileParams& T, Shared& S) {
 
 // ------------------------------------------------------------ the consumers
 
-// One tile after another, until the end; false when a wait gave up.
+// One tile after another, until the end; false when a wait gave up.  F: the rows'
+// format, as quad_pass has it.
+template <class F>
 __device__ bool consume(const TileParams& T, Shared& S) {
     const PagedFwd& P = T.f;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, tig = lane & 3;
@@ -417,7 +418,7 @@ __device__ bool consume(const TileParams& T, Shared& S) {
         const int cnt = x.cnt, i0 = x.i0, groups = x.groups;
         if (cnt == 0) return true;
         const bool mine = u0 < cnt;
-        Pair U[2];
+        typename F::Pair U[2];
         if (mine) {
             const uint32_t st = stage0 + (uint32_t)st_index * kStageB;
 #pragma unroll
@@ -546,7 +547,7 @@ __device__ bool consume(const TileParams& T, Shared& S) {
 
 // Token row t alone, as the quad that it stands in computes it.  (One for each
 // kernel: ptxas ends in a fault over a function that both call.)
-template <bool kAsk>
+template <bool kAsk, class F>
 __device__ __noinline__ void redo_query(const PagedFwd& P, const Shared& S, int t, int g) {
     const paged::Where x = paged::sequence_of(P.c, t);
     if (x.s >= P.c.S) return;
@@ -561,10 +562,10 @@ __device__ __noinline__ void redo_query(const PagedFwd& P, const Shared& S, int 
     Q.rn = S.rn;
     Q.rc = S.rc;
     Q.rt = S.rt;
-    paged::quad_pass<true, true>(P, Q, only);
+    paged::quad_pass<true, true, false, F>(P, Q, only);
 }
 
-template <bool kAsk>
+template <bool kAsk, class F>
 __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant__ TileParams T) {
     extern __shared__ unsigned char raw[];
     Shared& S = *reinterpret_cast<Shared*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kWarps) {
         produce<kAsk>(T, S);
-    } else if (!consume(T, S) && (tid & 31) == 0) {
+    } else if (!consume<F>(T, S) && (tid & 31) == 0) {
         S.abort_flag = 1;
         if (T.f.c.status) atomicOr(T.f.c.status, SFA_DEVSTAT_WAIT_TIMEOUT);
     }
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
     const int redos = S.redos;
     if (redos == 0 || S.abort_flag) return;
     if (redos <= kRedo) {
-        for (int i = warp; i < redos; i += kWarps + 1) redo_query<kAsk>(T.f, S, S.redo[i] / kHkv, S.redo[i] % kHkv);
+        for (int i = warp; i < redos; i += kWarps + 1) redo_query<kAsk, F>(T.f, S, S.redo[i] / kHkv, S.redo[i] % kHkv);
         return;
     }
     // more than the list holds: only a block that goes through many slots, both heads of each
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
         const int slot = kAsk ? v : blockIdx.x + v * gridDim.x;
         if (slot >= (kAsk ? S.ntaken : T.slots)) break;
         const Work x = work_of(T.f, S.rc, kAsk ? S.taken[slot] : slot);
-        for (int i = warp; i < x.cnt * kHkv; i += kWarps + 1) redo_query<kAsk>(T.f, S, x.t0 + i / kHkv, i % kHkv);
+        for (int i = warp; i < x.cnt * kHkv; i += kWarps + 1) redo_query<kAsk, F>(T.f, S, x.t0 + i / kHkv, i % kHkv);
     }
 }
 
@@ -652,12 +653,11 @@ bool encode_queries(CUtensorMap* m, const void* base, int N, long long stride) {
 // average length, and so leaves out the 30 ragged chunks for the 32 equal ones.
 constexpr int kAskRounds = 6, kAskEach = 800;
 
-}  // namespace
-
-cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
+template <class F>
+cudaError_t launch_tiles(const PagedFwd& P, cudaStream_t s) {
     const long long slots = (long long)P.c.N / kTQ + P.c.S, most = kSms * 2;
     const bool ask = slots > most && slots <= kAskRounds * most && P.c.N <= kAskEach * (long long)P.c.S;
-    void (*const kernel)(TileParams) = ask ? tile_kernel<true> : tile_kernel<false>;
+    void (*const kernel)(TileParams) = ask ? tile_kernel<true, F> : tile_kernel<false, F>;
     static CtxSetting done[2][64];  // per kernel and device: dynamic shared memory allowed
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -680,6 +680,12 @@ cudaError_t launch_paged_tiles(const PagedFwd& P, cudaStream_t s) {
             return cudaErrorInvalidValue;
     if (!encode_queries(&T.q, P.q, P.c.N, P.qs)) return cudaErrorInvalidValue;
     return launch_early(kernel, (unsigned)(T.split ? slots * kHkv : ask || slots < most ? slots : most), kThreads, smem, s, T);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tiles(const PagedFwd& P, bool copied, cudaStream_t s) {
+    return copied ? launch_tiles<paged::RowsCopied>(P, s) : launch_tiles<paged::RowsBf16>(P, s);
 }
 
 }  // namespace sfa

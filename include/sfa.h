@@ -593,9 +593,10 @@ SFA_API size_t sfa_paged_forward_fp8_workspace_size(const sfa_params *p, const s
  * scale that is no power of two is rounded to bf16 where rows are copied).
  *   workspace: device, 256-byte aligned, contents ignored on entry and clobbered;
  *     two calls that may overlap need one each; NULL where none is needed.
- * One launch, or two with a workspace.  Errors of the results as sfa_paged_forward's;
- * without a workspace probabilities on the tensor cores are rounded to fp16 instead
- * of bf16, and the error of O is 1.7e-3 of its norm there too. */
+ * One launch, or two with a workspace.  Errors of the results as sfa_paged_forward's
+ * in fp32 arithmetic: on the tensor cores probabilities are rounded to fp16, or with a
+ * workspace to two parts of a bf16 each (2^-16), and the error of O is 1.7e-3 of its
+ * norm there too. */
 SFA_API sfa_status sfa_paged_forward_fp8(const sfa_params *p, const sfa_paged_fp8 *c, const void *Q, long long q_stride,
                                          void *O, float *lse, void *workspace, size_t workspace_bytes,
                                          unsigned int *status, cudaStream_t stream);
