@@ -89,7 +89,10 @@ bool expands(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, Expand* E) {
     E->shift = c.shift < 6 ? c.shift : 6;
     E->back = a.W;
     for (int i = 0; i < a.nr; ++i) E->back = E->back > a.r[i].n + 1 ? E->back : a.r[i].n + 1;
-    E->extra = (E->back >> E->shift) + 3;
+    // A sequence of n new tokens is back + n + rows - 1 rows long in the copy at most: (back >>
+    // shift) + 3 pages more than n >> shift.  One more, since the capacity below, which moves by
+    // whole pages, can lie up to rows - 1 before the end of the table.
+    E->extra = (E->back >> E->shift) + 4;
     // (at most three rows expanded for one of the chunks, and a table of no more words)
     const long long own = c.N >> E->shift, reach = (long long)c.S * E->extra, cols = own + E->extra;
     if (reach > 2 * own || cols * c.S > 4LL * c.N) return false;
