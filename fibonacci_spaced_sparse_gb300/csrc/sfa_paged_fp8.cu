@@ -13,6 +13,8 @@
 // farthest row of a key list.  Its pages start at place (cu[s] >> shift) + s * extra of
 // the workspace, and at position 64 h of the sequence: all positions move by that, which
 // changes no mask, since every entry of a query exists from position back on.
+// Every word of the copies' table and lengths is written, page or no page, so what
+// the workspace held before reaches nothing, whatever the offsets are.
 #include "sfa_paged_quad.cuh"
 #include "sfa_paged_rows.cuh"
 
@@ -29,6 +31,7 @@ struct Expand {
     int back, extra;      // rows, pages before a sequence's chunk
     int shift, cols;      // log2 of the rows of such a page; entries of a sequence
     int cap, places;      // positions [0, cap) exist, as it sees them; pages
+    int chunks, heads;    // 32 entries each of a sequence; thread blocks of entries, in front
 };
 
 constexpr int kExpandRows = 16, kRowChunks = kHkv * kD / 16;  // of a thread block; 16-byte pieces of a row
@@ -47,25 +50,58 @@ __device__ __forceinline__ void expand16(uint4 u, float s, uint4* to) {
     to[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// A sequence's pages: the first that is read, the one that becomes number 0 and the last.
+// The first two are the same, but where the sequence's length passes the capacity, which
+// then has to stay where it is.
+struct Span {
+    int first, zero, last;
+};
+__device__ __forceinline__ Span span_of(const Expand& E, const paged::Where& x) {
+    const long long before = x.len - max((long long)x.end - x.start, 0LL);  // (offsets may be anything)
+    const int first = (int)(max(before - E.back, 0LL) >> E.shift);
+    return Span{first, x.len > E.c.cap ? (E.c.cap - E.cap) >> E.shift : first, (min(x.len, E.c.cap) - 1) >> E.shift};
+}
+__device__ __forceinline__ int place_of(const Expand& E, int start, int s) { return (start >> E.shift) + s * E.extra; }
+
+// 32 entries of a sequence in the copies' table, a warp: the places of its pages, where
+// the thread blocks of those places find the sequence as well (they do unless offsets
+// make no sense; a search that ends at it for two places does so for all between them).
+__device__ __forceinline__ void write_entries(const Expand& E, int s, int chunk) {
+    const int lane = threadIdx.x & 31, at = 32 * chunk + lane;
+    const paged::Where x = paged::look(E.c, s);
+    const Span y = span_of(E, x);
+    if (chunk == 0 && lane == 0) E.lens[s] = x.len - (y.zero << E.shift);
+    const int index = at + y.zero, place = place_of(E, x.start, s) + index - y.first;
+    const bool in = at < E.cols && index >= y.first && index <= y.last && place >= 0 && place < E.places;
+    const unsigned who = __ballot_sync(kFull, in);
+    bool found = who != 0u;
+    if (found) {
+        auto finder = [&](int of) {
+            return paged::last_at_most(E.c, __shfl_sync(kFull, place, of), [&](int start, int i) { return place_of(E, start, i); }).s;
+        };
+        found = finder(__ffs(who) - 1) == s && finder(31 - __clz(who)) == s;
+    }
+    if (at < E.cols)
+        E.table[(size_t)s * E.cols + at] = in && found && paged::page_row(E.c, s, index << E.shift) >= 0 ? place : -1;
+}
+
 // A thread block for 16 rows of a page.
 __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ Expand E) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if ((int)blockIdx.x < E.heads) {
+        const int w = blockIdx.x * (kExpandThreads / 32) + (threadIdx.x >> 5), s = w / E.chunks;
+        if (s < E.c.S) write_entries(E, s, w % E.chunks);
+        return;
+    }
     const PagedArgs& c = E.c;
-    const int parts = E.shift - 4, place = blockIdx.x >> parts, part = blockIdx.x & ((1 << parts) - 1);
+    const int parts = E.shift - 4, block = blockIdx.x - E.heads, place = block >> parts, part = block & ((1 << parts) - 1);
     static_assert(kExpandRows == 1 << 4, "parts of a page");
-    const paged::Where x = paged::last_at_most(c, place, [&](int start, int s) { return (start >> E.shift) + s * E.extra; });
-    const int n = place - (x.start >> E.shift) - x.s * E.extra;  // of the sequence's pages
-    if (n < 0) return;
-    // first page that is read, and the one that becomes number 0: the same, but where the
-    // sequence's length passes the capacity, which then has to stay where it is
-    const int before = x.len - max(x.end - x.start, 0), first = max(before - E.back, 0) >> E.shift;
-    const int h = x.len > c.cap ? (c.cap - E.cap) >> E.shift : first;
-    if (n == 0 && part == 0 && threadIdx.x == 0) E.lens[x.s] = x.len - (h << E.shift);
-    const int index = first + n, at = index - h;
-    if (index > (min(x.len, c.cap) - 1) >> E.shift || at < 0 || at >= E.cols) return;
+    const paged::Where x = paged::last_at_most(c, place, [&](int start, int s) { return place_of(E, start, s); });
+    const Span y = span_of(E, x);
+    const int n = place - place_of(E, x.start, x.s), index = y.first + n;  // of the sequence's pages
+    if (n < 0 || index > y.last) return;
     const int row0 = paged::page_row(c, x.s, index << E.shift);
-    if (part == 0 && threadIdx.x == 0) E.table[(size_t)x.s * E.cols + at] = row0 < 0 ? -1 : place;
     if (row0 < 0) return;
     const bool value = threadIdx.x >= kExpandThreads / 2;
     const int piece = threadIdx.x % (kExpandThreads / 2), row = part * kExpandRows + piece / kRowChunks;
@@ -98,6 +134,8 @@ bool expands(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, Expand* E) {
     if (reach > 2 * own || cols * c.S > 4LL * c.N) return false;
     E->cols = (int)cols;
     E->places = (int)(own + reach);
+    E->chunks = (E->cols + 31) / 32;
+    E->heads = (int)(((long long)E->chunks * c.S + kExpandThreads / 32 - 1) / (kExpandThreads / 32));
     const int rows = 1 << E->shift;
     const long long room = cols * rows - (rows - c.cap % rows) % rows;
     E->cap = c.cap <= room ? c.cap : (int)room;
@@ -123,7 +161,7 @@ cudaError_t launch_paged_fwd_fp8(const LayerArgs& a, const PagedArgs& c, sfa_dty
         E.v = reinterpret_cast<uint4*>(at + page_bytes(E));
         E.table = reinterpret_cast<int*>(at + 2 * page_bytes(E));
         E.lens = E.table + (size_t)E.cols * c.S;
-        const cudaError_t e = launch_early(expand_kernel, (unsigned)E.places << (E.shift - 4), kExpandThreads, 0, s, E);
+        const cudaError_t e = launch_early(expand_kernel, (unsigned)E.heads + ((unsigned)E.places << (E.shift - 4)), kExpandThreads, 0, s, E);
         if (e != cudaSuccess) return e;
         PagedFwd B = P;
         B.c.k = E.k;
