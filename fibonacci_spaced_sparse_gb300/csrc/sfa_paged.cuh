@@ -138,10 +138,17 @@ struct PagedFwd {
     float* lse;
 };
 
+// What goes with bf16 copies of 8-bit rows (sfa_paged_fp8.cu).
+constexpr int kMark = 1 << 30;
+struct Copies {
+    const int* marked;      // the block table, with kMark more for a page with factors other than 1
+    const int* first_rows;  // [S]: the row of the copies that is position 0; the others follow it
+};
+
 }  // namespace paged
 
-// The kernel for long chunks (sfa_paged_tile.cu).  copied: the pages are copies of 8-bit
-// rows.
-cudaError_t launch_paged_tiles(const paged::PagedFwd& P, bool copied, cudaStream_t s);
+// The kernel for long chunks (sfa_paged_tile.cu).  copies: of pages that are bf16 copies
+// of 8-bit rows.
+cudaError_t launch_paged_tiles(const paged::PagedFwd& P, const paged::Copies* copies, cudaStream_t s);
 
 }  // namespace sfa

@@ -6,13 +6,16 @@
 // tiles, and turning it from 8 bits costs more than the bytes it saves once it is in
 // L2.  So the rows that the chunks can reach are turned into bf16 once, into pages of
 // their own in the caller's workspace, and the kernel for long chunks of bf16 pages
-// runs on those (32 x 1024 tokens: 39.8 us, and 53.1 for quads on 8-bit rows), with its
+// runs on those (32 x 1024 tokens: 40.4 us, and 53.1 for quads on 8-bit rows), with its
 // probabilities in two parts (PairSplit; rounded to bf16 once, as over bf16 pages, 37.1 us and
 // an error of O of 2.0e-3 of its norm instead of 1.7e-3).
 // Sequence s reaches from position c - back on, c its rows before the step and back the
 // farthest row of a key list.  Its pages start at place (cu[s] >> shift) + s * extra of
 // the workspace, and at position 64 h of the sequence: all positions move by that, which
 // changes no mask, since every entry of a query exists from position back on.
+// A code times a power of two is exact in bf16, so a copy holds the codes times the power
+// of two in their scale, and the factor that is left stands in the workspace beside it, for
+// 8 rows of a head each, with a mark for every page that has one that is not 1.
 // Every word of the copies' table and lengths is written, page or no page, so what
 // the workspace held before reaches nothing, whatever the offsets are.
 #include "sfa_paged_quad.cuh"
@@ -27,7 +30,9 @@ namespace {
 struct Expand {
     PagedArgs c;
     uint4 *k, *v;         // bf16 rows, [places][rows of a page][Hkv][D]
+    float* factors;       // [places][rows of a page / 8][2][Hkv]: what the copies leave of their scales
     int *table, *lens;    // [S][cols], [S]: the pages and lengths that the attention sees
+    int *marked, *first_rows;  // [S][cols], [S]: as Copies has them
     int back, extra;      // rows, pages before a sequence's chunk
     int shift, cols;      // log2 of the rows of such a page; entries of a sequence
     int cap, places;      // positions [0, cap) exist, as it sees them; pages
@@ -36,6 +41,26 @@ struct Expand {
 
 constexpr int kExpandRows = 16, kRowChunks = kHkv * kD / 16;  // of a thread block; 16-byte pieces of a row
 constexpr int kExpandThreads = 2 * kExpandRows * kRowChunks;  // a piece of keys or values each
+
+// A scale as a power of two and a factor in [1, 2).  Zero, what is not finite, and what
+// leaves no room for the codes (outside of what a scale may be) stay whole.
+__device__ __forceinline__ float2 parts_of(float s) {
+    const unsigned u = __float_as_uint(s), e = u >> 23 & 255u;
+    if (e < 127u - 100u || e > 127u + 100u) return make_float2(s, 1.f);
+    return make_float2(__uint_as_float(u & 0xff800000u), __uint_as_float(u & 0x7fffffu | 0x3f800000u));
+}
+constexpr int kFactorShift = 3;  // log2 of the rows that share a factor (a block of rows has 8 at least)
+
+// Whether a page's first `rows` rows, from row row0 of the cache on, have factors other than 1.
+__device__ __forceinline__ bool has_factors(const PagedArgs& c, int row0, int rows) {
+    bool y = false;
+    for (int j = 0; j < rows; j += 1 << c.block_shift) {
+        const float4 s = fresh(reinterpret_cast<const float4*>(paged::row_scales(c, row0 + j)));
+        static_assert(kHkv == 2, "a block's scales are one load");
+        y = y || parts_of(s.x).y != 1.f || parts_of(s.y).y != 1.f || parts_of(s.z).y != 1.f || parts_of(s.w).y != 1.f;
+    }
+    return y;
+}
 
 // 16 codes and their scale as bf16.
 __device__ __forceinline__ void expand16(uint4 u, float s, uint4* to) {
@@ -70,8 +95,11 @@ __device__ __forceinline__ void write_entries(const Expand& E, int s, int chunk)
     const int lane = threadIdx.x & 31, at = 32 * chunk + lane;
     const paged::Where x = paged::look(E.c, s);
     const Span y = span_of(E, x);
-    if (chunk == 0 && lane == 0) E.lens[s] = x.len - (y.zero << E.shift);
     const int index = at + y.zero, place = place_of(E, x.start, s) + index - y.first;
+    if (at == 0) {
+        E.lens[s] = x.len - (y.zero << E.shift);
+        E.first_rows[s] = place << E.shift;
+    }
     const bool in = at < E.cols && index >= y.first && index <= y.last && place >= 0 && place < E.places;
     const unsigned who = __ballot_sync(kFull, in);
     bool found = who != 0u;
@@ -81,8 +109,19 @@ __device__ __forceinline__ void write_entries(const Expand& E, int s, int chunk)
         };
         found = finder(__ffs(who) - 1) == s && finder(31 - __clz(who)) == s;
     }
-    if (at < E.cols)
-        E.table[(size_t)s * E.cols + at] = in && found && paged::page_row(E.c, s, index << E.shift) >= 0 ? place : -1;
+    int entry = -1, marked = -1;
+    if (in && found) {
+        const int pos = index << E.shift, row0 = paged::page_row(E.c, s, pos);
+        const int rows = min(min(x.len, E.c.cap) - pos, 1 << E.shift);  // that exist
+        if (row0 >= 0) {
+            entry = place;
+            marked = has_factors(E.c, row0, rows) ? place + paged::kMark : place;
+        }
+    }
+    if (at < E.cols) {
+        E.table[(size_t)s * E.cols + at] = entry;
+        E.marked[(size_t)s * E.cols + at] = marked;
+    }
 }
 
 // A thread block for 16 rows of a page.
@@ -108,14 +147,17 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     const size_t i = (size_t)row0 * kRowChunks + part * kExpandRows * kRowChunks + piece;
     const uint4 u = fresh(static_cast<const uint4*>(value ? c.v : c.k) + i);
     const int head = piece % kRowChunks / (kRowChunks / kHkv);
-    const float s = fresh(paged::row_scales(c, row0 + row) + (value ? kHkv : 0) + head);
-    expand16(u, s, (value ? E.v : E.k) + 2 * ((((size_t)place << E.shift) + part * kExpandRows) * kRowChunks + piece));
+    const float2 s = parts_of(fresh(paged::row_scales(c, row0 + row) + (value ? kHkv : 0) + head));
+    // a lane of each head and 8 rows writes their factor
+    if ((row & ((1 << kFactorShift) - 1)) == 0 && piece % (kRowChunks / kHkv) == 0)
+        E.factors[(((size_t)place << E.shift) + row >> kFactorShift) * (2 * kHkv) + (value ? kHkv : 0) + head] = s.y;
+    expand16(u, s.x, (value ? E.v : E.k) + 2 * ((((size_t)place << E.shift) + part * kExpandRows) * kRowChunks + piece));
 }
 
 constexpr int kQuadsFrom = 305, kTilesEach = 32;  // as in sfa_paged_fwd.cu
 // Tokens from which rows are expanded (us, quads and expanded: one chunk of 8000 16.4 and
-// 15.4, of 12000 24.1 and 24.1; 16 chunks of 512 behind 2000 rows 17.0 and 16.1; 32 x 1024
-// in pages of 64 rows 52.9 and 39.8, of 16 53.7 and 42.6).
+// 16.0, of 12000 24.1 and 24.3; 16 chunks of 512 behind 2000 rows 17.0 and 16.2; 32 x 1024
+// in pages of 64 rows 52.9 and 40.4, of 16 53.7 and 44.2).
 constexpr int kExpandFrom = 7000;
 
 // Whether a call's rows are expanded, and how.
@@ -143,12 +185,13 @@ bool expands(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, Expand* E) {
 }
 
 size_t page_bytes(const Expand& E) { return ((size_t)E.places << E.shift) * kHkv * kD * 2; }
+size_t factor_bytes(const Expand& E) { return ((size_t)E.places << E.shift >> kFactorShift) * 2 * kHkv * sizeof(float); }
 
 }  // namespace
 
 size_t paged_fwd_fp8_workspace(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt) {
     Expand E;
-    return expands(a, c, dt, &E) ? 2 * page_bytes(E) + ((size_t)E.cols + 1) * c.S * sizeof(int) : 0;
+    return expands(a, c, dt, &E) ? 2 * page_bytes(E) + factor_bytes(E) + 2 * ((size_t)E.cols + 1) * c.S * sizeof(int) : 0;
 }
 
 cudaError_t launch_paged_fwd_fp8(const LayerArgs& a, const PagedArgs& c, sfa_dtype dt, const void* q, long long qs,
@@ -159,8 +202,12 @@ cudaError_t launch_paged_fwd_fp8(const LayerArgs& a, const PagedArgs& c, sfa_dty
         char* at = static_cast<char*>(ws);
         E.k = reinterpret_cast<uint4*>(at);
         E.v = reinterpret_cast<uint4*>(at + page_bytes(E));
-        E.table = reinterpret_cast<int*>(at + 2 * page_bytes(E));
-        E.lens = E.table + (size_t)E.cols * c.S;
+        E.factors = reinterpret_cast<float*>(at + 2 * page_bytes(E));
+        E.table = reinterpret_cast<int*>(at + 2 * page_bytes(E) + factor_bytes(E));
+        E.marked = E.table + (size_t)E.cols * c.S;
+        E.lens = E.marked + (size_t)E.cols * c.S;
+        E.first_rows = E.lens + c.S;
+        const Copies copies = {E.marked, E.first_rows};
         const cudaError_t e = launch_early(expand_kernel, (unsigned)E.heads + ((unsigned)E.places << (E.shift - 4)), kExpandThreads, 0, s, E);
         if (e != cudaSuccess) return e;
         PagedFwd B = P;
@@ -172,7 +219,9 @@ cudaError_t launch_paged_fwd_fp8(const LayerArgs& a, const PagedArgs& c, sfa_dty
         B.c.num_pages = E.places;
         B.c.shift = E.shift;
         B.c.cap = E.cap;
-        return launch_paged_tiles(B, true, s);
+        B.c.scales = E.factors;
+        B.c.block_shift = kFactorShift;
+        return launch_paged_tiles(B, &copies, s);
     }
     if (dt == SFA_BF16 && a.W <= 28 && c.N >= kQuadsFrom && c.N >= 2 * (long long)c.S) return launch_quads<RowsFp8>(P, s);
     return dt == SFA_BF16 ? launch_rows<__nv_bfloat16, __nv_fp8_e4m3>(P, s) : launch_rows<float, __nv_fp8_e4m3>(P, s);

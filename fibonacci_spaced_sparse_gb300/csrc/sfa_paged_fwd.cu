@@ -40,7 +40,7 @@ cudaError_t launch_paged_fwd(const LayerArgs& a, const PagedArgs& c, sfa_dtype d
     const bool wide = ((reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) & 31u) == 0;
     if (dt == SFA_BF16 && a.W <= 28 && wide) {
         if (quad_slots(c) > quad_wave(3) && c.N >= kTilesEach * (long long)c.S && c.shift >= 4)
-            return launch_paged_tiles(P, false, s);
+            return launch_paged_tiles(P, nullptr, s);
         if (c.N >= kQuadsFrom && c.N >= 2 * (long long)c.S) return launch_quads<RowsBf16>(P, s);
     }
     return dt == SFA_BF16 ? launch_rows<__nv_bfloat16, __nv_bfloat16>(P, s) : launch_rows<float, float>(P, s);

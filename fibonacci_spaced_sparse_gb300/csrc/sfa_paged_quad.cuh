@@ -63,8 +63,13 @@
 // Long chunks of 8-bit rows are attended over exact bf16 copies (PairSplit).  There
 // a probability is the sum of two bf16 parts, p = hi + lo with lo = p - hi rounded,
 // which leaves 2^-16 of it, and the value product is made of both: 4 more MMAs a
-// tile and pair, so that a long chunk is no less exact than a short one.
+// tile and pair, so that a long chunk is no less exact than a short one.  A copy holds
+// the codes times the power of two in their scale; the factor that is left, in [1, 2),
+// joins a key's score and a value's probability in fp32, as the scales of 8-bit rows do
+// (kFactors).  With a factor of 1 that changes no bit, so tiles without another skip it.
 #pragma once
+
+#include <type_traits>
 
 #include "sfa_fp8.cuh"
 #include "sfa_mma.cuh"
@@ -113,6 +118,24 @@ template <class X>
 constexpr bool kScaled = false;
 template <>
 constexpr bool kScaled<TileFp8> = true;
+
+// The factors of copied rows g, g + 8, and whether a tile has some.
+struct Factors {
+    float ks[2], vs[2];
+};
+struct TileCopied : Tile, Factors {};
+template <class X>
+constexpr bool kFactors = std::is_base_of_v<Factors, X>;
+
+// The factors of a copied row: row_scales holds them.  Where no row was copied it holds
+// anything, which here becomes a factor like the others.
+__device__ __forceinline__ float factor_of(float x) { return __uint_as_float(__float_as_uint(x) & 0x7fffffu | 0x3f800000u); }
+__device__ __forceinline__ void put_factors(const PagedArgs& c, int g, int row, int h, Factors& x) {
+    const float4 s = fresh(reinterpret_cast<const float4*>(row_scales(c, row)));
+    static_assert(kHkv == 2, "a block's factors are one load");
+    x.ks[h] = factor_of(g ? s.y : s.x);
+    x.vs[h] = factor_of(g ? s.w : s.z);
+}
 
 __device__ __forceinline__ float2 f2(float x, float y) { return make_float2(x, y); }
 
@@ -276,6 +299,10 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
             const float s0 = sl2 * x.ks[0], s1 = sl2 * x.ks[1];
             lo[k] = __fmul2_rn(f2(c[k][0], c[k][1]), __fmul2_rn(U[k].qn, f2(s0, s0)));
             hi[k] = __fmul2_rn(f2(c[k][2], c[k][3]), __fmul2_rn(U[k].qn, f2(s1, s1)));
+        } else if constexpr (kFactors<X>) {
+            const float s0 = sl2 * x.ks[0], s1 = sl2 * x.ks[1];
+            lo[k] = __fmul2_rn(f2(c[k][0], c[k][1]), f2(s0, s0));
+            hi[k] = __fmul2_rn(f2(c[k][2], c[k][3]), f2(s1, s1));
         } else {
             lo[k] = __fmul2_rn(f2(c[k][0], c[k][1]), sl);
             hi[k] = __fmul2_rn(f2(c[k][2], c[k][3]), sl);
@@ -311,6 +338,10 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
             b[k][0] = movm_t(pack_f16(lo[k].x * x.vs[0], lo[k].y * x.vs[0]));
             b[k][1] = movm_t(pack_f16(hi[k].x * x.vs[1], hi[k].y * x.vs[1]));
         } else {
+            if constexpr (kFactors<X>) {
+                lo[k] = __fmul2_rn(lo[k], f2(x.vs[0], x.vs[0]));
+                hi[k] = __fmul2_rn(hi[k], f2(x.vs[1], x.vs[1]));
+            }
             b[k][0] = pack_bf16(lo[k].x, lo[k].y);
             b[k][1] = pack_bf16(hi[k].x, hi[k].y);
             if constexpr (kSplit<P>) {
@@ -353,6 +384,9 @@ __device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, 
             const float fs = t * sl2 * x[k].ks[0], ns = u * sl2 * x[k].ks[1];
             s[k] = __fmul2_rn(__ffma2_rn(f2(fs, fs), f2(c[k][0][0], c[k][0][1]), __fmul2_rn(f2(ns, ns), f2(c[k][0][2], c[k][0][3]))),
                               U[k].qn);
+        } else if constexpr (kFactors<X>) {
+            const float fs = t * sl2 * x[k].ks[0], ns = u * sl2 * x[k].ks[1];
+            s[k] = __ffma2_rn(f2(fs, fs), f2(c[k][0][0], c[k][0][1]), __fmul2_rn(f2(ns, ns), f2(c[k][0][2], c[k][0][3])));
         } else {
             s[k] = __ffma2_rn(ts, f2(c[k][0][0], c[k][0][1]), __fmul2_rn(us, f2(c[k][0][2], c[k][0][3])));
         }
@@ -379,7 +413,15 @@ __device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, 
             b[k][0] = movm_t(pack_f16(p.x * fv, p.y * fv));
             b[k][1] = movm_t(pack_f16(p.x * nv, p.y * nv));
         } else {
-            const float2 far_p = __fmul2_rn(p, tt), near_p = __fmul2_rn(p, uu);
+            float2 far_p, near_p;
+            if constexpr (kFactors<X>) {
+                const float fv = t * x[k].vs[0], nv = u * x[k].vs[1];
+                far_p = __fmul2_rn(p, f2(fv, fv));
+                near_p = __fmul2_rn(p, f2(nv, nv));
+            } else {
+                far_p = __fmul2_rn(p, tt);
+                near_p = __fmul2_rn(p, uu);
+            }
             b[k][0] = pack_bf16(far_p.x, far_p.y);
             b[k][1] = pack_bf16(near_p.x, near_p.y);
             if constexpr (kSplit<P>) {
@@ -406,6 +448,7 @@ struct RowsBf16 {
     using Tile = paged::Tile;
     using Pair = paged::Pair;
     static constexpr int kBytes = 2;  // of an element
+    static constexpr bool kCopied = false;
     template <bool kAlone, bool kNatural>
     static __device__ __forceinline__ void load(const PagedArgs&, int, const char* k, const char* v, int row, int base, Tile& x) {
         load_tile<kAlone, kNatural>(k, v, row, base, x);
@@ -421,7 +464,19 @@ struct RowsBf16 {
 
 // bf16 copies of 8-bit rows.
 struct RowsCopied : RowsBf16 {
+    using Tile = TileCopied;
     using Pair = PairSplit;
+    static constexpr bool kCopied = true;
+    template <bool kAlone, bool kNatural>
+    static __device__ __forceinline__ void load(const PagedArgs& c, int g, const char* k, const char* v, int row, int base,
+                                                Tile& x) {
+        load_tile<kAlone, kNatural>(k, v, row, base, x);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = __shfl_sync(kFull, row, base + 8 * h + ((threadIdx.x & 31) >> 2));
+            put_factors(c, g, max(r, 0), h, x);
+        }
+    }
 };
 
 struct RowsFp8 {

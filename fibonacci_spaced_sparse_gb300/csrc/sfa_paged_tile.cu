@@ -35,6 +35,11 @@
 // latency: three stages a block, two blocks a SM), and the arithmetic, 1000
 // instructions a quad at 16 warps a SM, hides that only in part.
 //
+// Over bf16 copies of 8-bit rows (RowsCopied) the warps load the factors of a tile's rows
+// themselves, from the first tile on that has a page with some: a factor of 1 changes no
+// bit, so the tiles after it may take that form as well (32 x 1024 tokens, copies and all:
+// without factors 40.4 us, with 47.1; with both forms in one loop 42.4 and 47.5).
+//
 // Queries whose result is not finite are kept in a list and redone from global
 // memory when the block's tiles are done (redo_query, with the score sums in
 // this kernel's order of the dimensions; a call inside the loop costs it 1 KB
@@ -65,6 +70,7 @@ constexpr int kQueries = 2 * kWinValues;        // its queries: (query, head) ro
 constexpr int kQueryB = kTQ * kG * kRowB;
 constexpr int kStageB = 2 * kValues;
 constexpr int kStages = 3;
+constexpr int kHole = 1, kFactor = 2;           // what is odd about a page: it is bad, has factors
 constexpr int kTaken = 256; // slots that a block takes at most
 constexpr int kRedo = 256;  // queries of a block that are not finite (at least a slot's); past that, all of its queries are redone
 static_assert(kRedo >= kTQ, "a block with one tile never runs over");
@@ -75,6 +81,7 @@ static_assert((kPitch / kRowB) % 8 == 6, "rungs start in different swizzle phase
 struct Work {
     int s, g, t0, cnt, i0, last;
     int used, groups;  // rungs that its last query uses, in groups of four
+    bool factors;      // copied rows: it reads pages with factors
 };
 
 struct Shared {
@@ -100,6 +107,7 @@ struct TileParams {
     PagedFwd f;
     int slots;
     bool split;  // a block takes one head only
+    paged::Copies copies;
 };
 
 // K and V rows of a tile in shared memory: the row addresses that this lane
@@ -107,6 +115,8 @@ struct TileParams {
 struct SharedTile {
     uint32_t k, v;
 };
+// The same with the factors of rows g and g + 8.
+struct FactorTile : SharedTile, paged::Factors {};
 
 template <int kN, class P>
 __device__ __forceinline__ void scores(const SharedTile& x, const P* U, float (*c)[4]) {
@@ -192,32 +202,37 @@ __device__ __forceinline__ Work work_of(const PagedFwd& P, const int* rc, int sl
 // nothing) from row `row` of the pages on, to row `at` of the block.
 struct Part {
     int row, rows, at;
-    bool bad;  // its page is
+    int odd;  // what is odd about its page
 };
 
 // Part `n` of the block whose row 0 is position `base` and of which the
 // positions lo .. hi are read: what lies in the n-th page from lo's.
-__device__ __forceinline__ Part part_of(const PagedFwd& P, int s, int base, int lo, int hi, int n) {
+template <class F>
+__device__ __forceinline__ Part part_of(const TileParams& T, int s, int base, int lo, int hi, int n) {
+    const PagedFwd& P = T.f;
     const int sh = P.c.shift, index = (max(lo, 0) >> sh) + n;
     const int from = max(lo, index << sh), to = min(hi, ((index + 1) << sh) - 1);
-    if (from > to) return Part{0, 0, 0, false};
-    const int page = fresh(P.c.table + (size_t)s * P.c.max_pages + index);
-    if ((unsigned)page >= (unsigned)P.c.num_pages) return Part{0, 0, 0, true};
-    return Part{(page << sh) + (from & ((1 << sh) - 1)), to - from + 1, from - base, false};
+    if (from > to) return Part{0, 0, 0, 0};
+    int page = fresh((F::kCopied ? T.copies.marked : P.c.table) + (size_t)s * P.c.max_pages + index);
+    const bool mark = F::kCopied && page >= paged::kMark;
+    if (mark) page -= paged::kMark;
+    if ((unsigned)page >= (unsigned)P.c.num_pages) return Part{0, 0, 0, kHole};
+    return Part{(page << sh) + (from & ((1 << sh) - 1)), to - from + 1, from - base, mark ? kFactor : 0};
 }
 
 // Rung r's block: row j is position i0 - n - 1 + j, the far row of query j and
 // the near row of query j - 1.
-__device__ __forceinline__ Part rung_part(const PagedFwd& P, const Shared& S, const Work& x, int r, int n) {
+template <class F>
+__device__ __forceinline__ Part rung_part(const TileParams& T, const Shared& S, const Work& x, int r, int n) {
     const int c = r < SFA_MAX_RUNGS ? S.rc[r] : 0x7fffffff;
-    if (c > x.last) return Part{0, 0, 0, false};
+    if (c > x.last) return Part{0, 0, 0, 0};
     const int back = S.rn[r] + 1, from = max(c, x.i0) + (S.rt[r] > 0.f ? 0 : 1);
-    return part_of(P, x.s, x.i0 - back, from - back, x.last + 1 - back, n);
+    return part_of<F>(T, x.s, x.i0 - back, from - back, x.last + 1 - back, n);
 }
 
 // kAsk: the block's slots after its own are those of blocks that have not started,
 // one asked for at a time; else those a grid apart.
-template <bool kAsk>
+template <bool kAsk, class F>
 __device__ void produce(const TileParams& T, Shared& S) {
     const PagedFwd& P = T.f;
     const int lane = threadIdx.x & 31, W = P.a.W;
@@ -237,7 +252,7 @@ __device__ void produce(const TileParams& T, Shared& S) {
         const int high = min(max(y.rows, 1), kHeights);  // 56 rows at most: two boxes, the second may overlap
         const int boxes = y.rows == 0 ? 0 : y.rows > high ? 2 : 1;
         const uint32_t bytes = __reduce_add_sync(kFull, (unsigned)(boxes * high * kRowB)) + more;
-        const bool bad = __any_sync(kFull, y.bad);
+        const bool bad = __any_sync(kFull, y.odd & kHole);
         if (lane == 0) {
             S.holes[n % kStages] = bad;
             if (bad) paged::report(P.c.status);
@@ -305,15 +320,22 @@ __device__ void produce(const TileParams& T, Shared& S) {
             }
             ++taken;
         }
-        y.win = part_of(P, y.x.s, y.x.i0 - W, max(0, y.x.i0 - W), y.x.last, lane >> 1);
+        y.win = part_of<F>(T, y.x.s, y.x.i0 - W, max(0, y.x.i0 - W), y.x.last, lane >> 1);
 #pragma unroll
-        for (int k = 0; k < kEarly; ++k) y.run[k] = rung_part(P, S, y.x, 4 * k + p, part);
+        for (int k = 0; k < kEarly; ++k) y.run[k] = rung_part<F>(T, S, y.x, 4 * k + p, part);
         if (lane < y.x.cnt && (y.x.i0 + lane < 0 || y.x.i0 + lane >= P.c.cap)) paged::report(P.c.status);
         return y;
     };
     const uint32_t block = tensor * kValues + p * kPitch;
     Plan y = plan(), z;
     while (ok && y.x.cnt > 0) {
+        if (F::kCopied) {
+            int odd = y.win.odd;
+#pragma unroll
+            for (int k = 0; k < kEarly; ++k) odd |= y.run[k].odd;
+            for (int k = kEarly; k < y.x.groups; ++k) odd |= rung_part<F>(T, S, y.x, 4 * k + p, part).odd;
+            y.x.factors = __any_sync(kFull, odd & kFactor);
+        }
         // the heads' tiles read the same rows
         for (int g = g0; ok && g < g1; ++g) {
             Work x = y.x;
@@ -333,7 +355,7 @@ __device__ void produce(const TileParams& T, Shared& S) {
             for (int k = 1; k < kEarly; ++k)
                 if (ok && k < x.groups && wait()) fetch(y.run[k], x, block, 0u);
             for (int k = kEarly; k < x.groups; ++k) {
-                const Part more = rung_part(P, S, x, 4 * k + p, part);
+                const Part more = rung_part<F>(T, S, x, 4 * k + p, part);
                 if (ok && wait()) fetch(more, x, block, 0u);
             }
         }
@@ -359,10 +381,17 @@ __device__ void produce(const TileParams& T, Shared& S) {
 
 // ------------------------------------------------------------ the consumers
 
-// One tile after another, until the end; false when a wait gave up.  F: the rows'
-// format, as quad_pass has it.
-template <class F>
-__device__ bool consume(const TileParams& T, Shared& S) {
+enum class After { kEnd, kGaveUp, kFactors };  // the last tile; a wait gave up; the next tile has factors
+
+// How far a warp is: its stage and the parity of its barriers, its tile.
+struct Place {
+    int stage, phase, tile;
+};
+
+// One tile after another, from place `at_tile` on.  F: the rows' format, as quad_pass has it.
+// kFactors: with the factors of their rows, else up to a tile that has some.
+template <class F, bool kFactors>
+__device__ __forceinline__ After consume(const TileParams& T, Shared& S, Place& at_tile) {
     const PagedFwd& P = T.f;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, tig = lane & 3;
     const int W = P.a.W, u0 = 4 * warp;
@@ -395,6 +424,22 @@ __device__ bool consume(const TileParams& T, Shared& S) {
         }
         return m;
     };
+    // rows g and g + 8 are positions pos and pos + step of the sequence (of a masked row any
+    // copied row's factors will do)
+    auto with_factors = [&](const SharedTile& t, const Work& x, int pos, int step) {
+        if constexpr (kFactors) {
+            FactorTile y;
+            y.k = t.k;
+            y.v = t.v;
+            const int row0 = fresh(T.copies.first_rows + x.s), most = (P.c.num_pages << P.c.shift) - 1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                paged::put_factors(P.c, x.g, min(max(row0 + min(max(pos + h * step, 0), x.last), 0), most), h, y);
+            return y;
+        } else {
+            return t;
+        }
+    };
     const SharedTile whole[2] = {rung_at(0, 4), rung_at(1, 4)}, first = window_at(0);
     const unsigned mask0 = window_mask(0, [](int) { return true; });
     // outputs: stmatrix rows of this lane in the staging buffer, its 16-byte piece
@@ -403,7 +448,7 @@ __device__ bool consume(const TileParams& T, Shared& S) {
     const int mi = lane >> 3;
     const uint32_t put = swizzled(out + (lane & 7) * kRowB, mi);           // chunks mi and 4 + mi
     const uint32_t get = swizzled(out + (lane >> 3) * kRowB, lane & 7);    // row lane / 8; row + 4: chunk ^ 4
-    int st_index = 0, phase = 0, tile = 0;
+    int st_index = at_tile.stage, phase = at_tile.phase, tile = at_tile.tile;
     auto done_with_stage = [&]() {
         __syncwarp();
         mbar_arrive_if(empty0 + 8 * st_index, lane == 0);
@@ -413,10 +458,14 @@ __device__ bool consume(const TileParams& T, Shared& S) {
         }
     };
     for (;; ++tile) {
-        if (!warp_wait(full0 + 8 * st_index, phase, &S.abort_flag)) return false;
+        if (!warp_wait(full0 + 8 * st_index, phase, &S.abort_flag)) return After::kGaveUp;
         const Work& x = S.work[tile & 3];
         const int cnt = x.cnt, i0 = x.i0, groups = x.groups;
-        if (cnt == 0) return true;
+        if (cnt == 0) return After::kEnd;
+        if (F::kCopied && !kFactors && x.factors) {
+            at_tile = Place{st_index, phase, tile};
+            return After::kFactors;
+        }
         const bool mine = u0 < cnt;
         typename F::Pair U[2];
         if (mine) {
@@ -436,16 +485,17 @@ __device__ bool consume(const TileParams& T, Shared& S) {
                 return !holes || (pos <= x.last && paged::page_row(P.c, x.s, pos) >= 0);
             };
             const unsigned m = lo > 0 || holes ? window_mask(0, there) : mask0;
-            paged::window_tile<true>(SharedTile{first.k + st, first.v + st}, m, sl2, U);
+            paged::window_tile<true>(with_factors(SharedTile{first.k + st, first.v + st}, x, i0 + u0 - W + g8, 8), m, sl2, U);
             if (W > 12) {
                 const SharedTile X = window_at(1);
-                paged::window_tile<false>(SharedTile{X.k + st, X.v + st}, window_mask(1, there), sl2, U);
+                paged::window_tile<false>(with_factors(SharedTile{X.k + st, X.v + st}, x, i0 + u0 - W + 16 + g8, 8),
+                                          window_mask(1, there), sl2, U);
             }
         }
         done_with_stage();
         const int my_i = (g8 >> 2) == (tig >> 1) ? i0 + u0 + (tig >> 1) : -(1 << 30);
         for (int k = 0; k < groups; ++k) {
-            if (!warp_wait(full0 + 8 * st_index, phase, &S.abort_flag)) return false;
+            if (!warp_wait(full0 + 8 * st_index, phase, &S.abort_flag)) return After::kGaveUp;
             if (mine) {
                 const uint32_t st = stage0 + (uint32_t)st_index * kStageB;
                 const int r = 4 * k + (g8 & 3), np = x.used - 4 * k;
@@ -470,7 +520,13 @@ __device__ bool consume(const TileParams& T, Shared& S) {
                     X[i].k += st;
                     X[i].v += st;
                 }
-                paged::rung_tiles<2>(X, ok, frac, sl2, U);
+                if constexpr (kFactors) {
+                    const int far = i0 + u0 + (g8 >> 2) - S.rn[r] - 1;
+                    const FactorTile Y[2] = {with_factors(X[0], x, far, 1), with_factors(X[1], x, far + 2, 1)};
+                    paged::rung_tiles<2>(Y, ok, frac, sl2, U);
+                } else {
+                    paged::rung_tiles<2>(X, ok, frac, sl2, U);
+                }
             }
             done_with_stage();
         }
@@ -594,10 +650,17 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kWarps) {
-        produce<kAsk>(T, S);
-    } else if (!consume<F>(T, S) && (tid & 31) == 0) {
-        S.abort_flag = 1;
-        if (T.f.c.status) atomicOr(T.f.c.status, SFA_DEVSTAT_WAIT_TIMEOUT);
+        produce<kAsk, F>(T, S);
+    } else {
+        Place place{};
+        After how = consume<F, false>(T, S, place);
+        if constexpr (F::kCopied) {
+            if (how == After::kFactors) how = consume<F, true>(T, S, place);
+        }
+        if (how == After::kGaveUp && (tid & 31) == 0) {
+            S.abort_flag = 1;
+            if (T.f.c.status) atomicOr(T.f.c.status, SFA_DEVSTAT_WAIT_TIMEOUT);
+        }
     }
     __syncthreads();
     const int redos = S.redos;
@@ -654,7 +717,7 @@ bool encode_queries(CUtensorMap* m, const void* base, int N, long long stride) {
 constexpr int kAskRounds = 6, kAskEach = 800;
 
 template <class F>
-cudaError_t launch_tiles(const PagedFwd& P, cudaStream_t s) {
+cudaError_t launch_tiles(const PagedFwd& P, const paged::Copies* copies, cudaStream_t s) {
     const long long slots = (long long)P.c.N / kTQ + P.c.S, most = kSms * 2;
     const bool ask = slots > most && slots <= kAskRounds * most && P.c.N <= kAskEach * (long long)P.c.S;
     void (*const kernel)(TileParams) = ask ? tile_kernel<true, F> : tile_kernel<false, F>;
@@ -672,6 +735,7 @@ cudaError_t launch_tiles(const PagedFwd& P, cudaStream_t s) {
     TileParams T;
     std::memset(&T, 0, sizeof(T));
     T.f = P;
+    if (copies) T.copies = *copies;
     T.slots = (int)slots;
     T.split = slots * kHkv <= most;  // fewer slots than blocks: the heads side by side
     const long long rows = (long long)P.c.num_pages << P.c.shift;
@@ -684,8 +748,8 @@ cudaError_t launch_tiles(const PagedFwd& P, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_paged_tiles(const PagedFwd& P, bool copied, cudaStream_t s) {
-    return copied ? launch_tiles<paged::RowsCopied>(P, s) : launch_tiles<paged::RowsBf16>(P, s);
+cudaError_t launch_paged_tiles(const PagedFwd& P, const paged::Copies* copies, cudaStream_t s) {
+    return copies ? launch_tiles<paged::RowsCopied>(P, copies, s) : launch_tiles<paged::RowsBf16>(P, nullptr, s);
 }
 
 }  // namespace sfa

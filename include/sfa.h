@@ -585,12 +585,12 @@ SFA_API sfa_status sfa_paged_append_fp8(const sfa_params *p, const sfa_paged_fp8
                                         void *Qhat, unsigned int *status, cudaStream_t stream);
 
 /* Bytes of device workspace sfa_paged_forward_fp8 needs (0: none).  The long chunks
- * of a bf16 call are attended over bf16 copies of the rows that they reach. */
+ * of a bf16 call are attended over exact bf16 copies of the rows that they reach. */
 SFA_API size_t sfa_paged_forward_fp8_workspace_size(const sfa_params *p, const sfa_paged_fp8 *c);
 
 /* sfa_paged_forward over 8-bit pages; p->dtype is the type of Q and O.  Scales need
- * not be powers of two here: anything from 2^-100 to 2^100 will do (a value times a
- * scale that is no power of two is rounded to bf16 where rows are copied).
+ * not be powers of two here: anything from 2^-100 to 2^100 will do, with the same errors
+ * (long chunks take some 15 % more time over other scales).
  *   workspace: device, 256-byte aligned, contents ignored on entry and clobbered;
  *     two calls that may overlap need one each; NULL where none is needed.
  * One launch, or two with a workspace.  Errors of the results as sfa_paged_forward's
