@@ -55,9 +55,14 @@
 // its scores take back with the keys' scales, so its halves hold what its bf16
 // values did (but for elements below 2^-14 of the largest, to 2^-25 of it).  A
 // value row's scale joins its probability: p s is rounded to a half, 2^-11 where
-// bf16 pages lose 2^-8, and the running maximum runs over score + log2(s) so that
-// p s stays in range (what is 2^-14 of the largest or less is off by up to 2^-25
-// of it).  The sum for lse takes p alone.  (Turning 8 bits into bf16 instead takes
+// bf16 pages lose 2^-8, and the running maximum runs over score + log2(s), so that
+// the largest p s lies between 2^kUp and 2^(kUp + kLazy), in a half's range.  The sum
+// for lse takes p alone.  What is below 2^-14 is off by up to 2^-25, 2^-32 of the
+// largest p s.  A scale says nothing about the row's codes, though: where the row of the
+// largest p s holds zeros, the output can be made of such remainders.  With n rows each
+// element of O is off by 448 n 2^-25 at most, so a query of which a head's largest
+// element is less than 2^13 times that is redone in fp32 arithmetic (one_exact), and the
+// others' loss is below 2^-10 of O's norm, whatever the scales are.  (Turning 8 bits into bf16 instead takes
 // nine operations for four values where halves take two.)
 //
 // Long chunks of 8-bit rows are attended over exact bf16 copies (PairSplit).  There
@@ -74,6 +79,7 @@
 #include "sfa_fp8.cuh"
 #include "sfa_mma.cuh"
 #include "sfa_paged.cuh"
+#include "sfa_paged_rows.cuh"
 
 namespace sfa {
 namespace paged {
@@ -118,6 +124,14 @@ template <class X>
 constexpr bool kScaled = false;
 template <>
 constexpr bool kScaled<TileFp8> = true;
+
+// Where the running maximum puts the largest probability (times its scale), log2.
+template <class X>
+constexpr float kUp = kScaled<X> ? 7.f : 0.f;
+// log2 of a value row's scale, of a zero one (all of its codes are zero) that of the
+// smallest there is.
+constexpr float kLeastScale = 7.8886090522101181e-31f;  // 2^-100
+__device__ __forceinline__ float log2_scale(float s) { return fast_log2(fmaxf(s, kLeastScale)); }
 
 // The factors of copied rows g, g + 8, and whether a tile has some.
 struct Factors {
@@ -260,12 +274,17 @@ __device__ __forceinline__ float2 column_max(float2 x) {
 
 // Raise the running maximum of each column whose largest x passes the margin,
 // and rescale it.
+template <class X>
 __device__ __forceinline__ void raise(Pair& U, float2 x) {
     x = column_max(x);
-    const float n0 = x.x > U.th.x ? -x.x : U.nm.x, n1 = x.y > U.th.y ? -x.y : U.nm.y;
+    if constexpr (kScaled<X>) {
+        x.x = x.x > U.th.x ? x.x - kUp<X> : -U.nm.x;
+        x.y = x.y > U.th.y ? x.y - kUp<X> : -U.nm.y;
+    }
+    const float n0 = kScaled<X> || x.x > U.th.x ? -x.x : U.nm.x, n1 = kScaled<X> || x.y > U.th.y ? -x.y : U.nm.y;
     const float2 f = f2(fast_exp2(n0 - U.nm.x), fast_exp2(n1 - U.nm.y));
     U.nm = f2(n0, n1);
-    U.th = f2(kLazy - n0, kLazy - n1);
+    U.th = f2(kLazy + kUp<X> - n0, kLazy + kUp<X> - n1);
     U.l = __fmul2_rn(U.l, f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -310,22 +329,22 @@ __device__ __forceinline__ void window_tile(const X& x, unsigned mask, float sl2
         if (!(mask >> (2 * k) & 1u)) lo[k] = f2(-INFINITY, -INFINITY);
         if (!(mask >> (2 * k + 1) & 1u)) hi[k] = f2(-INFINITY, -INFINITY);
         if constexpr (kScaled<X>) {
-            const float l0 = fast_log2(x.vs[0]), l1 = fast_log2(x.vs[1]);
+            const float l0 = log2_scale(x.vs[0]), l1 = log2_scale(x.vs[1]);
             top[k] = f2(fmaxf(lo[k].x + l0, hi[k].x + l1), fmaxf(lo[k].y + l0, hi[k].y + l1));
         } else {
             top[k] = f2(fmaxf(lo[k].x, hi[k].x), fmaxf(lo[k].y, hi[k].y));
         }
         if (kFirst) {
             const float2 m = column_max(top[k]);
-            U[k].nm = f2(-fmaxf(m.x, kFloor), -fmaxf(m.y, kFloor));
-            U[k].th = f2(kLazy - U[k].nm.x, kLazy - U[k].nm.y);
+            U[k].nm = f2(kUp<X> - fmaxf(m.x, kFloor), kUp<X> - fmaxf(m.y, kFloor));
+            U[k].th = f2(kLazy + kUp<X> - U[k].nm.x, kLazy + kUp<X> - U[k].nm.y);
         } else {
             over = over || top[k].x > U[k].th.x || top[k].y > U[k].th.y;
         }
     }
     if (!kFirst && __any_sync(kFull, over)) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) raise(U[k], top[k]);
+        for (int k = 0; k < 2; ++k) raise<X>(U[k], top[k]);
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -393,14 +412,14 @@ __device__ __forceinline__ void rung_tiles(const X* x, const bool* ok, float t, 
         if (!ok[k]) s[k] = f2(-INFINITY, -INFINITY);
         top[k] = s[k];
         if constexpr (kScaled<X>) {
-            const float l = fast_log2(fmaxf(t * x[k].vs[0], u * x[k].vs[1]));
+            const float l = log2_scale(fmaxf(t * x[k].vs[0], u * x[k].vs[1]));
             top[k] = f2(s[k].x + l, s[k].y + l);
         }
         over = over || top[k].x > U[k].th.x || top[k].y > U[k].th.y;
     }
     if (__any_sync(kFull, over)) {
 #pragma unroll
-        for (int k = 0; k < kN; ++k) raise(U[k], top[k]);
+        for (int k = 0; k < kN; ++k) raise<X>(U[k], top[k]);
     }
     uint32_t b[kN][2], rest[kN][2];
 #pragma unroll
@@ -547,7 +566,8 @@ struct Entry {
 };
 
 // All queries of the quad, or the query `only` alone; returns the queries
-// whose results are not finite (they are not written).  kNatural: the sums of
+// whose results are not finite (bits 0 .. 3; not when alone) or too small for halves (bits
+// 4 .. 7); they are not written.  kNatural: the sums of
 // the scores run over the dimensions in their natural order.  kDeep: four tiles
 // of rows in registers instead of two.
 template <bool kAlone, bool kNatural, bool kDeep = false, class F = RowsBf16>
@@ -675,7 +695,8 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
         }
     }
     if (__any_sync(kFull, bad) && lane == 0) paged::report(P.c.status);
-    unsigned redo = 0;
+    unsigned redo = 0, small = 0;
+    const float least = (float)(W + 1 + 2 * P.a.nr) * (448.f * 8192.f / 33554432.f);  // 2^13 448 n 2^-25
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         float2 l = U[k].l;
@@ -695,7 +716,23 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
             const unsigned who = __ballot_sync(kFull, odd.x + odd.y != 0.f && qq < Q.cnt && in);
             redo |= ((who & 0x33333333u ? 1u : 0u) | (who & 0xccccccccu ? 2u : 0u)) << (2 * k);
         }
-        const bool stores = qq < Q.cnt && (kAlone ? qq == only : !(redo >> qq & 1u));
+        if constexpr (kScaled<Tile>) {
+            float2 top = f2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                top = f2(fmaxf(top.x, fmaxf(fabsf(U[k].o[j][0]), fabsf(U[k].o[j][2]))),
+                         fmaxf(top.y, fmaxf(fabsf(U[k].o[j][1]), fabsf(U[k].o[j][3]))));
+            // columns 2 tig and 2 tig + 1 are the eight lanes' with this tig
+            unsigned a = __ballot_sync(kFull, top.x >= least), b = __ballot_sync(kFull, top.y >= least);
+            a |= a >> 16, b |= b >> 16;
+            a |= a >> 8, b |= b >> 8;
+            a |= a >> 4, b |= b >> 4;
+            a = ~(a & b);
+            const unsigned who = __ballot_sync(kFull, (a >> tig & 1u) && qq < Q.cnt && in && (!kAlone || qq == only));
+            small |= ((who & 0x33333333u ? 1u : 0u) | (who & 0xccccccccu ? 2u : 0u)) << (2 * k);
+            small &= ~redo;
+        }
+        const bool stores = qq < Q.cnt && (kAlone ? qq == only : !(redo >> qq & 1u)) && !(small >> qq & 1u);
         const unsigned who_stores = __ballot_sync(kFull, stores);
         if (!stores) continue;
         // l >= 2^-8 (the entry at the maximum, at most the margin below it; with 8-bit rows that
@@ -730,7 +767,7 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
             *reinterpret_cast<float2*>(P.lse + at) = in ? f2(y0, y1) : f2(0.f, 0.f);
         }
     }
-    return redo;
+    return redo | small << 4;
 }
 
 // ----------------------------------------------------------------- the kernel
@@ -749,8 +786,20 @@ constexpr long long quad_wave(int blocks) { return kSms * (long long)blocks * kQ
 // A call of its own, so that the rare pass takes no registers of the common one
 // (and one for each kernel: they differ in their registers).
 template <class F, int kBlocks>
-__device__ __noinline__ void one_alone(const PagedFwd& P, const Quad& Q, int only) {
-    quad_pass<true, false, false, F>(P, Q, only);
+__device__ __noinline__ unsigned one_alone(const PagedFwd& P, const Quad& Q, int only) {
+    return quad_pass<true, false, false, F>(P, Q, only);
+}
+
+// The query `only` in fp32 arithmetic (sfa_paged_rows.cuh), by one warp.
+template <int kBlocks>
+__device__ __noinline__ void one_exact(const PagedFwd& P, const Quad& Q, int only) {
+    const int lane = threadIdx.x & 31, t = Q.t0 + only;
+    Chunk<__nv_bfloat16> raw[kG];
+#pragma unroll
+    for (int h = 0; h < kG; ++h)
+        load(static_cast<const __nv_bfloat16*>(P.q) + (size_t)t * P.qs + (Q.g * kG + h) * kD + 8 * (lane & 7), raw[h]);
+    const Partial y = query_part<__nv_bfloat16, __nv_fp8_e4m3, false>(P, Q.s, Q.i0 + only, Q.g, raw, 0, 4);
+    write_part<__nv_bfloat16>(P, t, Q.g, lane >> 3, lane & 7, y);
 }
 
 template <class F, int kBlocks>
@@ -785,8 +834,14 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kBlocks) quad_kernel(const __
     Q.rt = rt;
     if (__any_sync(kFull, lane < Q.cnt && (Q.i0 + lane < 0 || Q.i0 + lane >= P.c.cap)) && lane == 0)
         paged::report(P.c.status);
-    for (unsigned redo = quad_pass<false, false, kBlocks == 2, F>(P, Q, -1); redo; redo &= redo - 1)
-        one_alone<F, kBlocks>(P, Q, __ffs(redo) - 1);
+    unsigned redo = quad_pass<false, false, kBlocks == 2, F>(P, Q, -1);
+    if constexpr (kScaled<typename F::Tile>) {
+        unsigned small = redo >> 4;
+        for (redo &= 15u; redo; redo &= redo - 1) small |= one_alone<F, kBlocks>(P, Q, __ffs(redo) - 1) >> 4;
+        for (; small; small &= small - 1) one_exact<kBlocks>(P, Q, __ffs(small) - 1);
+    } else {
+        for (; redo; redo &= redo - 1) one_alone<F, kBlocks>(P, Q, __ffs(redo) - 1);
+    }
 }
 
 // Slots of four queries at most (quad_kernel has their places).
