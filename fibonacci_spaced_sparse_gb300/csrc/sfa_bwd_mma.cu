@@ -850,11 +850,8 @@ cudaError_t launch_bwd_mma(const LayerArgs& a, const void* q, const void* k, con
     const size_t smem = 1024 + kHeaderBytes + BwdParams::kQMaps * (size_t)kQTileBytes + (size_t)P.win_slot_bytes +
                         NGS * (size_t)kGroupSlotBytes + NCW * (size_t)kObufBytes + kDtBytes + 1024 + NCW * 8192;
     static CtxSetting configured_smem[64];
-    if (!ctx_setting_holds(configured_smem[dev & 63], smem)) {
-        e = cudaFuncSetAttribute(bwd_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        ctx_setting_done(configured_smem[dev & 63], smem);
-    }
+    e = allow_smem(configured_smem[dev & 63], bwd_mma_kernel, smem);
+    if (e != cudaSuccess) return e;
     // CTAs per SM for this shared-memory size (looked up once per device and
     // size, so that no runtime query runs while a stream is being captured)
     static int occ_per_sm[64];

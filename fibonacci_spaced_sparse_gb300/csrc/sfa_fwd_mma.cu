@@ -756,11 +756,9 @@ cudaError_t launch_fwd_attention(const LayerArgs& a, const void* q, const void* 
     const size_t smem = 1024 + kHeaderBytes + FwdParams::kQMaps * (size_t)kQTileBytes + (size_t)P.win_slot_bytes +
                         NGS * (size_t)kGroupSlotBytes + NCW * (size_t)kObufBytes;
     if (!ctx_setting_holds(configured_smem[kidx][dev & 63], smem)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e == cudaSuccess) e = allow_smem(configured_smem[kidx][dev & 63], kernel, smem);
         if (e != cudaSuccess) return e;
-        ctx_setting_done(configured_smem[kidx][dev & 63], smem);
     }
     // CTAs per SM for this shared-memory size (looked up once per device and
     // size, so that no runtime query runs while a stream is being captured)

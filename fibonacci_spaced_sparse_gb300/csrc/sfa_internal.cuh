@@ -3,8 +3,10 @@
 // the C ABI).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -52,8 +54,8 @@ unsigned long long context_key();
 
 // Host: set-up of one kernel attribute value done in one context, per device.
 struct CtxSetting {
-    unsigned long long key;  // context_key() when it was done (0: never)
-    size_t value;
+    std::atomic<unsigned long long> key;  // context_key() when it was done (0: never)
+    std::atomic<size_t> value;
 };
 
 // True when `s` records `value` or more, set in the context current now.
@@ -65,6 +67,20 @@ inline bool ctx_setting_holds(const CtxSetting& s, size_t value) {
 inline void ctx_setting_done(CtxSetting& s, size_t value) {
     s.value = value;
     s.key = context_key();
+}
+
+// Allows a kernel `bytes` of dynamic shared memory where they go by the call.  The limit never
+// falls: a thread that finds less than it needs looks again under the lock, so that one with a
+// smaller size does not take back what another has just set and is about to launch with.
+inline std::mutex smem_limits;
+template <typename... P>
+cudaError_t allow_smem(CtxSetting& s, void (*kernel)(P...), size_t bytes) {
+    if (ctx_setting_holds(s, bytes)) return cudaSuccess;
+    const std::lock_guard<std::mutex> lock(smem_limits);
+    if (ctx_setting_holds(s, bytes)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) ctx_setting_done(s, bytes);
+    return e;
 }
 
 // SFA_TEST_FAULT=launch in the environment: entry points fail with

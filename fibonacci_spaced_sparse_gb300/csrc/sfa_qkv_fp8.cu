@@ -320,11 +320,8 @@ cudaError_t launch(Params& P, const QkvFp8Args& a, int sms, int dev, cudaStream_
     P.tiles = (P.M + BM * S::kHalves - 1) / (BM * S::kHalves) * S::kTiles;
     const size_t smem = S::smem(P.nkb);
     static CtxSetting configured[64];
-    if (!ctx_setting_holds(configured[dev & 63], smem)) {
-        const cudaError_t e = cudaFuncSetAttribute(qkv_fp8_kernel<kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        ctx_setting_done(configured[dev & 63], smem);
-    }
+    const cudaError_t e = allow_smem(configured[dev & 63], qkv_fp8_kernel<kForm>, smem);
+    if (e != cudaSuccess) return e;
     // with W8 in place a CTA keeps its features: a grid of whole rows of tiles
     const int most = S::kHeld ? sms / S::kTiles * S::kTiles : sms;
     return launch_early(qkv_fp8_kernel<kForm>, (unsigned)(P.tiles < most ? P.tiles : most), S::kThreads, smem, s, P);
