@@ -115,7 +115,6 @@ __global__ void __launch_bounds__(Shape<kForm>::kThreads, 1) qkv_fp8_kernel(cons
     const uint32_t stores = stages + S::kStages * S::kStageBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 32) {
         prefetch_map(&P.xmap);
         prefetch_map(&P.wmap);
@@ -139,6 +138,9 @@ __global__ void __launch_bounds__(Shape<kForm>::kThreads, 1) qkv_fp8_kernel(cons
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
+    // Only now may the next launch start: one that allocated tensor memory first, and then
+    // waited for this grid, would leave this CTA without.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
         if (lane == 0) {
