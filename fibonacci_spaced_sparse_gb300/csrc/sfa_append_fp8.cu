@@ -14,10 +14,11 @@
 // launch.  Four lanes hold a head row (sfa_heads.cuh), eight rows a warp at a time,
 // sixteen in registers between the two passes, so a block of up to 64 rows is read
 // once (64 rows read twice by one warp: 15.0 us for 16 prompts of up to 2048 tokens).
-// Blocks of rows are found in one of two ways: warps for N / R + 2 S places, where sequence s starts at
-// place cu[s] / R + 2 s, which leaves room for all blocks that its tokens can
-// touch; or, where sequences bring about one token each, a warp for every token,
-// which has the token's block if the token is the first there.  Queries are rows
+// Blocks of rows are found in one of two ways: a thread block for each of N / R + 2 S places,
+// where sequence s starts at place cu[s] / R + 2 s, which leaves room for all blocks that its
+// tokens can touch (the others return after the lookup); or, where sequences bring about one
+// token each, a thread block for every token, which has the token's block of rows if the token
+// is the first there.  Queries are rows
 // as in sfa_append.cu, in thread blocks of their own in the same launch.
 //
 // Bound by memory when there are many tokens and by the latency of its lookups in
