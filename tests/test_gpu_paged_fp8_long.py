@@ -31,3 +31,19 @@ def test_probabilities_are_not_rounded_to_bf16(lens, page, block, W):
     # the norm of the error: that of rounding to bf16 alone, uniform in a half step, is 1.66e-3
     off = (o[:used].double().cpu() - ref[0]).norm() / ref[0].norm()
     assert float(off) < 1.75e-3
+
+
+@pytest.mark.parametrize("lens,page,W", [([(3803, 70), (0, 9), (3302, 0), (1, 1200), (133, 986)], 8, 12), ([(7001, 37), (160, 0)], 32, 29),
+                                         ([(40, 30)] * 180, 64, 12), ([(6992, 0)], 64, 12)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_calls_that_copy_nothing(lens, page, W, dtype):
+    """Pages of 8 rows, wide windows, chunks too short for what they reach and one token row too
+    few: each kernel against its own bound."""
+    cache = Cache8(lens, page, dtype, 8, seed=page + W)
+    assert dtype == "f32" or workspace(cache, W, **KW) == 0
+    o, lse = api.sfa_paged_forward_fp8(cache.q.cuda(), *cache.pages8(), *cache.meta(), W=W, **KW)
+    ref = forward64(cache, W=W, **KW)
+    bo, bl = fp32_bounds(ref, dtype)
+    used = ref[0].shape[0]
+    within(o[:used], ref[0], bo + (halves_bound(ref) if dtype == "bf16" and W <= 28 else 0), "o")
+    within(lse[:used], ref[1], bl, "lse")
