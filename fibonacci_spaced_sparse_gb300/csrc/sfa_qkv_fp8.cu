@@ -282,8 +282,9 @@ __global__ void __launch_bounds__(Shape<kForm>::kThreads, 1) qkv_fp8_kernel(cons
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const uint32_t* a = acc + 4 * i + 2 * r;
-                        float2 x = __fmul2_rn(make_float2(__uint_as_float(a[0]), __uint_as_float(a[1])), __fmul2_rn(wx, sx[r]));
-                        float2 y = __fmul2_rn(make_float2(__uint_as_float(a[16]), __uint_as_float(a[17])), __fmul2_rn(wy, sx[r]));
+                        // the sum first: the scales' product alone may be too small for a float, or too large
+                        float2 x = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(a[0]), __uint_as_float(a[1])), wx), sx[r]);
+                        float2 y = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(a[16]), __uint_as_float(a[17])), wy), sx[r]);
                         if (rot) {
                             const float2 u = x, c = cs[r][i], n = sn[r][i];
                             x = make_float2(fmaf(u.x, c.x, -(y.x * n.x)), fmaf(u.y, c.y, -(y.y * n.y)));
