@@ -6,7 +6,7 @@
 // tiles, and turning it from 8 bits costs more than the bytes it saves once it is in
 // L2.  So the rows that the chunks can reach are turned into bf16 once, into pages of
 // their own in the caller's workspace, and the kernel for long chunks of bf16 pages
-// runs on those (32 x 1024 tokens: 40.4 us, and 53.1 for quads on 8-bit rows), with its
+// runs on those (32 x 1024 tokens: 40.4 us, and 55.0 for quads on 8-bit rows), with its
 // probabilities in two parts (PairSplit; rounded to bf16 once, as over bf16 pages, 37.1 us and
 // an error of O of 2.0e-3 of its norm instead of 1.7e-3).
 // Sequence s reaches from position c - back on, c its rows before the step and back the
@@ -155,9 +155,9 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
 }
 
 constexpr int kQuadsFrom = 305, kTilesEach = 32;  // as in sfa_paged_fwd.cu
-// Tokens from which rows are expanded (us, quads and expanded: one chunk of 8000 16.4 and
-// 16.0, of 12000 24.1 and 24.3; 16 chunks of 512 behind 2000 rows 17.0 and 16.2; 32 x 1024
-// in pages of 64 rows 52.9 and 40.4, of 16 53.7 and 44.2).
+// Tokens from which rows are expanded (us, quads and expanded: one chunk of 8000 16.9 and
+// 15.7, of 12000 24.7 and 25.1; 16 chunks of 512 behind 2000 rows 17.2 and 16.6; 32 x 1024
+// in pages of 64 rows 55.0 and 40.4, of 16 55.7 and 44.1).
 constexpr int kExpandFrom = 7000;
 
 // Whether a call's rows are expanded, and how.

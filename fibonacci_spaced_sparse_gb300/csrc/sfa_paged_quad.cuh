@@ -778,8 +778,8 @@ __device__ __forceinline__ unsigned quad_pass(const PagedFwd& P, const Quad& Q, 
 // 3100 6.8 and 9.3, 512 chunks of 2 5.7 and 8.2, 1000 of 16 43 and 49).  A tile of
 // 8-bit rows has half the words, so that two fit 128 registers as well (4, 16
 // warps), which pays where 12 warps a SM do not hold all (us, 3 and 4: 64 chunks of
-// up to 100 tokens, one wave of 3, 8.2 and 9.9; 1000 of 4 12.7 and 11.2, 32 of
-// 1024 57.6 and 53.1).
+// up to 100 tokens, one wave of 3, 8.2 and 9.9; 1000 of 4 behind up to 1000 rows 14.4
+// and 14.6, 32 of 1024 58.8 and 55.0).
 constexpr int kQuadWarps = 4;
 constexpr long long quad_wave(int blocks) { return kSms * (long long)blocks * kQuadWarps / kHkv; }  // slots at once
 
