@@ -62,8 +62,8 @@
 // largest p s holds zeros, the output can be made of such remainders.  With n rows each
 // element of O is off by 448 n 2^-25 at most, so a query of which a head's largest
 // element is less than 2^13 times that is redone in fp32 arithmetic (one_exact), and the
-// others' loss is below 2^-10 of O's norm, whatever the scales are.  (Turning 8 bits into bf16 instead takes
-// nine operations for four values where halves take two.)
+// others' loss is below 2^-10 of O's norm, whatever the scales are.  (Turning 8 bits into
+// bf16 instead takes nine operations for four values where halves take two.)
 //
 // Long chunks of 8-bit rows are attended over exact bf16 copies (PairSplit).  There
 // a probability is the sum of two bf16 parts, p = hi + lo with lo = p - hi rounded,

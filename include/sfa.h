@@ -591,8 +591,8 @@ SFA_API size_t sfa_paged_forward_fp8_workspace_size(const sfa_params *p, const s
 /* sfa_paged_forward over 8-bit pages; p->dtype is the type of Q and O.  Scales need
  * not be powers of two here: anything from 2^-100 to 2^100 will do, and 0, with the same
  * errors, however much the scales of a query's rows differ.  (Long chunks take some 15 % more
- * time over scales that are no powers of two; a query whose output is 2^-15 or less of what a
- * code of 1 in its heaviest row would make is attended a second time, in fp32 arithmetic.)
+ * time over scales that are no powers of two; a query whose output is below some 2^-5 of what
+ * a code of 1 in its heaviest row would make can be attended a second time, in fp32 arithmetic.)
  *   workspace: device, 256-byte aligned, contents ignored on entry and clobbered;
  *     two calls that may overlap need one each; NULL where none is needed.
  * One launch, or two with a workspace.  Errors of the results as sfa_paged_forward's
